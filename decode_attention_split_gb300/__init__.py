@@ -8,25 +8,32 @@ missing.
 """
 from .api import (  # noqa: F401
     DEV_APPEND_OVERFLOW,
+    DEV_BAD_POSITION,
     DEV_BAD_TOKEN,
     DEV_NEGATIVE_SEQLEN,
     DEV_SEQLEN_CLAMPED,
     DEV_VERIFY_SHORT,
     DEV_WAIT_TIMEOUT,
     DEV_WORKSPACE_DIRTY,
+    make_f8_cache,
     make_workspace,
     td_decode_attn,
+    td_decode_attn_f8,
     td_decode_attn_q8,
     td_decode_workspace_bytes,
     td_kv_append,
+    td_kv_append_f8,
     td_kv_append_q8,
+    td_kv_read_f8,
     td_lse_merge,
     td_prefill_attn,
     td_rope_append_attn,
     td_rope_kv_append,
+    td_rope_kv_append_f8,
     td_quantize_q8,
     td_spec_accept,
     td_split_plan,
     td_verify_attn,
+    td_verify_attn_f8,
     td_verify_attn_q8,
 )

@@ -22,6 +22,11 @@ SYMBOLS = (
     "td_kv_append_q8",
     "td_decode_attn_q8",
     "td_verify_attn_q8",
+    "td_kv_append_f8",
+    "td_rope_kv_append_f8",
+    "td_kv_read_f8",
+    "td_decode_attn_f8",
+    "td_verify_attn_f8",
     "td_prefill_attn",
     "td_kv_append",
     "td_decode_attn",
@@ -72,6 +77,17 @@ def _declare(lib):
     lib.td_decode_attn_q8.restype = i
     lib.td_verify_attn_q8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp, sz, vp, vp]
     lib.td_verify_attn_q8.restype = i
+    lib.td_kv_append_f8.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp, vp]
+    lib.td_kv_append_f8.restype = i
+    lib.td_rope_kv_append_f8.argtypes = [i, vp, vp, i, vp, vp, vp, vp, i, vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, i,
+                                         i, i, vp, vp]
+    lib.td_rope_kv_append_f8.restype = i
+    lib.td_kv_read_f8.argtypes = [i, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp, vp, vp]
+    lib.td_kv_read_f8.restype = i
+    lib.td_decode_attn_f8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp, sz, vp, vp]
+    lib.td_decode_attn_f8.restype = i
+    lib.td_verify_attn_f8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, vp, vp, vp, sz, vp, vp]
+    lib.td_verify_attn_f8.restype = i
     lib.td_prefill_attn.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, vp, vp, vp, vp]
     lib.td_prefill_attn.restype = i
     lib.td_spec_accept.restype = i

@@ -33,11 +33,11 @@ size_t elem_size(td_dtype d) { return d == TD_F32 ? 4 : 2; }
 td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens,
                   int B, int Hq, int Hkv, int T, int Smax, int D, float scale, int split, void *out, float *lse,
                   void *workspace, size_t workspace_bytes, uint32_t *dev_status, td::SplitPlan *plan,
-                  td::SplitParams *p, bool q8 = false) {
+                  td::SplitParams *p, td::KvFormat format = td::KvFormat::kRows) {
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr || out == nullptr)
     return TD_ERR_INVALID_ARG;
   if (!isfinite(scale)) return TD_ERR_INVALID_ARG;
-  const td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, q8);
+  const td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, format);
   if (st == TD_ERR_CUDA) return cuda_fail(cudaGetLastError());
   if (st != TD_OK) return st;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(seq_lens) ||
@@ -114,9 +114,11 @@ size_t td_decode_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_
     if (td::plan_split(dt, B, Hq, Hkv, q_len, Smax, D, split, &plan) != TD_OK) return 0;
     if (plan.bytes > bytes) bytes = plan.bytes;
   }
-  td::SplitPlan plan;  // the 8-bit cache kernel's layout (its grid may differ)
-  if (td::plan_split(TD_BF16, B, Hq, Hkv, q_len, Smax, D, split, &plan, true) == TD_OK && plan.bytes > bytes)
-    bytes = plan.bytes;
+  for (td::KvFormat f : {td::KvFormat::kQ8, td::KvFormat::kF8}) {  // the 8-bit kernels' layouts (their grids may differ)
+    td::SplitPlan plan;
+    if (td::plan_split(TD_BF16, B, Hq, Hkv, q_len, Smax, D, split, &plan, f) == TD_OK && plan.bytes > bytes)
+      bytes = plan.bytes;
+  }
   return bytes;
 }
 
@@ -301,7 +303,7 @@ td_status td_verify_attn_q8(const void *q, const int8_t *k_codes, const float *k
   td::SplitPlan plan;
   td::SplitParams p;
   const td_status st = prepare(TD_BF16, q, k_codes, v_codes, seq_lens, B, Hq, Hkv, T, Smax, D, scale, split, out,
-                               lse, workspace, workspace_bytes, dev_status, &plan, &p, true);
+                               lse, workspace, workspace_bytes, dev_status, &plan, &p, td::KvFormat::kQ8);
   if (st != TD_OK) return st;
   p.k_scales = k_scales;
   p.v_scales = v_scales;
@@ -315,6 +317,153 @@ td_status td_decode_attn_q8(const void *q, const int8_t *k_codes, const float *k
                             uint32_t *dev_status, void *stream) {
   return td_verify_attn_q8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, B, Hq, Hkv, 1, Smax, D, scale, split,
                            out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// log2 of a block size that the f8 caches take, or -1.
+int block_log2(int block) {
+  for (int l = 4; l <= 7; ++l)
+    if (block == 1 << l) return l;
+  return -1;
+}
+
+// Checks shared by the f8 appends, then the launch.
+td_status append_f8(td_dtype dtype, const void *q, void *q_out, int Hq, const void *k_new, const void *v_new,
+                    const float *cos_t, const float *sin_t, int table_rows, const int32_t *positions,
+                    const int32_t *axes, int n_axes, void *k_codes, float *k_scales, void *v_codes, float *v_scales,
+                    int32_t *seq_lens, int B, int Hkv, int T, int Smax, int D, int block, int advance,
+                    uint32_t *dev_status, void *stream) {
+  if (dtype != TD_F32 && dtype != TD_BF16) return TD_ERR_UNSUPPORTED;
+  if (k_new == nullptr || v_new == nullptr || k_codes == nullptr || k_scales == nullptr || v_codes == nullptr ||
+      v_scales == nullptr || seq_lens == nullptr)
+    return TD_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || T < 1 || Smax < 1 || (q != nullptr && Hq < 1)) return TD_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || block_log2(block) < 0 || B > 65535 || T > Smax || Smax > (1 << 30) ||
+      Hkv > 16384 || (q != nullptr && Hq > 16384))
+    return TD_ERR_UNSUPPORTED;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||
+      !aligned4(v_scales) || !aligned4(seq_lens) || (dev_status != nullptr && !aligned4(dev_status)))
+    return TD_ERR_UNSUPPORTED;
+  td::AppendF8 p = {};
+  p.q = q;
+  p.q_out = q_out;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.cos_t = cos_t;
+  p.sin_t = sin_t;
+  p.positions = positions;
+  p.axes = axes;
+  p.k_codes = static_cast<uint8_t *>(k_codes);
+  p.v_codes = static_cast<uint8_t *>(v_codes);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.seq_lens = seq_lens;
+  p.status = dev_status;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.Smax = Smax;
+  p.block_log2 = block_log2(block);
+  p.NB = (Smax + block - 1) / block;
+  p.A = n_axes;
+  p.table_rows = table_rows;
+  p.advance = advance != 0;
+  const cudaError_t e = td::launch_append_f8(elem_size(dtype), D, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+td_status td_kv_append_f8(td_dtype dtype, const void *k_new, const void *v_new, void *k_codes, float *k_scales,
+                          void *v_codes, float *v_scales, int32_t *seq_lens, int B, int Hkv, int T, int Smax, int D,
+                          int block, int advance, uint32_t *dev_status, void *stream) {
+  return append_f8(dtype, nullptr, nullptr, 0, k_new, v_new, nullptr, nullptr, 0, nullptr, nullptr, 0, k_codes,
+                   k_scales, v_codes, v_scales, seq_lens, B, Hkv, T, Smax, D, block, advance, dev_status, stream);
+}
+
+td_status td_rope_kv_append_f8(td_dtype dtype, const void *q, void *q_out, int Hq, const void *k_new,
+                               const void *v_new, const float *cos_t, const float *sin_t, int table_rows,
+                               const int32_t *positions, const int32_t *axes, int n_axes, void *k_codes,
+                               float *k_scales, void *v_codes, float *v_scales, int32_t *seq_lens, int B, int Hkv,
+                               int T, int Smax, int D, int block, int advance, uint32_t *dev_status, void *stream) {
+  if (cos_t == nullptr || sin_t == nullptr || (q == nullptr) != (q_out == nullptr)) return TD_ERR_INVALID_ARG;
+  if (positions == nullptr ? (axes != nullptr || table_rows < Smax) : (n_axes < 1 || table_rows < 1))
+    return TD_ERR_INVALID_ARG;
+  if (positions != nullptr && n_axes > 16) return TD_ERR_UNSUPPORTED;
+  if (!aligned16(cos_t) || !aligned16(sin_t) || (q != nullptr && (!aligned16(q) || !aligned16(q_out))) ||
+      (positions != nullptr && !aligned4(positions)) || (axes != nullptr && !aligned4(axes)))
+    return TD_ERR_UNSUPPORTED;
+  return append_f8(dtype, q, q_out, Hq, k_new, v_new, cos_t, sin_t, table_rows, positions, axes, n_axes, k_codes,
+                   k_scales, v_codes, v_scales, seq_lens, B, Hkv, T, Smax, D, block, advance, dev_status, stream);
+}
+
+td_status td_kv_read_f8(td_dtype dtype, const void *k_codes, const float *k_scales, const void *v_codes,
+                        const float *v_scales, const int32_t *seq_lens, const int32_t *start, int B, int Hkv, int N,
+                        int Smax, int D, int block, void *k_out, void *v_out, uint32_t *dev_status, void *stream) {
+  if (dtype != TD_F32 && dtype != TD_BF16) return TD_ERR_UNSUPPORTED;
+  if (k_codes == nullptr || k_scales == nullptr || v_codes == nullptr || v_scales == nullptr || seq_lens == nullptr ||
+      k_out == nullptr || v_out == nullptr)
+    return TD_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || N < 1 || Smax < 1) return TD_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || block_log2(block) < 0 || B > 65535 || Hkv > 16384 || Smax > (1 << 30) || N > (1 << 30))
+    return TD_ERR_UNSUPPORTED;
+  if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_out) || !aligned16(v_out) || !aligned4(k_scales) ||
+      !aligned4(v_scales) || !aligned4(seq_lens) || (start != nullptr && !aligned4(start)) ||
+      (dev_status != nullptr && !aligned4(dev_status)))
+    return TD_ERR_UNSUPPORTED;
+  td::ReadF8 p = {};
+  p.k_codes = static_cast<const uint8_t *>(k_codes);
+  p.v_codes = static_cast<const uint8_t *>(v_codes);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.seq_lens = seq_lens;
+  p.start = start;
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.status = dev_status;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.N = N;
+  p.Smax = Smax;
+  p.block_log2 = block_log2(block);
+  p.NB = (Smax + block - 1) / block;
+  const cudaError_t e = td::launch_read_f8(elem_size(dtype), D, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+td_status td_verify_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
+                            const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax,
+                            int D, int block, float scale, int split, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+  if (k_scales == nullptr || v_scales == nullptr) return TD_ERR_INVALID_ARG;
+  // chunks start at multiples of 16 rows, so a 16-row step has one scale
+  if (block_log2(block) < 0 || split % 16 != 0 || !aligned4(k_scales) || !aligned4(v_scales))
+    return TD_ERR_UNSUPPORTED;
+  td::SplitPlan plan;
+  td::SplitParams p;
+  const td_status st = prepare(TD_BF16, q, k_codes, v_codes, seq_lens, B, Hq, Hkv, T, Smax, D, scale, split, out,
+                               lse, workspace, workspace_bytes, dev_status, &plan, &p, td::KvFormat::kF8);
+  if (st != TD_OK) return st;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_log2 = block_log2(block);
+  p.n_blocks = (Smax + block - 1) / block;
+  const cudaError_t e = td::launch_split(TD_BF16, D, plan, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+td_status td_decode_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
+                            const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D,
+                            int block, float scale, int split, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+  return td_verify_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, B, Hq, Hkv, 1, Smax, D, block, scale,
+                           split, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 }  // extern "C"

@@ -27,6 +27,7 @@ struct SplitPlan {
   int cluster;   // 0: persistent kernel; else CTAs per cluster of the cluster kernel (grid = groups x cluster)
   int counters_n;  // completion and slice-merge counters before the fused step's read count in the workspace
   bool q8;       // int8 cache (codes + per-row scales): the quantised-cache kernel
+  bool f8;       // block-scaled e4m3 cache: its kernel
   size_t off_part, bytes;  // workspace layout: counters, then partial blocks
 };
 
@@ -34,10 +35,49 @@ struct SplitPlan {
 // so a later call does not report it as its own); returns TD_ERR_CUDA.
 td_status cuda_fail(cudaError_t e);
 
+// What the caches of an attention call hold: rows of the call's dtype, int8 codes with per-row
+// scales, or e4m3 codes with per-block scales (q and out are bf16 for both, dtype TD_BF16).
+enum class KvFormat { kRows, kQ8, kF8 };
+
 // Fills *plan for the current device; TD_OK, or an error for unsupported shapes.
-// q8: the caches hold int8 codes with per-row scales (q and out are bf16; dtype must be TD_BF16).
 td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, int D, int split, SplitPlan *plan,
-                     bool q8 = false);
+                     KvFormat format = KvFormat::kRows);
+
+// The block-scaled kernel for row blocks of R rows: its function (for the occupancy query) and
+// dynamic shared memory, and its launch.
+const void *f8_kernel(int D, int R, int *smem);
+cudaError_t launch_split_f8(int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream);
+
+// Appends to the block-scaled 8-bit cache (the rotation is skipped when cos_t is null).
+struct AppendF8 {
+  const void *q;   // [B, Hq, T, D] or null
+  void *q_out;
+  const void *k_new, *v_new;  // [B, Hkv, T, D]
+  const float *cos_t, *sin_t;
+  const int32_t *positions;   // [B, T, A] or null: row L + t
+  const int32_t *axes;        // [D / 2] or null: axis 0
+  uint8_t *k_codes, *v_codes;  // [B, Hkv, Smax, D]
+  float *k_scales, *v_scales;  // [B, Hkv, NB]
+  int32_t *seq_lens;
+  uint32_t *status;
+  int B, Hq, Hkv, T, Smax, NB, block_log2, A, table_rows, advance;
+  int per_cta;  // heads of a CTA (tiles kernel)
+};
+// Longest chunk of new rows that the warp-per-row kernel takes, and its CTA's size.
+constexpr int kF8RowsT = 16;
+constexpr int kF8RowsThreads = 1024;
+cudaError_t launch_append_f8(size_t elem_bytes, int D, const AppendF8 &p, cudaStream_t stream);
+
+// Read-back of rows start[b] .. start[b] + N - 1 (start null: 0).
+struct ReadF8 {
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  const int32_t *seq_lens, *start;
+  void *k_out, *v_out;  // [B, Hkv, N, D]
+  uint32_t *status;
+  int B, Hkv, N, Smax, NB, block_log2;
+};
+cudaError_t launch_read_f8(size_t elem_bytes, int D, const ReadF8 &p, cudaStream_t stream);
 
 // Per-row int8 quantisation (codes + fp32 scales) of `rows` rows of D elements.
 cudaError_t launch_quantize_q8(size_t elem_bytes, const void *x, long long rows, int D, int8_t *codes, float *scales,

@@ -13,7 +13,8 @@ namespace td {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kKernelSlots = 2 * 2 * 4 + 2 * 2 + 2;  // CUDA-core: dtype x D x row padding; mma: D x m tiles; q8: D
+// CUDA-core: dtype x D x row padding; mma: D x m tiles; q8: D; f8: D x n tiles
+constexpr int kKernelSlots = 2 * 2 * 4 + 2 * 2 + 2 + 2 * 3;
 
 struct KernelRef {
   const void *fn;
@@ -58,6 +59,8 @@ KernelRef pick_d(int D, int RP) {
   return KernelRef{nullptr, 0, nullptr};
 }
 
+}  // namespace
+
 // cuTensorMapEncodeTiled, resolved once through the runtime (no link against the driver).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -72,6 +75,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+namespace {
 
 // 3-D map over a bf16 cache [B*Hkv][Smax][D]: boxes of 64 columns (128 bytes) x 64 rows,
 // 128-byte swizzle, zero fill outside the tensor.
@@ -347,7 +352,8 @@ static int device_l2_bytes(int device) {
 }
 
 td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, int D, int split, SplitPlan *plan,
-                     bool q8) {
+                     KvFormat format) {
+  const bool q8 = format == KvFormat::kQ8, f8 = format == KvFormat::kF8;
   if (dtype != TD_F32 && dtype != TD_BF16) return TD_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return TD_ERR_UNSUPPORTED;
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Smax < 1 || split < 0 || Hq % Hkv != 0) return TD_ERR_INVALID_ARG;
@@ -375,13 +381,20 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   }
   const long long RB = (GT + R - 1) / R;
   const long long U = (long long)Hkv * RB;
-  if (q8 && !mma) return TD_ERR_UNSUPPORTED;
-  const KernelRef k = q8 ? (D == 64 ? q8_ref_of<64>() : q8_ref_of<128>()) : pick(dtype, D, mma, variant);
+  if ((q8 || f8) && !mma) return TD_ERR_UNSUPPORTED;
+  KernelRef k{};
+  if (f8)
+    k.fn = f8_kernel(D, R, &k.smem);
+  else
+    k = q8 ? (D == 64 ? q8_ref_of<64>() : q8_ref_of<128>()) : pick(dtype, D, mma, variant);
   if (k.fn == nullptr) return TD_ERR_UNSUPPORTED;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return TD_ERR_CUDA;
   const int sms = device_sm_count(device);
-  const int per_sm = blocks_per_sm(device, q8 ? 20 + (D == 64 ? 0 : 1) : slot_of(dtype, D, mma, variant), k);
+  const int slot = f8   ? 22 + (D == 64 ? 0 : 3) + (R - 1) / 8
+                   : q8 ? 20 + (D == 64 ? 0 : 1)
+                        : slot_of(dtype, D, mma, variant);
+  const int per_sm = blocks_per_sm(device, slot, k);
   if (sms <= 0 || per_sm <= 0) return TD_ERR_CUDA;
   // CTAs the automatic split aims to fill. When a kv head's rows fit one row block and the
   // groups are few, leave one slot per group free: the previous call's merging CTAs (one per
@@ -407,6 +420,7 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   if (items_max >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
   plan->mma = mma;
   plan->q8 = q8;
+  plan->f8 = f8;
   plan->RP = variant;
   plan->R = R;
   plan->RB = (int)RB;
@@ -422,7 +436,7 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   // of clusters of at least two CTAs, about two CTAs per SM: one cluster per group, the
   // largest that fits (its CTAs share the group's keys evenly and merge on chip)
   plan->cluster = 0;
-  if (mma && !q8 && split == 0) {
+  if (mma && !q8 && !f8 && split == 0) {
     const long long groups = (long long)B * U;
     for (int cs = kMaxCluster; cs >= 2; cs /= 2) {
       if (groups * cs * 5 < (long long)sms * 8) break;
@@ -445,7 +459,7 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   // blocks per kv head read each tile more than once and warm 4 units (the 6-token verify:
   // 27.8 us without, 27.5 with 4, 29.9 with 16).
   {
-    const long long unit = 2LL * 64 * (q8 ? D + 4 : (long long)D * (dtype == TD_F32 ? 4 : 2));
+    const long long unit = 2LL * 64 * (q8 ? D + 4 : f8 ? D : (long long)D * (dtype == TD_F32 ? 4 : 2));
     const long long l2 = device_l2_bytes(device);
     const long long warm = RB == 1 ? (l2 * 9 / 10) / ((long long)plan->grid * unit) : 4;
     plan->warm = (int)(warm < 1 ? 1 : warm > 16 ? 16 : warm);
@@ -461,7 +475,9 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
 
 cudaError_t launch_split(td_dtype dtype, int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
   cudaError_t e;
-  if (plan.q8) {
+  if (plan.f8) {
+    e = launch_split_f8(D, plan, p, stream);
+  } else if (plan.q8) {
     e = D == 64 ? launch_q8<64>(p, plan.grid, plan.smem, plan.spare, stream)
                 : launch_q8<128>(p, plan.grid, plan.smem, plan.spare, stream);
   } else if (plan.cluster > 0) {

@@ -1,0 +1,551 @@
+// Split-KV attention over the block-scaled 8-bit cache (e4m3 codes, one fp32 scale per block of
+// tokens and kv head).
+//
+//   out = sum_j p_j vs_j v_j / sum_j p_j,   p_j = 2^(scale log2(e) ks_j (q . k_j) - m)
+// with codes k_j, v_j and the scales ks_j, vs_j of the blocks that hold row j. The method is the
+// split attention of split_attn_mma_kernel: the plan, the chunks, the L2 warm-up before the wait
+// for the previous kernel and the fused merge are its own.
+//
+// Design:
+//  * Stages of 128 rows of K and V cross by TMA as code tiles (128-byte swizzle for D = 128,
+//    64-byte for D = 64); each of the 4 warps takes 32 keys of a stage. Half the bytes of bf16, so
+//    the register work of a key counts: the tensor-core operands are taken from the code tiles by
+//    ldmatrix (16-bit words, two codes), and one conversion turns two codes into the exact fp16
+//    pair of their values (e4m3's range and precision lie inside fp16's).
+//  * Keys lie on the m side of the products and the query rows of a row block on 1, 2 or 3 8-wide
+//    n tiles, so a converted K or V fragment serves up to 24 rows (a verify chunk of 6 tokens of 4
+//    grouped heads reads the cache once).
+//  * A block holds at least 16 rows and a chunk starts at a multiple of 16, so the scales are
+//    uniform over each 16-key half of a warp's step: the key scale multiplies the half's scores,
+//    the value scale its p V product, in fp32, on the way into the running sums. Nothing of a
+//    scale reaches the fp16 operands, so any scale is as good as another.
+//  * fp16 has 11 significant bits but a short range: a query row is first brought to a largest
+//    element in [2^14, 2^15) by a power of two (undone with the scores' scale), and probabilities
+//    are kept 2^7 above their usual place (at most 2^15), which puts the least normal fp16 at
+//    2^-21 of a row's reference.
+//  * A code may be NaN (a stored NaN or infinity; any byte behind a sequence's end). A step that
+//    reaches a row's limit or the sequence's end zeroes the value codes past the end, and a NaN
+//    value code that only some rows see is taken out of the product and put into those rows' sums
+//    by a product of NaN and visibility indicators.
+#include <algorithm>
+#include <mutex>
+
+#include "td_f8.cuh"
+#include "td_internal.h"
+#include "td_split_mma.cuh"
+
+namespace td {
+
+namespace {
+
+template <int D>
+struct F8Cfg {
+  static constexpr int NST = D == 128 ? 3 : 6;  // ring stages: two CTAs per SM
+  static constexpr int TK = 128;                // keys per stage, 32 per warp
+  static constexpr int CODE_BYTES = TK * D;     // one code tile
+  static constexpr int STAGE_BYTES = 2 * CODE_BYTES;
+  static constexpr int RING_BYTES = NST * STAGE_BYTES;
+  static constexpr int SMEM_BYTES = RING_BYTES + 1024;  // + alignment slack
+  static_assert(CODE_BYTES % 1024 == 0, "code tiles keep the swizzle's 1024-byte alignment");
+  static_assert(kWarps * kMaxTileRows * (D + 6) * 4 + (2 + kWarps) * kMaxTileRows * 4 <= RING_BYTES, "combine area fits");
+  static_assert((merge_fixed_floats<D, kMaxTileRows>() + part_block_floats(kMaxTileRows, D)) * 4 <= RING_BYTES,
+                "merge stages at least one chunk");
+  static_assert(SMEM_BYTES + 8704 <= 227 * 1024, "shared memory of a CTA");
+};
+
+// Powers of two that the probabilities are kept above their usual place by.
+constexpr float kPShift = 7.f;
+
+// Byte offset of 16-byte chunk `ch` of row `row` in a code tile of D-byte rows as the TMA unit
+// writes it (128- or 64-byte swizzle): the 8 rows one ldmatrix reads fall in 8 bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t code_swz(int row, int ch) {
+  if constexpr (D == 128) {
+    return (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4));
+  } else {
+    return (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+  }
+}
+
+struct F8Args {
+  CUtensorMap kmap, vmap;  // codes [B*Hkv][Smax][D]
+  SplitParams p;
+};
+
+__device__ __forceinline__ uint32_t lo_pair(uint32_t w) { return e4m3x2_f16x2((uint16_t)w); }
+__device__ __forceinline__ uint32_t hi_pair(uint32_t w) { return e4m3x2_f16x2((uint16_t)(w >> 16)); }
+
+// The bytes of w that are NaN codes (0x7f or 0xff), as 0x80 each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Bytes 0, 2 (or 1, 3) of a word marked 0x80 as an fp16 pair of ones.
+__device__ __forceinline__ uint32_t ones_of(uint32_t n, int odd) {
+  return ((n >> (8 * odd)) & 0x80u ? 0x3c00u : 0u) | ((n >> (8 * odd + 16)) & 0x80u ? 0x3c000000u : 0u);
+}
+
+// One warp's step over 32 keys (rows kr .. kr+31 of the code tiles kt / vt; keys key0 ..) for the
+// NT * 8 query rows of the block. Fragment orders (mma m16n8k16, g = lane / 4, c = lane % 4):
+//  - scores S^T = K Q^T: ldmatrix gives thread (g, c) codes 4c .. 4c+3 of a 16-dim block of keys g
+//    and g + 8; they fill k slots 2c, 2c+1, 2c+8, 2c+9 of the A fragment, and the query fragments
+//    qn hold the same dims in the same slots. sc[nt][hf] holds keys g, g + 8 of 16-key half hf
+//    for rows 8 nt + 2c, + 1;
+//  - O^T += V^T P^T: the transposed ldmatrix gives thread (g, c) dims 2g, 2g+1 of keys 2c, 2c+1;
+//    with the middle bytes swapped the two conversions give dim 2g's pair (tile o[2i]) and dim
+//    2g+1's (tile o[2i+1]). o[nt][2i] holds dims 32i + 2g and 32i + 16 + 2g of rows 8 nt + 2c, + 1,
+//    o[nt][2i+1] the dims after them.
+// ksc / vsc: the halves' scales; qs: the rows' score scale (base 2); lim: the rows' visible keys
+// (index 2 nt + e); kend: the sequence's end. MASK: some key lies past a row's limit or the end.
+template <int D, int NT, bool MASK>
+__device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[NT][D / 16][2], uint32_t kt, uint32_t vt, int kr,
+                                               int key0, int kend, const int (&lim)[2 * NT], const float (&qs)[2 * NT],
+                                               const float (&ksc)[2], const float (&vsc)[2],
+                                               float (&o)[NT][D / 16][4], float (&m_run)[2 * NT],
+                                               float (&l_run)[2 * NT]) {
+  constexpr int NX = D / 32;  // ldmatrix.x4 per 16 keys: 16 keys x 32 dims
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int lrow = kr + (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
+  float sc[NT][2][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) sc[nt][hf][0] = sc[nt][hf][1] = sc[nt][hf][2] = sc[nt][hf][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NX; ++i)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t r[4];  // keys 0-7 / 8-15 of dims 32i .. 32i+15, then of dims 32i+16 .. 32i+31
+      ldmatrix_x4(r, kt + code_swz<D>(lrow + 16 * hf, 2 * i + lch));
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint32_t ak[4] = {lo_pair(r[2 * blk]), lo_pair(r[2 * blk + 1]), hi_pair(r[2 * blk]),
+                                hi_pair(r[2 * blk + 1])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt][hf], ak, qn[nt][2 * i + blk][0], qn[nt][2 * i + blk][1]);
+      }
+    }
+  float alpha[2 * NT];
+  bool moved = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int ri = 2 * nt + e;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float kss = ksc[hf] * qs[ri];
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk) {
+          const int key = key0 + 16 * hf + 8 * hk + gid;
+          const float v = !MASK || key < lim[ri] ? sc[nt][hf][2 * hk + e] * kss : -INFINITY;
+          sc[nt][hf][2 * hk + e] = v;
+          mx = fmaxf(mx, v);
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      // lazy reference maximum (see warp_keys16): rows with no visible key are never rescaled
+      const bool move = mx > m_run[ri] + kMaxGap;
+      alpha[ri] = move ? exp2_approx(m_run[ri] - mx) : 1.f;
+      if (move) m_run[ri] = mx;
+      moved |= move;
+      const float base = m_run[ri] == -INFINITY ? 0.f : m_run[ri] - kPShift;
+      float ps = 0.f;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk) {
+          const float pv = exp2_approx(sc[nt][hf][2 * hk + e] - base);
+          sc[nt][hf][2 * hk + e] = pv;
+          ps += pv;
+        }
+      l_run[ri] = l_run[ri] * alpha[ri] + ps;  // this thread's keys; lanes summed at the end
+    }
+  if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        o[nt][t][0] *= alpha[2 * nt];
+        o[nt][t][1] *= alpha[2 * nt + 1];
+        o[nt][t][2] *= alpha[2 * nt];
+        o[nt][t][3] *= alpha[2 * nt + 1];
+      }
+  }
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    // P^T as B operands: keys 2c, 2c+1 (+8) of row 8 nt + g
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      pb[nt][0] = movmatrix_trans(pack_f16x2(sc[nt][hf][0], sc[nt][hf][1]));
+      pb[nt][1] = movmatrix_trans(pack_f16x2(sc[nt][hf][2], sc[nt][hf][3]));
+    }
+    uint32_t live[2];  // bytes of keys 2c, 2c+1 (+8) before the sequence's end
+    if constexpr (MASK) {
+#pragma unroll
+      for (int hk = 0; hk < 2; ++hk) {
+        const int key = key0 + 16 * hf + 8 * hk + 2 * tig;
+        live[hk] = (key < kend ? 0xffffu : 0u) | (key + 1 < kend ? 0xffff0000u : 0u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+      uint32_t r[4];  // transposed: keys 0-7 / 8-15 of dims 32i .. 32i+15, then of 32i+16 ..
+      ldmatrix_x4_trans(r, vt + code_swz<D>(lrow + 16 * hf, 2 * i + lch));
+      if constexpr (MASK) {
+        uint32_t n[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          r[x] &= live[x & 1];
+          n[x] = nan_bytes(r[x]);
+          r[x] &= ~((n[x] >> 7) * 0xffu);
+        }
+        if (__any_sync(0xffffffffu, (n[0] | n[1] | n[2] | n[3]) != 0u)) {
+          // rows that see a NaN value code: count them per output by indicators
+#pragma unroll 1
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t see[2] = {0u, 0u};
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+              if (x == nt)
+#pragma unroll
+                for (int hk = 0; hk < 2; ++hk) {
+                  const int key = key0 + 16 * hf + 8 * hk + gid;
+                  see[hk] = (key < lim[2 * x] ? 0x3c00u : 0u) | (key < lim[2 * x + 1] ? 0x3c000000u : 0u);
+                }
+            const uint32_t b0 = movmatrix_trans(see[0]), b1 = movmatrix_trans(see[1]);
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+              const uint32_t a[4] = {ones_of(n[0], odd), ones_of(n[2], odd), ones_of(n[1], odd), ones_of(n[3], odd)};
+              float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16_16816(cnt, a, b0, b1);
+#pragma unroll
+              for (int x = 0; x < NT; ++x)
+                if (x == nt)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y)
+                    if (cnt[y] > 0.f) o[x][2 * i + odd][y] = __uint_as_float(0x7fffffffu);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) r[x] = __byte_perm(r[x], 0u, 0x3120);  // the middle bytes swapped
+      const uint32_t ae[4] = {lo_pair(r[0]), lo_pair(r[2]), lo_pair(r[1]), lo_pair(r[3])};
+      const uint32_t ao[4] = {hi_pair(r[0]), hi_pair(r[2]), hi_pair(r[1]), hi_pair(r[3])};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float te[4] = {0.f, 0.f, 0.f, 0.f}, to[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16_16816(te, ae, pb[nt][0], pb[nt][1]);
+        mma_f16_16816(to, ao, pb[nt][0], pb[nt][1]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          o[nt][2 * i][y] = fmaf(te[y], vsc[hf], o[nt][2 * i][y]);
+          o[nt][2 * i + 1][y] = fmaf(to[y], vsc[hf], o[nt][2 * i + 1][y]);
+        }
+      }
+    }
+  }
+}
+
+// Streams keys [c0, c1) of (b, kvh) for row block rb, as stream_chunk does for bf16 caches,
+// leaving the same combine area (at the start of `smem`), 8 NT rows per warp. c0 is a multiple of
+// 16. False, CTA-uniformly, if a copy never completed.
+template <int D, int NT>
+__device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *s_bars, uint32_t &seq, int b, int kvh,
+                                int rb, int L, int c0, int c1) {
+  using C = F8Cfg<D>;
+  constexpr int NST = C::NST, TR = 8 * NT;
+  const SplitParams &p = a.p;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+  const int GT = p.G * p.T;
+  const int nstages = (c1 - c0 + C::TK - 1) / C::TK;
+  const int zc = b * p.Hkv + kvh;
+  const uint64_t policy = l2_evict_first_policy();
+
+  auto issue = [&](int sidx) {
+    const int buf = (seq + sidx) % NST;
+    const uint32_t bar = smem_u32(&s_bars[buf]);
+    const uint32_t dst = sbase + buf * C::STAGE_BYTES;
+    const int y = c0 + sidx * C::TK;
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+    tma_load_3d(dst, &a.kmap, 0, y, zc, bar, policy);
+    tma_load_3d(dst + C::CODE_BYTES, &a.vmap, 0, y, zc, bar, policy);
+  };
+  if (tid == 0) {
+    for (int s2 = 0; s2 < min(NST - 1, nstages); ++s2) issue(s2);
+  }
+  // lanes 0 .. 3 fetch the scales of this warp's two 16-key halves of a stage (K, then V), one
+  // stage ahead of their use; a half past the chunk's end reads none
+  const float *scales = (lane & 2 ? p.v_scales : p.k_scales) + (size_t)zc * p.n_blocks;
+  auto load_scale = [&](int st) -> float {
+    const int key = c0 + st * C::TK + warp * 32 + (lane & 1) * 16;
+    return lane < 4 && st < nstages && key < c1 ? __ldcg(scales + (key >> p.block_log2)) : 0.f;
+  };
+  float s_next = load_scale(0);
+
+  // query row 8 nt + g of this block as fp16 B fragments (slots 2c, 2c+1 <- dims 4c, 4c+1; slots
+  // 2c+8, 2c+9 <- dims 4c+2, 4c+3), brought to a largest element in [2^14, 2^15); the limits and
+  // score scales of rows 8 nt + 2c, + 1
+  uint32_t qn[NT][D / 16][2];
+  int lim[2 * NT];
+  float qs[2 * NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + gid, gr = rb * p.R + r;
+    const bool valid = r < p.R && gr < GT;
+    const int hq = kvh * p.G + (valid ? gr / p.T : 0), t = valid ? gr % p.T : 0;
+    const uint2 *qrow = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                        (((size_t)b * p.Hq + hq) * p.T + t) * D);
+    uint2 w[D / 16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      w[ks] = valid ? qrow[ks * 4 + tig] : make_uint2(0u, 0u);
+      top = max(max(top, w[ks].x & 0x7fffu), (w[ks].x >> 16) & 0x7fffu);
+      top = max(max(top, w[ks].y & 0x7fffu), (w[ks].y >> 16) & 0x7fffu);
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // exponent of the row's largest element (a bf16's 8 exponent bits); rows of zeros and rows
+    // with an infinity or NaN stay as they are
+    const int ex = (int)(top >> 7);
+    const int k = top == 0u || ex == 255 ? 0 : min(14 - (ex - 127), 126);
+    const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      float f[4];
+      widen_bf16x2(w[ks].x, f[0], f[1]);
+      widen_bf16x2(w[ks].y, f[2], f[3]);
+      qn[nt][ks][0] = pack_f16x2(f[0] * up, f[1] * up);
+      qn[nt][ks][1] = pack_f16x2(f[2] * up, f[3] * up);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      qs[2 * nt + e] = p.qscale * __shfl_sync(0xffffffffu, down, 4 * (2 * tig + e));
+      const int lr = 8 * nt + 2 * tig + e, lgr = rb * p.R + lr;
+      lim[2 * nt + e] = lr < p.R && lgr < GT ? min(max(L - p.T + lgr % p.T + 1, 0), c1) : 0;
+    }
+  }
+  // keys every row of the block sees: the limit of its first token (token 0 if the rows wrap)
+  const int first = (rb * p.R) % p.T, rows = min(p.R, GT - rb * p.R);
+  const int lim_all = min(c1, max(L - p.T + (first + rows > p.T ? 0 : first) + 1, 0));
+  float o[NT][D / 16][4];
+  float m_run[2 * NT], l_run[2 * NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2 * NT; ++h) m_run[h] = -INFINITY, l_run[h] = 0.f;
+
+  int consumed = 0;
+  bool ok = true;
+  for (int st = 0; st < nstages; ++st) {
+    const float s_mine = s_next;
+    s_next = load_scale(st + 1);
+    const int buf = (seq + st) % NST;
+    const bool landed = mbar_wait_bounded(smem_u32(&s_bars[buf]), ((seq + st) / NST) & 1u);
+    // every warp has finished the previous stage, whose buffer is refilled next; one decision
+    // for the whole CTA
+    if (!__syncthreads_and(landed)) {
+      ok = false;
+      break;
+    }
+    if (tid == 0 && st + NST - 1 < nstages) issue(st + NST - 1);
+    const int kr = warp * 32, key0 = c0 + st * C::TK + kr;
+    if (key0 < c1) {
+      const uint32_t kt = sbase + buf * C::STAGE_BYTES, vt = kt + C::CODE_BYTES;
+      const float ksc[2] = {__shfl_sync(0xffffffffu, s_mine, 0), __shfl_sync(0xffffffffu, s_mine, 1)};
+      const float vsc[2] = {__shfl_sync(0xffffffffu, s_mine, 2), __shfl_sync(0xffffffffu, s_mine, 3)};
+      if (key0 + 32 <= lim_all)
+        warp_keys32_f8<D, NT, false>(qn, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
+      else
+        warp_keys32_f8<D, NT, true>(qn, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
+    }
+    consumed = st + 1;
+  }
+  if (!ok) {
+    const int issued = min(nstages, consumed + NST - 1);
+    for (int st = consumed; st < issued; ++st)
+      mbar_wait_bounded(smem_u32(&s_bars[(seq + st) % NST]), ((seq + st) / NST) & 1u);
+    if (tid == 0) report(p.status, TD_DEV_WAIT_TIMEOUT);
+#pragma unroll
+    for (int h = 0; h < 2 * NT; ++h) m_run[h] = -INFINITY, l_run[h] = 0.f;
+  }
+  seq += nstages;
+#pragma unroll
+  for (int h = 0; h < 2 * NT; ++h) {
+    l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 4);
+    l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 8);
+    l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], 16);
+  }
+  __syncthreads();  // ring idle: reuse it as the combine area
+  float *cm = reinterpret_cast<float *>(smem);
+  float *cl = cm + kWarps * TR;
+  float *ca = cm + 2 * kWarps * TR;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * nt + 2 * tig + e, ri = 2 * nt + e;
+      if (gid == 0) {
+        // a row that saw a NaN key: the merges drop partials whose sum is not positive, so it is
+        // given a sum and a maximum that outweigh every other partial's
+        const bool bad = isnan(l_run[ri]);
+        cm[warp * TR + r] = bad ? 3e38f : m_run[ri] - kPShift;
+        cl[warp * TR + r] = bad ? INFINITY : l_run[ri];
+      }
+      float *row = &ca[(warp * TR + r) * combine_stride<D>()];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        *reinterpret_cast<float2 *>(&row[32 * i + 2 * gid]) = make_float2(o[nt][2 * i][e], o[nt][2 * i + 1][e]);
+        *reinterpret_cast<float2 *>(&row[32 * i + 16 + 2 * gid]) =
+            make_float2(o[nt][2 * i][2 + e], o[nt][2 * i + 1][2 + e]);
+      }
+    }
+  __syncthreads();
+  return ok;
+}
+
+// Persistent kernel over a block-scaled cache: the items, chunks and fused merge of
+// split_attn_mma_kernel. EARLY_PLAN: planned before the wait for the previous kernel and kept if
+// the lengths read the same after it (launched when the plan leaves slots free for that kernel's
+// merging CTAs).
+template <int D, int NT, bool EARLY_PLAN>
+__global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid_constant__ F8Args a) {
+  using C = F8Cfg<D>;
+  using E = __nv_bfloat16;
+  constexpr int NST = C::NST, TR = 8 * NT;
+  const SplitParams &p = a.p;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ int s_len[TD_MAX_BATCH];
+  __shared__ int s_prefix[TD_MAX_BATCH + 1];
+  __shared__ long long s_red[2 * kWarps];
+  __shared__ int s_chunk, s_last;
+  __shared__ __align__(8) uint64_t s_merge_bar;
+  __shared__ __align__(8) uint64_t s_bars[NST];
+
+  const int tid = threadIdx.x;
+  unsigned char *smem = align1024(smem_raw);
+  float *combine = reinterpret_cast<float *>(smem);
+  if (tid == 0) {
+    mbar_init(smem_u32(&s_merge_bar), 1);
+#pragma unroll
+    for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&s_bars[i]), 1);
+    fence_mbar_init();
+  }
+  uint32_t merge_phase = 0;
+  uint32_t seq = 0;
+  if (tid == 0) prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
+  if constexpr (EARLY_PLAN) plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
+  griddep_wait();  // inputs may come from the previous kernel in the stream
+  griddep_launch_dependents();
+  if constexpr (EARLY_PLAN)
+    confirm_plan(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+  else
+    plan_items(p, s_len, s_prefix, &s_chunk, s_red);
+  const int S = s_chunk;
+  const int W = s_prefix[p.B];
+  const int rows = p.Hq * p.T;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (s_len[b] != 0) continue;
+    for (int idx = tid; idx < rows * D; idx += kThreads)
+      store_elem<E>(static_cast<E *>(p.out) + (long long)b * rows * D + idx, 0.f);
+    if (p.lse != nullptr)
+      for (int r = tid; r < rows; r += kThreads) p.lse[(long long)b * rows + r] = -INFINITY;
+  }
+  for (int item = blockIdx.x; item < W; item += gridDim.x) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_prefix[mid] <= item) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo;
+    const int L = s_len[b];
+    const int NC = (L + S - 1) / S;
+    const int local = item - s_prefix[b];
+    const int c = local % NC;
+    const int rest = local / NC;
+    const int rb = rest % p.RB;
+    const int kvh = rest / p.RB;
+    const int c0 = c * S;
+    const bool ok = stream_chunk_f8<D, NT>(a, smem, s_bars, seq, b, kvh, rb, L, c0, min(c0 + S, L));
+    finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
+                                                       rb, c, NC, &s_last, W <= (int)gridDim.x);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (!ok) break;
+  }
+}
+
+template <int D>
+const void *kernel_of(int nt, bool early) {
+  switch (nt) {
+    case 1:
+      return early ? reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 1, true>)
+                   : reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 1, false>);
+    case 2: return reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 2, false>);
+    default: return reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 3, false>);
+  }
+}
+
+bool encode_code_map(CUtensorMap *m, const void *base, const SplitParams &p, int D) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Smax, (cuuint64_t)p.B * p.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)p.Smax * D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)F8Cfg<128>::TK, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
+  constexpr int kMaxDevices = 64;
+  F8Args a;
+  if (!encode_code_map(&a.kmap, p.k, p, D) || !encode_code_map(&a.vmap, p.v, p, D)) return cudaErrorInvalidValue;
+  a.p = p;
+  {
+    // every instantiation's shared-memory opt-in, once per device
+    static std::mutex mu;
+    static bool done[kMaxDevices] = {};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[device]) {
+      for (const void *fn : {kernel_of<D>(1, true), kernel_of<D>(1, false), kernel_of<D>(2, false), kernel_of<D>(3, false)}) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem);
+        if (e != cudaSuccess) return e;
+      }
+      done[device] = true;
+    }
+  }
+  const dim3 grid(plan.grid), block(kThreads);
+  if (p.R <= 8)
+    return plan.spare ? launch_pdl(split_attn_f8_kernel<D, 1, true>, grid, block, plan.smem, stream, a)
+                      : launch_pdl(split_attn_f8_kernel<D, 1, false>, grid, block, plan.smem, stream, a);
+  if (p.R <= 16) return launch_pdl(split_attn_f8_kernel<D, 2, false>, grid, block, plan.smem, stream, a);
+  return launch_pdl(split_attn_f8_kernel<D, 3, false>, grid, block, plan.smem, stream, a);
+}
+
+}  // namespace
+
+const void *f8_kernel(int D, int R, int *smem) {
+  const int nt = (R + 7) / 8;
+  *smem = D == 64 ? F8Cfg<64>::SMEM_BYTES : F8Cfg<128>::SMEM_BYTES;
+  return D == 64 ? kernel_of<64>(nt, false) : kernel_of<128>(nt, false);
+}
+
+cudaError_t launch_split_f8(int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
+  return D == 64 ? launch<64>(plan, p, stream) : launch<128>(plan, p, stream);
+}
+
+}  // namespace td

@@ -40,6 +40,9 @@ namespace td {
 
 constexpr int kMmaRows = 16;  // query rows per CTA: one m16 tile
 
+// The driver's tensor-map encoder; null without a driver.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 // Tile of a warp's 16-key step, by the query rows of a row block:
 //   kTileN8   at most 8 rows: keys on the m side, the rows on one 8-wide n tile (warp_keys16_n8);
 //   kTileM16  9 to 16 rows: the rows on the m side of one 16-row tile, keys on n (warp_keys16);
@@ -649,11 +652,14 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
   return ok;
 }
 
-// Warms L2 with the first `n` stages (of 64 rows) of K and V of keys [c0, c1) of (b, kvh):
-// bf16 rows, or for 8-bit caches (Q8) the code rows and their scales.
-template <int D, bool Q8 = false>
+// What a warm-up fetches: bf16 rows, int8 code rows with their scales, or e4m3 code rows alone
+// (their block scales are a few lines).
+enum : int { kWarmRows = 0, kWarmQ8 = 1, kWarmF8 = 2 };
+
+// Warms L2 with the first `n` stages (of 64 rows) of K and V of keys [c0, c1) of (b, kvh).
+template <int D, int WARM = kWarmRows>
 __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, int c1, int n) {
-  constexpr int ROWB = Q8 ? D : D * 2, TK = 64;
+  constexpr int ROWB = WARM != kWarmRows ? D : D * 2, TK = 64;
   const size_t row0 = ((size_t)b * p.Hkv + kvh) * p.Smax + c0;
   const unsigned char *k = static_cast<const unsigned char *>(p.k) + row0 * ROWB;
   const unsigned char *v = static_cast<const unsigned char *>(p.v) + row0 * ROWB;
@@ -664,7 +670,7 @@ __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, 
     prefetch_l2_bulk(k + (size_t)r * ROWB, bytes);
     prefetch_l2_bulk(v + (size_t)r * ROWB, bytes);
   }
-  if constexpr (Q8) {
+  if constexpr (WARM == kWarmQ8) {
     // the whole 16-byte units holding the rows' scales (a sequence's Smax scales are a whole
     // number of 16-byte units, so these stay inside its own)
     const float *sc[2] = {p.k_scales + row0, p.v_scales + row0};
@@ -685,7 +691,7 @@ __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, 
 // prefetch, and the real plan is made after the wait. Batches of up to 8 sequences.
 // `item` is the CTA's first work item; a cluster of `parts` CTAs shares each item, this CTA
 // taking run `part` of its whole 64-key stages (as split_attn_cc_kernel cuts it).
-template <int D, bool Q8 = false>
+template <int D, int WARM = kWarmRows>
 __device__ void prefetch_first_item(const SplitParams &p, int n, int item, int part = 0, int parts = 1) {
   if (p.B > 8) return;
   long long all = 0;
@@ -708,7 +714,7 @@ __device__ void prefetch_first_item(const SplitParams &p, int n, int item, int p
       const int c0 = c * S, c1 = min(c0 + S, L);
       const int per = ((c1 - c0 + parts - 1) / parts + 63) / 64 * 64;
       const int r0 = min(c0 + part * per, c1);
-      prefetch_chunk_l2<D, Q8>(p, b, kvh, r0, min(r0 + per, c1), n);
+      prefetch_chunk_l2<D, WARM>(p, b, kvh, r0, min(r0 + per, c1), n);
       return;
     }
     item -= NC * U;

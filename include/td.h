@@ -32,6 +32,9 @@
  *                  its next step; "tinydecode"'s prefill path is causal over the prompt).
  *   td_*_q8        an 8-bit KV cache: int8 codes with one fp32 scale per row (the per-row
  *                  INT8 scheme "llm-decode-cuda" applies to its weights, for the K/V bytes).
+ *   td_*_f8        an 8-bit KV cache in blocks: e4m3 codes with one fp32 scale per block of
+ *                  tokens and kv head, written (optionally rotated first, by positions with
+ *                  several axes), read back, and attended.
  *
  * Layouts (row-major, contiguous, element type given by td_dtype):
  *   q, out         [B, Hq, D] for decode; [B, Hq, T, D] for verify
@@ -83,6 +86,7 @@ typedef enum td_dtype { TD_F32 = 0, TD_BF16 = 1 } td_dtype;
 #define TD_DEV_WORKSPACE_DIRTY 32u /* a completion counter was not zero: workspace not zeroed for this
                                       layout; output invalid (zero the workspace and call again) */
 #define TD_DEV_BAD_TOKEN 64u       /* speculative accept: a draft token outside [0, V), counted as rejected */
+#define TD_DEV_BAD_POSITION 128u   /* rotation: an axis or position out of range, its pairs left unrotated */
 
 /* Largest batch a call accepts. */
 #define TD_MAX_BATCH 1024
@@ -269,6 +273,74 @@ td_status td_decode_attn_q8(const void *q, const int8_t *k_codes, const float *k
 td_status td_verify_attn_q8(const void *q, const int8_t *k_codes, const float *k_scales, const int8_t *v_codes,
                             const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax,
                             int D, float scale, int split, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/*
+ * 8-bit KV cache in blocks (f8). Codes are e4m3 (sign, 4 exponent and 3 mantissa bits; largest
+ * value 448, NaN 0x7f and 0xff, no infinity), k_codes and v_codes uint8 [B, Hkv, Smax, D]; scales
+ * are fp32, k_scales and v_scales [B, Hkv, NB], NB = ceil(Smax / block), one for `block`
+ * consecutive rows of one kv head (block 16, 32, 64 or 128). A row reads back as code * scale.
+ * D is 64 or 128 in every f8 call. seq_lens is int32 [B] on the device.
+ *
+ * An append gives every block it writes rows of
+ *   c = 2^k, the least k >= -126 with |x| <= 448 * 2^k for all finite new elements x in the block,
+ *   s = max(stored scale, c) if the block already holds rows of its sequence (below L), else c;
+ * where that is more than the stored scale, the block's older codes become
+ *   e4m3(code * (stored scale / s)),
+ * and the new rows are stored as e4m3(x * (1 / s)): fp32 operations rounded to nearest even, then
+ * one rounding to nearest even (ties to even, saturating) into e4m3. For the powers of two that
+ * appends write, both products are exact. NaN and infinite elements are stored as NaN. A scale
+ * only grows until its block's first row is written again. Stored scales are positive and finite;
+ * caches filled in another way may hold any such scales.
+ */
+
+/* td_kv_append for an f8 cache (new rows [B, Hkv, T, D] of dtype TD_F32 or TD_BF16): the same
+ * overflow rule, advance and status bit; 16-byte aligned rows and codes. One launch, and for
+ * T > 16 with advance a second one that moves the lengths. */
+td_status td_kv_append_f8(td_dtype dtype, const void *k_new, const void *v_new, void *k_codes, float *k_scales,
+                          void *v_codes, float *v_scales, int32_t *seq_lens, int B, int Hkv, int T, int Smax, int D,
+                          int block, int advance, uint32_t *dev_status, void *stream);
+
+/*
+ * td_rope_kv_append for an f8 cache: the keys (and, when q is given, the query rows of q_out,
+ * which may be q) are rotated in fp32 first; the keys go from there into codes with one rounding.
+ * Pair i of token t turns by the angle in row P of cos_t / sin_t, fp32 [table_rows, D/2]:
+ *   positions NULL: P = L + t, the token's cache row (table_rows >= Smax);
+ *   else            P = positions[b, t, axes[i]], positions int32 [B, T, n_axes], axes int32 [D/2]
+ *                   (NULL: axis 0), n_axes 1 .. 16: time, height and width of image or video
+ *                   tokens, or a position that is not the cache row.
+ * A position outside [0, table_rows) or an axis outside [0, n_axes) leaves its pair as it was and
+ * sets TD_DEV_BAD_POSITION. A sequence that does not fit is left untouched, its q_out rows too.
+ */
+td_status td_rope_kv_append_f8(td_dtype dtype, const void *q, void *q_out, int Hq, const void *k_new,
+                               const void *v_new, const float *cos_t, const float *sin_t, int table_rows,
+                               const int32_t *positions, const int32_t *axes, int n_axes, void *k_codes,
+                               float *k_scales, void *v_codes, float *v_scales, int32_t *seq_lens, int B, int Hkv,
+                               int T, int Smax, int D, int block, int advance, uint32_t *dev_status, void *stream);
+
+/*
+ * Read-back: for every b, kv head and t < N with 0 <= j = start[b] + t < L_b (seq_lens[b] clamped
+ * to [0, Smax], see TD_DEV_* bits; start NULL: 0),
+ *   k_out[b, h, t, :] = k code * scale of row j, and v_out likewise,
+ * fp32 products rounded to nearest even into dtype. Other rows of the outputs are left as they
+ * were. k_out, v_out [B, Hkv, N, D], 16-byte aligned: with N = Smax of another cache they are the
+ * bf16 caches that td_prefill_attn reads.
+ */
+td_status td_kv_read_f8(td_dtype dtype, const void *k_codes, const float *k_scales, const void *v_codes,
+                        const float *v_scales, const int32_t *seq_lens, const int32_t *start, int B, int Hkv, int N,
+                        int Smax, int D, int block, void *k_out, void *v_out, uint32_t *dev_status, void *stream);
+
+/* td_decode_attn / td_verify_attn over an f8 cache: the results over the cache the codes stand
+ * for, q and out bf16. split is 0 or a multiple of 16. A row that sees a NaN key gives NaN and
+ * lse = +inf, a NaN value NaN in that element; bytes past a sequence's length are never used.
+ * The workspace is td_decode_workspace_bytes' (which covers it). */
+td_status td_decode_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
+                            const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D,
+                            int block, float scale, int split, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, uint32_t *dev_status, void *stream);
+td_status td_verify_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
+                            const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax,
+                            int D, int block, float scale, int split, void *out, float *lse, void *workspace,
                             size_t workspace_bytes, uint32_t *dev_status, void *stream);
 
 /*
