@@ -13,17 +13,14 @@
 #include <stdint.h>
 
 #include "td_device.cuh"
+#include "td_mma.cuh"
 
 namespace td {
 
-constexpr uint32_t kInfBits = 0x7f800000u;
-
-// |x| as bits for a maximum over finite elements: 0 for NaN and infinities (positive floats
-// order as unsigned integers).
-__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
-  const uint32_t a = __float_as_uint(x) & 0x7fffffffu;
-  return a < kInfBits ? a : 0u;
-}
+// Infinities become NaN, everything else stays: x * 0 is NaN for an infinity and +-0 otherwise.
+// Applied before a maximum (which passes NaN over, so it is taken over finite elements) and before
+// the conversion to e4m3 (which would saturate an infinity).
+__device__ __forceinline__ float2 finite_or_nan(float2 x) { return ffma2(x, make_float2(0.f, 0.f), x); }
 
 // The least power of two s >= 2^-126 with amax <= 448 s (amax as bits, finite). 448 = 1.75 * 2^8:
 // the exponent of s is that of amax less 8, plus one if amax's significand is above 1.75.
@@ -32,14 +29,16 @@ __device__ __forceinline__ float pow2_scale(uint32_t amax_bits) {
   return __uint_as_float((uint32_t)(e < 1 ? 1 : e) << 23);
 }
 
-// Two elements to e4m3 codes (lo in the low byte), each x * inv rounded to nearest even. NaN and
-// infinities become NaN codes: the conversion saturates an infinity, so x * 0 (NaN for both) is
-// added first.
-__device__ __forceinline__ uint16_t quant2_e4m3(float lo, float hi, float inv) {
-  const float a = __fmaf_rn(lo, 0.f, __fmul_rn(lo, inv)), b = __fmaf_rn(hi, 0.f, __fmul_rn(hi, inv));
+// Two values to e4m3 codes (x in the low byte): rounded to nearest even, saturating, NaN kept.
+__device__ __forceinline__ uint16_t to_e4m3x2(float2 v) {
   uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v.y), "f"(v.x));
   return d;
+}
+
+// Two elements to codes of x * inv; infinities become NaN codes.
+__device__ __forceinline__ uint16_t quant2_e4m3(float2 x, float inv) {
+  return to_e4m3x2(fmul2(finite_or_nan(x), make_float2(inv, inv)));
 }
 
 // Two codes to the fp16 pair of their values (exact).
@@ -57,7 +56,8 @@ __device__ __forceinline__ float2 e4m3x2_float2(uint16_t codes) {
 // Four codes of a word brought to another scale: value * r rounded to nearest even.
 __device__ __forceinline__ uint32_t rescale4_e4m3(uint32_t w, float r) {
   const float2 a = e4m3x2_float2((uint16_t)w), b = e4m3x2_float2((uint16_t)(w >> 16));
-  return (uint32_t)quant2_e4m3(a.x, a.y, r) | ((uint32_t)quant2_e4m3(b.x, b.y, r) << 16);
+  const float2 rr = make_float2(r, r);
+  return (uint32_t)to_e4m3x2(fmul2(a, rr)) | ((uint32_t)to_e4m3x2(fmul2(b, rr)) << 16);
 }
 
 }  // namespace td

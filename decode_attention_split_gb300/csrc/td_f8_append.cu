@@ -12,9 +12,14 @@
 // token's rows by the chain of dependent loads (length, then scale and table row).
 //  * rows (T <= kRowsT): one CTA per sequence, a warp per (head, block) or query row, which
 //    advances the length itself once its warps have read it;
-//  * tiles: one CTA per (block, group of heads), the block's rows held in registers between the
-//    maximum and the conversion (128 bytes a thread in flight), so the rows cross once; the
-//    lengths are advanced by a second launch, after every read of them.
+//  * tiles: a team of warps per (block, head) with the block's rows held in registers between the
+//    maximum and the conversion (128 bytes a thread in flight), so the rows cross once; the lengths
+//    are advanced by a second launch, after every read of them. Plain appends take one team per
+//    CTA. A rotation's CTA gathers the block's table rows into shared memory once and turns several
+//    heads by them, fetching each head's rows a round ahead. Measured (GPU time in a graph):
+//    a 4096-token chunk of 8 heads of 128, bf16, 6.0 us (25.2 MB, 4.2 TB/s); an 8000-token chunk
+//    rotated with 24 query heads 29 us (150 MB, 5.1 TB/s), where rotating from the tables in L1,
+//    head by head, took 39; three position axes, 4 x 1531 tokens, 31 us (83).
 #include <math.h>
 
 #include "td_f8.cuh"
@@ -88,12 +93,11 @@ __device__ __forceinline__ void load_n(const E *x, float (&f)[N]) {
 }
 template <typename E, int N>
 __device__ __forceinline__ void store_n(E *y, const float (&f)[N]) {
-  if constexpr (N * sizeof(E) == 16) {
-    uint4 w;
-    E *e = reinterpret_cast<E *>(&w);
-#pragma unroll
-    for (int i = 0; i < N; ++i) store_elem<E>(e + i, f[i]);
-    *reinterpret_cast<uint4 *>(y) = w;
+  if constexpr (N == 8) {
+    *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                               pack_bf16x2(f[6], f[7]));
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<float4 *>(y) = make_float4(f[0], f[1], f[2], f[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) store_elem<E>(y + i, f[i]);
@@ -102,24 +106,50 @@ __device__ __forceinline__ void store_n(E *y, const float (&f)[N]) {
 template <int N>
 __device__ __forceinline__ void store_codes(uint8_t *c, const float (&f)[N], float inv) {
   if constexpr (N == 1) {
-    c[0] = (uint8_t)quant2_e4m3(f[0], 0.f, inv);
+    c[0] = (uint8_t)quant2_e4m3(make_float2(f[0], 0.f), inv);
   } else if constexpr (N == 2) {
-    *reinterpret_cast<uint16_t *>(c) = quant2_e4m3(f[0], f[1], inv);
+    *reinterpret_cast<uint16_t *>(c) = quant2_e4m3(make_float2(f[0], f[1]), inv);
   } else {
+    uint32_t w[N / 4];
 #pragma unroll
     for (int e = 0; e < N; e += 4)
-      *reinterpret_cast<uint32_t *>(c + e) =
-          (uint32_t)quant2_e4m3(f[e], f[e + 1], inv) | ((uint32_t)quant2_e4m3(f[e + 2], f[e + 3], inv) << 16);
+      w[e / 4] = (uint32_t)quant2_e4m3(make_float2(f[e], f[e + 1]), inv) |
+                 ((uint32_t)quant2_e4m3(make_float2(f[e + 2], f[e + 3]), inv) << 16);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint2 *>(c) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t *>(c) = w[0];
   }
 }
+// rope_pair's products on two pairs at a time (the same operations, so the same bits).
 template <int N>
 __device__ __forceinline__ void rotate(float (&lo)[N], float (&hi)[N], const float (&c)[N], const float (&s)[N]) {
+  if constexpr (N == 1) {
+    const float a = lo[0], b = hi[0];
+    rope_pair(a, b, c[0], s[0], lo[0], hi[0]);
+  } else {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float a = lo[e], b = hi[e];
-    rope_pair(a, b, c[e], s[e], lo[e], hi[e]);
+    for (int e = 0; e < N; e += 2) {
+      const float2 a = make_float2(lo[e], lo[e + 1]), b = make_float2(hi[e], hi[e + 1]);
+      const float2 cc = make_float2(c[e], c[e + 1]), ss = make_float2(s[e], s[e + 1]);
+      const float2 y = ffma2(a, cc, fmul2(b, make_float2(-s[e], -s[e + 1]))), z = ffma2(b, cc, fmul2(a, ss));
+      lo[e] = y.x, lo[e + 1] = y.y, hi[e] = z.x, hi[e + 1] = z.y;
+    }
   }
 }
+// The larger of amax and the finite |f|.
+template <int N>
+__device__ __forceinline__ float finite_max(float amax, const float (&f)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) {
+    const float2 z = finite_or_nan(make_float2(f[e], N == 1 ? 0.f : f[e + (N > 1)]));
+    amax = fmaxf(amax, fabsf(z.x));
+    if (N > 1) amax = fmaxf(amax, fabsf(z.y));
+  }
+  return amax;
+}
+// The largest of a warp's amax (not negative, so its bits order as its values).
+__device__ __forceinline__ uint32_t warp_amax(float amax) { return __reduce_max_sync(0xffffffffu, __float_as_uint(amax)); }
 
 // The scale a block takes: its new rows' own, or the older rows' if that is larger.
 __device__ __forceinline__ float block_scale(uint32_t amax, bool held, float s_old) {
@@ -173,7 +203,7 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
     const bool held = r0 > base;
     const float s_old = held ? *scale : 0.f;
     float lo[N], hi[N];
-    uint32_t amax = 0;
+    float big = 0.f;
     for (int r = r0; r < r1; ++r) {
       load_n<E, N>(x + (long long)(r - r0) * D, lo);
       load_n<E, N>(x + (long long)(r - r0) * D + H, hi);
@@ -182,10 +212,9 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
         load_turn<D, N>(p, b, r - L, L, lane * N, c, s);
         rotate<N>(lo, hi, c, s);
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) amax = max(amax, max(finite_abs_bits(lo[e]), finite_abs_bits(hi[e])));
+      big = finite_max<N>(finite_max<N>(big, lo), hi);
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    const uint32_t amax = warp_amax(big);
     const float sn = block_scale(amax, held, s_old);
     const float inv = __fdiv_rn(1.f, sn);
     if (held && sn > s_old) {
@@ -218,15 +247,53 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
 
 // ---- tiles of a block's rows ---------------------------------------------------------------
 
-constexpr int kVecs = 8;  // 16-byte vectors a thread holds
+constexpr int kTilesThreads = 256;
+constexpr int kTilesCtas = 450;  // CTAs a rotation's launch aims for: one and a half waves of two per SM
+constexpr int kVecs = 8;  // 16-byte vectors a thread holds: 128 bytes in flight
+
+// The rotation table of a tile in shared memory: cosines, then sines, of every (row, pair), the
+// pairs of a row in the order that gives a warp's 16-byte reads consecutive addresses (for 8-pair
+// vectors: the first four pairs of every vector, then the last four).
+template <typename E, int D>
+__device__ __forceinline__ int table_at(int row, int i) {
+  constexpr int VE = 16 / sizeof(E);
+  if constexpr (VE == 8) return row * (D / 2) + ((i >> 2) & 1) * (D / 4) + (i >> 3) * 4 + (i & 3);
+  return row * (D / 2) + i;
+}
+
+template <typename E, int D>
+__device__ __forceinline__ void load_table(const float *tab, int sines, int row, int v, float (&c)[16 / sizeof(E)],
+                                           float (&s)[16 / sizeof(E)]) {
+  constexpr int VE = 16 / sizeof(E);
+#pragma unroll
+  for (int e = 0; e < VE; e += 4) {
+    const int at = table_at<E, D>(row, v * VE + e);
+    const float4 cv = *reinterpret_cast<const float4 *>(tab + at);
+    const float4 sv = *reinterpret_cast<const float4 *>(tab + sines + at);
+    c[e] = cv.x, c[e + 1] = cv.y, c[e + 2] = cv.z, c[e + 3] = cv.w;
+    s[e] = sv.x, s[e + 1] = sv.y, s[e + 2] = sv.z, s[e + 3] = sv.w;
+  }
+}
+
+__device__ __forceinline__ void copy_pairs(uint4 (&lo)[kVecs / 2], uint4 (&hi)[kVecs / 2],
+                                           const uint4 (&next_lo)[kVecs / 2], const uint4 (&next_hi)[kVecs / 2]) {
+#pragma unroll
+  for (int k = 0; k < kVecs / 2; ++k) lo[k] = next_lo[k], hi[k] = next_hi[k];
+}
 
 // blockIdx: x the touched block, y the group of heads (K heads, then V heads, then query heads),
-// z the sequence. blockDim.x * kVecs >= rows of a block * vectors of a row.
+// z the sequence. The CTA's warps form teams of `p.team` threads, enough to hold a block's rows of
+// one head (team * kVecs vectors), and the teams take the group's heads in turn. A rotation's
+// table rows are gathered once per CTA, into shared memory.
+// At most 256 threads for bf16 rows, 512 for fp32 ones (blocks of 128 rows of 512 bytes).
 template <typename E, int D, bool ROPE>
-__global__ void __launch_bounds__(512) append_f8_tiles_kernel(const AppendF8 p) {
+__global__ void __launch_bounds__(sizeof(E) == 2 ? 256 : 512, (ROPE ? 2 : 4) * (int)sizeof(__nv_bfloat16) / (int)sizeof(E))
+    append_f8_tiles_kernel(const AppendF8 p) {
   constexpr int VE = 16 / sizeof(E), NV = D / VE, NH = NV / 2, H = D / 2;
+  extern __shared__ __align__(16) float tab[];
   __shared__ uint32_t s_max[2][16];
-  const int b = blockIdx.z, tid = threadIdx.x, threads = blockDim.x;
+  const int b = blockIdx.z, tid = threadIdx.x, threads = p.team;
+  const int team = tid / threads, teams = blockDim.x / threads, tt = tid % threads;
   griddep_wait();
   griddep_launch_dependents();
   const long long L64 = p.seq_lens[b];
@@ -243,100 +310,137 @@ __global__ void __launch_bounds__(512) append_f8_tiles_kernel(const AppendF8 p) 
   const int n = r1 - r0, t0 = r0 - L;
   const int units = 2 * p.Hkv + (ROPE && p.q != nullptr ? p.Hq : 0);
   const int u0 = blockIdx.y * p.per_cta, u1 = min(u0 + p.per_cta, units);
+  const bool held = r0 > base;
+  // a head's tile as pairs of vectors (v, v + D/2) of a row, kVecs / 2 pairs a thread; a rotation's
+  // CTA fetches each head's one round ahead, the first while it gathers its table
+  uint4 lo[kVecs / 2], hi[kVecs / 2];
+  auto fetch = [&](int u, uint4(&x0)[kVecs / 2], uint4(&x1)[kVecs / 2]) {
+    const bool isq = u >= 2 * p.Hkv, isv = !isq && u >= p.Hkv;
+    const long long head = isq ? (long long)b * p.Hq + u - 2 * p.Hkv : (long long)b * p.Hkv + (isv ? u - p.Hkv : u);
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const E *>(isq ? p.q : isv ? p.v_new : p.k_new) +
+                                                     (head * T + t0) * D);
+#pragma unroll
+    for (int k = 0; k < kVecs / 2; ++k) {
+      const int i = tt + k * threads;
+      if (u < u1 && i < n * NH) {
+        const uint4 *row = x + (i / NH) * NV + i % NH;
+        x0[k] = __ldcs(row);
+        x1[k] = __ldcs(row + NH);
+      }
+    }
+  };
+  if constexpr (ROPE) fetch(u0 + team, lo, hi);
+  const int sines = H << p.block_log2;
+  if constexpr (ROPE) {
+    for (int i = tid; i < n * (H / 4); i += blockDim.x) {
+      const int r = i / (H / 4), pair = i % (H / 4) * 4;
+      float c[4], s[4];
+      load_turn<D, 4>(p, b, t0 + r, L, pair, c, s);
+      *reinterpret_cast<float4 *>(tab + table_at<E, D>(r, pair)) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4 *>(tab + sines + table_at<E, D>(r, pair)) = make_float4(s[0], s[1], s[2], s[3]);
+    }
+    __syncthreads();
+  }
   int flip = 0;
-  for (int u = u0; u < u1; ++u) {
+  // rounds of one head per team; the barrier of a round with K or V heads is the whole CTA's
+#pragma unroll 1
+  for (int first = u0; first < u1; first += teams) {
+    const int u = first + team;
+    const bool mine = u < u1;
     const bool isq = u >= 2 * p.Hkv, isv = !isq && u >= p.Hkv;
     const int h = isq ? u - 2 * p.Hkv : isv ? u - p.Hkv : u;
     const long long head = (long long)b * (isq ? p.Hq : p.Hkv) + h;
-    const E *x = static_cast<const E *>(isq ? p.q : isv ? p.v_new : p.k_new) + (head * T + t0) * D;
-    if (ROPE && isq) {
-      E *y = static_cast<E *>(p.q_out) + (head * T + t0) * D;
-      for (int i = tid; i < n * NH; i += threads) {
-        const int r = i / NH, v = i % NH;
-        float lo[VE], hi[VE], c[VE], s[VE];
-        load_n<E, VE>(x + (long long)r * D + v * VE, lo);
-        load_n<E, VE>(x + (long long)r * D + v * VE + H, hi);
-        load_turn<D, VE>(p, b, t0 + r, L, v * VE, c, s);
-        rotate<VE>(lo, hi, c, s);
-        store_n<E, VE>(y + (long long)r * D + v * VE, lo);
-        store_n<E, VE>(y + (long long)r * D + v * VE + H, hi);
-      }
-      continue;
-    }
     uint8_t *codes = (isv ? p.v_codes : p.k_codes) + (head * p.Smax + base) * D;
     float *scale = (isv ? p.v_scales : p.k_scales) + head * p.NB + j;
-    const bool held = r0 > base;
-    const float s_old = held ? *scale : 0.f;
-    // the tile as pairs of vectors (v, v + D/2) of a row: kVecs / 2 pairs a thread
-    uint4 lo[kVecs / 2], hi[kVecs / 2];
-    uint32_t amax = 0;
+    const float s_old = held && mine && !isq ? *scale : 0.f;
+    const int items = mine ? n * NH : 0;
+    uint4 next_lo[kVecs / 2], next_hi[kVecs / 2];
+    if constexpr (!ROPE)
+      fetch(u, lo, hi);
+    else if (first + teams < u1)
+      fetch(u + teams, next_lo, next_hi);
+    if (ROPE && isq) {
+      uint4 *y = reinterpret_cast<uint4 *>(static_cast<E *>(p.q_out) + (head * T + t0) * D);
 #pragma unroll
-    for (int k = 0; k < kVecs / 2; ++k) {
-      const int i = tid + k * threads;
-      if (i < n * NH) {
-        const uint4 *row = reinterpret_cast<const uint4 *>(x + (long long)(i / NH) * D) + i % NH;
-        lo[k] = row[0];
-        hi[k] = row[NH];
+      for (int k = 0; k < kVecs / 2; ++k) {
+        const int i = tt + k * threads;
+        if (i < items) {
+          float a[VE], z[VE], c[VE], s[VE];
+          load_widen<E, VE>(&lo[k], a);
+          load_widen<E, VE>(&hi[k], z);
+          load_table<E, D>(tab, sines, i / NH, i % NH, c, s);
+          rotate<VE>(a, z, c, s);
+          E *row = reinterpret_cast<E *>(y + (i / NH) * NV + i % NH);
+          store_n<E, VE>(row, a);
+          store_n<E, VE>(row + H, z);
+        }
       }
+    }
+    if (ROPE && first >= 2 * p.Hkv) {  // query heads alone in this round: no barrier
+      copy_pairs(lo, hi, next_lo, next_hi);
+      continue;
     }
     // fp32 rows are rotated in place; bf16 rows stay as read (their rotation has more bits than
     // the register holds) and are rotated again for the conversion
+    const int stored = isq ? 0 : items;
+    float big = 0.f;
 #pragma unroll
     for (int k = 0; k < kVecs / 2; ++k) {
-      const int i = tid + k * threads;
-      if (i < n * NH) {
+      const int i = tt + k * threads;
+      if (i < stored) {
         float a[VE], z[VE];
         load_widen<E, VE>(&lo[k], a);
         load_widen<E, VE>(&hi[k], z);
         if (ROPE && !isv) {
           float c[VE], s[VE];
-          load_turn<D, VE>(p, b, t0 + i / NH, L, (i % NH) * VE, c, s);
+          load_table<E, D>(tab, sines, i / NH, i % NH, c, s);
           rotate<VE>(a, z, c, s);
           if constexpr (sizeof(E) == 4) {
             store_n<E, VE>(reinterpret_cast<E *>(&lo[k]), a);
             store_n<E, VE>(reinterpret_cast<E *>(&hi[k]), z);
           }
         }
-#pragma unroll
-        for (int e = 0; e < VE; ++e) amax = max(amax, max(finite_abs_bits(a[e]), finite_abs_bits(z[e])));
+        big = finite_max<VE>(finite_max<VE>(big, a), z);
       }
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    // every thread holds the old scale before one of them writes the new
-    if (threads == 32) {
-      __syncwarp();
-    } else {
+    uint32_t amax = warp_amax(big);
+    if (threads > 32) {
       // two areas in turn: a warp may still read one unit's while another writes the next's
       if ((tid & 31) == 0) s_max[flip][tid >> 5] = amax;
       __syncthreads();
-      for (int w = 0; w < (threads >> 5); ++w) amax = max(amax, s_max[flip][w]);
+#pragma unroll 1
+      for (int w = 0; w < (threads >> 5); ++w) amax = max(amax, s_max[flip][team * (threads >> 5) + w]);
       flip ^= 1;
+    } else {
+      __syncwarp();  // every thread of the team holds the old scale before one writes the new
     }
     const float sn = block_scale(amax, held, s_old);
     const float inv = __fdiv_rn(1.f, sn);
 #pragma unroll
     for (int k = 0; k < kVecs / 2; ++k) {
-      const int i = tid + k * threads;
-      if (i < n * NH) {
+      const int i = tt + k * threads;
+      if (i < stored) {
         float a[VE], z[VE];
         load_widen<E, VE>(&lo[k], a);
         load_widen<E, VE>(&hi[k], z);
         if (ROPE && !isv && sizeof(E) == 2) {
           float c[VE], s[VE];
-          load_turn<D, VE>(p, b, t0 + i / NH, L, (i % NH) * VE, c, s);
+          load_table<E, D>(tab, sines, i / NH, i % NH, c, s);
           rotate<VE>(a, z, c, s);
         }
-        uint8_t *dst = codes + (long long)(r0 - base + i / NH) * D + (i % NH) * VE;
+        uint8_t *dst = codes + (r0 - base + i / NH) * D + (i % NH) * VE;
         store_codes<VE>(dst, a, inv);
         store_codes<VE>(dst + H, z, inv);
       }
     }
-    if (held && sn > s_old) {
+    if (stored > 0 && held && sn > s_old) {
       const float ratio = __fdiv_rn(s_old, sn);
       uint32_t *w = reinterpret_cast<uint32_t *>(codes);
-      for (int i = tid; i < (r0 - base) * (D / 4); i += threads) w[i] = rescale4_e4m3(w[i], ratio);
+#pragma unroll 1
+      for (int i = tt; i < (r0 - base) * (D / 4); i += threads) w[i] = rescale4_e4m3(w[i], ratio);
     }
-    if (tid == 0) *scale = sn;
+    if (stored > 0 && tt == 0) *scale = sn;
+    if constexpr (ROPE) copy_pairs(lo, hi, next_lo, next_hi);
   }
 }
 
@@ -361,15 +465,23 @@ cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
   }
   const int block = 1 << p.block_log2;
   const int vecs = block * D * (int)sizeof(E) / 16;
-  const int threads = vecs / kVecs < 32 ? 32 : vecs / kVecs;
+  p.team = vecs / kVecs < 32 ? 32 : vecs / kVecs;
+  // a rotation's CTAs share their table among several teams and heads; plain appends share nothing
+  const int threads = !ROPE || p.team > kTilesThreads ? p.team : kTilesThreads;
+  const int teams = threads / p.team;
   const int nblk = (p.T + block - 2) / block + 1;
-  // heads of a CTA: enough that the grid is a few waves, so a tile's table rows stay in L1 for
-  // the next head
-  const long long tiles = (long long)nblk * units * p.B;
-  long long per = tiles / 4096;
-  p.per_cta = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+  // heads of a CTA: a round of its teams or more, as long as the grid still fills the GPU
+  const long long tiles = (long long)nblk * p.B;
+  long long per = ROPE ? tiles * units / kTilesCtas / teams * teams : 1;
+  if (per < teams) per = teams;
+  p.per_cta = (int)(per > units ? units : per);
   const int groups = (units + p.per_cta - 1) / p.per_cta;
-  cudaError_t e = launch_pdl(append_f8_tiles_kernel<E, D, ROPE>, dim3(nblk, groups, p.B), dim3(threads), 0, stream, p);
+  const int smem = ROPE ? block * D * (int)sizeof(float) : 0;
+  const void *fn = reinterpret_cast<const void *>(&append_f8_tiles_kernel<E, D, ROPE>);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = launch_pdl(append_f8_tiles_kernel<E, D, ROPE>, dim3(nblk, groups, p.B), dim3(threads), smem, stream, p);
   if (e == cudaSuccess && p.advance)
     e = launch_pdl(advance_f8_kernel, dim3((p.B + 255) / 256), dim3(256), 0, stream, p.seq_lens, p.B, p.T, p.Smax);
   return e;

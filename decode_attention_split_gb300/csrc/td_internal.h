@@ -61,7 +61,7 @@ struct AppendF8 {
   int32_t *seq_lens;
   uint32_t *status;
   int B, Hq, Hkv, T, Smax, NB, block_log2, A, table_rows, advance;
-  int per_cta;  // heads of a CTA (tiles kernel)
+  int per_cta, team;  // tiles kernel: heads of a CTA, threads of a head
 };
 // Longest chunk of new rows that the warp-per-row kernel takes, and its CTA's size.
 constexpr int kF8RowsT = 16;
