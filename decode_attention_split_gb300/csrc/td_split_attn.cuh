@@ -231,11 +231,10 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
   __syncthreads();
 }
 
-// The plan made before the wait for the previous kernel (from lengths that kernel may still
-// have been writing) is kept after the wait if every attended length reads the same now: the
-// plan is a function of those lengths alone. Otherwise it is made again. Either way the
-// status bits come from the lengths as read after the wait. Ends with a __syncthreads.
-static __device__ void confirm_plan(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red) {
+// Whether every attended length reads, after the wait for the previous kernel, as the plan made
+// before it found it (that kernel may still have been writing them); if so, reports the status
+// bits that the reading raises. One decision for the CTA; ends with a barrier.
+static __device__ bool lengths_unchanged(const SplitParams &p, const int *s_len) {
   constexpr int kSeg = (TD_MAX_BATCH + kThreads - 1) / kThreads;
   const int b0 = threadIdx.x * kSeg;
   uint32_t bits = 0;
@@ -245,11 +244,17 @@ static __device__ void confirm_plan(const SplitParams &p, int *s_len, int *s_pre
     const int b = b0 + i;
     if (b < p.B) same = attended_len(p, ld_relaxed(p.seq_lens + b), bits) == s_len[b] && same;
   }
-  if (__syncthreads_and(same)) {
-    if (blockIdx.x == 0) report(p.status, bits);
-    return;
-  }
-  plan_items(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
+  if (!__syncthreads_and(same)) return false;
+  if (blockIdx.x == 0) report(p.status, bits);
+  return true;
+}
+
+// The plan made before the wait for the previous kernel is kept after the wait if every attended
+// length reads the same now: the plan is a function of those lengths alone. Otherwise it is made
+// again. Either way the status bits come from the lengths as read after the wait. Ends with a
+// __syncthreads.
+static __device__ void confirm_plan(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red) {
+  if (!lengths_unchanged(p, s_len)) plan_items(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
 }
 
 // Fused step with advance: the last CTA of the grid to have read the lengths moves every

@@ -413,6 +413,123 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
   return ok;
 }
 
+// The plan of plan_items (chunks of one size, an item per chunk), or, where that leaves CTAs idle,
+// the balanced one: the stages of 128 keys of every group (sequence, kv head, row block), one group
+// after another, cut into equal runs, one run per CTA. Starting and finishing a segment of a group
+// takes a CTA about as long as kSegmentStages stages, so each group counts that many more, ahead
+// of its own (without them the CTAs that hold several short groups end last: 67.5 us instead of
+// 56). s_prefix then counts these units and *s_chunk is minus the run's length. Chunks that are
+// longer than a run by at most a segment's cost are kept (few groups, which they divide evenly; the
+// early-plan kernel, whose groups are at most 1/16 of the CTAs, does not ask).
+// Ragged batch of 32 (256 groups of 1 to 8192 keys, D = 128): one chunk per group 68 us, runs 56.
+constexpr int kSegmentStages = 3;
+
+// Units of a group of L keys.
+__device__ __forceinline__ int group_units(int L) {
+  constexpr int TK = F8Cfg<128>::TK;
+  return L > 0 ? (L + TK - 1) / TK + kSegmentStages : 0;
+}
+
+__device__ void plan_f8(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red) {
+  constexpr int kSeg = (TD_MAX_BATCH + kThreads - 1) / kThreads, TK = F8Cfg<128>::TK;
+  plan_items(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
+  if (p.split > 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = tid * kSeg;
+  const int U = p.Hkv * p.RB, S = *s_chunk;
+  long long seg = 0;
+  int lmax = 0;
+#pragma unroll
+  for (int i = 0; i < kSeg; ++i) {
+    const int b = b0 + i;
+    if (b < p.B) {
+      seg += (long long)group_units(s_len[b]) * U;
+      lmax = max(lmax, s_len[b]);
+    }
+  }
+  long long incl = seg;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  lmax = __reduce_max_sync(0xffffffffu, lmax);
+  if (lane == 31) s_red[warp] = incl;
+  if (lane == 0) s_red[kWarps + warp] = lmax;
+  __syncthreads();
+  long long W = 0, before = incl - seg;
+  int longest = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_red[w];
+    W += s_red[w];
+    longest = max(longest, (int)s_red[kWarps + w]);
+  }
+  const long long run = (W + gridDim.x - 1) / gridDim.x;
+  if (W > 0x7fffffffLL || (min(S, longest) + TK - 1) / TK <= run) return;  // the same in every thread
+#pragma unroll
+  for (int i = 0; i < kSeg; ++i) {
+    const int b = b0 + i;
+    if (b < p.B) {
+      s_prefix[b] = (int)before;
+      before += (long long)group_units(s_len[b]) * U;
+    }
+  }
+  if (tid == 0) {
+    s_prefix[p.B] = (int)W;
+    *s_chunk = -(int)run;
+  }
+  __syncthreads();
+}
+
+// Run by one thread before the wait for the previous kernel: warms L2 with the start of this CTA's
+// first segment, as prefetch_first_item does, on a guess of plan_f8's choice (without its second
+// look at chunks that overshoot the grid). Batches of up to 8 sequences.
+template <int D>
+__device__ void prefetch_first_f8(const SplitParams &p) {
+  constexpr int TK = F8Cfg<D>::TK;
+  if (p.B > 8) return;
+  const int U = p.Hkv * p.RB;
+  long long all = 0, W = 0, items = 0;
+  int len[8], longest = 0;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) len[b] = b < p.B ? attended_len(p, ld_relaxed(p.seq_lens + b), bits) : 0;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    all += len[b];
+    longest = max(longest, len[b]);
+    W += (long long)group_units(len[b]) * U;
+  }
+  const int S = first_chunk_size(p, all, longest);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) items += (long long)((len[b] + S - 1) / S) * U;
+  const long long grown = items > p.p_target ? S * items / p.p_target : S;
+  const long long run = (W + gridDim.x - 1) / gridDim.x;
+  if (p.split > 0 || (min(grown, (long long)longest) + TK - 1) / TK <= run) {
+    prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
+    return;
+  }
+  long long at = blockIdx.x * run;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const int K = group_units(len[b]);
+    if (at >= 0 && at < (long long)K * U) {
+      const int st = max((int)(at % K) - kSegmentStages, 0), kvh = (int)(at / K) / p.RB;
+      prefetch_chunk_l2<D, kWarmF8>(p, b, kvh, st * TK, min((int)(st + run) * TK, len[b]), prefetch_stages(p));
+    }
+    at -= (long long)K * U;
+  }
+}
+
+// The last sequence b with s_prefix[b] <= at.
+__device__ __forceinline__ int sequence_of(const int *s_prefix, int B, int at) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_prefix[mid] <= at) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Persistent kernel over a block-scaled cache: the items, chunks and fused merge of
 // split_attn_mma_kernel. EARLY_PLAN: planned before the wait for the previous kernel and kept if
 // the lengths read the same after it (launched when the plan leaves slots free for that kernel's
@@ -442,14 +559,19 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   }
   uint32_t merge_phase = 0;
   uint32_t seq = 0;
-  if (tid == 0) prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
+  if (tid == 0) {
+    if constexpr (EARLY_PLAN)
+      prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
+    else
+      prefetch_first_f8<D>(p);
+  }
   if constexpr (EARLY_PLAN) plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   if constexpr (EARLY_PLAN)
     confirm_plan(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   else
-    plan_items(p, s_len, s_prefix, &s_chunk, s_red);
+    plan_f8(p, s_len, s_prefix, &s_chunk, s_red);
   const int S = s_chunk;
   const int W = s_prefix[p.B];
   const int rows = p.Hq * p.T;
@@ -460,24 +582,38 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
     if (p.lse != nullptr)
       for (int r = tid; r < rows; r += kThreads) p.lse[(long long)b * rows + r] = -INFINITY;
   }
-  for (int item = blockIdx.x; item < W; item += gridDim.x) {
-    int lo = 0, hi = p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_prefix[mid] <= item) lo = mid; else hi = mid - 1;
-    }
-    const int b = lo;
+  // chunks: items blockIdx.x, + gridDim.x, ...; runs: segments of stages [at, end)
+  const bool runs = !EARLY_PLAN && S < 0;
+  int at = runs ? min((long long)blockIdx.x * -S, (long long)W) : blockIdx.x;
+  const int end = runs ? min((long long)at - S, (long long)W) : W;
+  while (at < end) {
+    const int b = sequence_of(s_prefix, p.B, at);
     const int L = s_len[b];
-    const int NC = (L + S - 1) / S;
-    const int local = item - s_prefix[b];
-    const int c = local % NC;
-    const int rest = local / NC;
-    const int rb = rest % p.RB;
-    const int kvh = rest / p.RB;
-    const int c0 = c * S;
-    const bool ok = stream_chunk_f8<D, NT>(a, smem, s_bars, seq, b, kvh, rb, L, c0, min(c0 + S, L));
+    const int local = at - s_prefix[b];
+    int unit, c, NC, c0, c1;
+    if (runs) {
+      const int K = group_units(L);
+      unit = local / K;
+      const int in = local % K, n = min(end - at, K - in);
+      const int first = at - in + kSegmentStages, last = at - in + K - 1;  // units of the group's stages
+      at += n;
+      if (in + n <= kSegmentStages) continue;  // the run ends ahead of the group's first stage
+      c = (int)blockIdx.x - first / -S;
+      NC = last / -S - first / -S + 1;
+      c0 = max(in - kSegmentStages, 0) * C::TK;
+      c1 = min((in + n - kSegmentStages) * C::TK, L);
+    } else {
+      NC = (L + S - 1) / S;
+      unit = local / NC;
+      c = local % NC;
+      c0 = c * S;
+      c1 = min(c0 + S, L);
+      at += gridDim.x;
+    }
+    const int rb = unit % p.RB, kvh = unit / p.RB;
+    const bool ok = stream_chunk_f8<D, NT>(a, smem, s_bars, seq, b, kvh, rb, L, c0, c1);
     finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
-                                                       rb, c, NC, &s_last, W <= (int)gridDim.x);
+                                                       rb, c, NC, &s_last, !runs && W <= (int)gridDim.x);
     fence_proxy_async_smem();
     __syncthreads();
     if (!ok) break;

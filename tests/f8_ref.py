@@ -86,13 +86,15 @@ def rotate(x, cos, sin):
 
 def attention(q, k, v, lens, scale):
     """The oracle's exact attention and lse over float64 values, and per output the sums its
-    tolerance needs: (out, lse, status, sum_j w_j |v_j|, largest scale * sum_i |q_i k_i|)."""
+    tolerance needs: (out, lse, status, sum_j w_j |v_j| + 2^-21 sum_j |v_j|, largest
+    scale * sum_i |q_i k_i|). v is zero behind the lengths."""
     orc = oracle.load()
     lens = np.ascontiguousarray(lens, np.int32)
     out, lse, st = orc.attention(q, k, v, lens, scale)
     absv, _, _ = orc.attention(q, k, np.abs(v), lens, scale)
     B, Hq, T, _ = q.shape
     G, S = Hq // k.shape[1], k.shape[2]
+    absv = absv + 2.0 ** -21 * np.repeat(np.abs(v).sum(axis=2), G, axis=1)[:, :, None]
     big = np.zeros((B, Hq, T))
     for b in range(B):
         n = min(max(int(lens[b]), 0), S)
@@ -107,11 +109,13 @@ def bounds(out, lse, absv, big, D, n):
 
     A score is a D-term dot product in fp32 (each product exact, at most 2^-23 of the terms' sum of
     magnitudes lost at each of D additions, 2^-22 for the scales and the exponent): off by at most
-    e = (D + 4) 2^-23 big, so a weight by a factor e^(2e). A probability is rounded to fp16 (2^-11;
-    below 2^-21 of the reference, an absolute 2^-32), the sums over n keys run in fp32 (n 2^-24
+    e = (D + 4) 2^-23 big, so a weight by a factor e^(2e). A probability is rounded to fp16, 2^7
+    above its place: by 2^-11 of it, or below fp16's least normal 2^-14 by an absolute 2^-25, which
+    is 2^-32 of the sum of probabilities (the reference key's alone is 2^7). With every key's weight
+    w_j |v_j| + 2^-21 |v_j| in absv, 2^-11 absv covers both. The sums over n keys run in fp32 (n 2^-24
     of the terms' magnitudes, in pieces of a warp's share: n / 4 additions at most), and the output
     is rounded to bf16 (2^-8)."""
     e = (D + 4) * 2.0 ** -23 * big
-    grow = np.expm1(2 * e) + 2.0 ** -11 + n * 2.0 ** -25 + n * 2.0 ** -32
+    grow = np.expm1(2 * e) + 2.0 ** -11 + n * 2.0 ** -25
     return (2.0 ** -8 * np.abs(out) + (1 + 2.0 ** -8) * grow[..., None] * absv + 1e-30,
             e + n * 2.0 ** -25 + 2.0 ** -21 * (1 + np.abs(np.where(np.isfinite(lse), lse, 0.0))))

@@ -360,7 +360,7 @@ def check(td, q, cache, lens, block, scale, split=0):
     tol, ltol = f8_ref.bounds(ref, rlse, absv, big, D, max(max(lens), 1))
     assert np.all(np.abs(out - ref) <= tol), float((np.abs(out - ref) / tol).max())
     none = np.isneginf(rlse)
-    assert np.array_equal(np.isneginf(lse), none) and np.all(np.abs(lse - rlse)[~none] <= ltol[~none])
+    assert np.array_equal(np.isneginf(lse), none) and np.all(np.abs(lse[~none] - rlse[~none]) <= ltol[~none])
 
 
 ATTN = [
@@ -383,6 +383,11 @@ ATTN = [
     (64, 3, 3, 2048, 3, 64, [2048, 1], 112),
     (128, 2, 2, 1, 1, 16, [1, 0], 0),                # a cache of one row
     (128, 24, 8, 600, 1, 64, [(37 * i) % 601 for i in range(40)], 0),
+    # ragged: equal runs of stages that cross from group to group, several groups in one run
+    (128, 16, 8, 4096, 1, 64, [4096, 130, 128, 0, 1, 2999, 640] + [(331 * i) % 1500 for i in range(33)], 0),
+    (64, 24, 8, 5000, 3, 16, [5000, 127, 4097] + [(97 * i) % 700 for i in range(30)], 0),    # 9 rows
+    (128, 32, 8, 6000, 6, 32, [6000, 5, 300, 4500, 77, 1000, 129, 0], 0),                    # 24 rows, a batch of 8
+    (64, 2, 2, 9000, 1, 128, [9000] + [5] * 200, 0),
 ]
 
 
