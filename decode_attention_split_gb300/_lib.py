@@ -2,10 +2,14 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libtd.so")
+
+BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_td_torch.so")
 
 # the exported symbols, as declared in include/td.h
 SYMBOLS = (
@@ -118,6 +122,18 @@ def lib():
                         "`python -m decode_attention_split_gb300.build` first")
                 _lib = _declare(ctypes.CDLL(LIB_PATH))
     return _lib
+
+
+def torch_binding():
+    """The native binding of the f8 calls; raises if it has not been built."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(
+            f"native binding not built ({BINDING_PATH} missing); run "
+            "`python -m decode_attention_split_gb300.build` first")
+    loader = importlib.machinery.ExtensionFileLoader("_td_torch", BINDING_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_td_torch", BINDING_PATH, loader=loader))
+    loader.exec_module(module)
+    return module
 
 
 def check(func: str, status: int) -> None:

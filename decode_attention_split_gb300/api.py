@@ -3,7 +3,9 @@
 Argument marshalling only: shapes and pointers are read off torch tensors, outputs and the
 workspace are allocated with torch when the caller does not pass them, and every step of
 the computation runs in the CUDA library. Nothing falls back to another implementation:
-without the built library, or with tensors off the GPU, the calls raise.
+without the built library, or with tensors off the GPU, the calls raise. The calls on the
+block-scaled cache (f8) do this marshalling in a native module (csrc/td_torch.cpp), the
+others here through ctypes.
 
 For CUDA-graph capture pass ``out`` (and ``lse``), ``workspace`` and ``stream`` explicitly
 and warm the call up once outside the capture.
@@ -17,7 +19,7 @@ import threading
 
 import torch
 
-from ._lib import check, lib
+from ._lib import check, lib, torch_binding
 
 TD_F32, TD_BF16 = 0, 1
 # bits a call ORs into dev_status (see td.h)
@@ -424,64 +426,13 @@ def td_decode_attn_q8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, scale: 
 # ------------------------------------------------------------------ 8-bit cache in blocks (f8)
 
 F8_BLOCKS = (16, 32, 64, 128)
+_f8 = None  # the native binding of these calls (csrc/td_torch.cpp)
 
 
-def _same_device(name: str, first, *rest) -> int:
-    """The CUDA device index all the given tensors are on, contiguous (None is skipped)."""
-    dev = first.get_device()
-    if dev < 0:
-        raise ValueError("td kernels take CUDA tensors")
-    if not first.is_contiguous():
-        raise ValueError("td kernels take contiguous tensors")
-    for t in rest:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            if not t.is_cuda:
-                raise ValueError("td kernels take CUDA tensors")
-            raise ValueError(f"{name}: all tensors must be on one CUDA device and contiguous")
-    return dev
-
-
-def _f8_cache(k_codes, k_scales, v_codes, v_scales, seq_lens, block):
-    """(B, Hkv, Smax, D) of a block-scaled cache, its tensors checked against one another."""
-    if k_codes.dtype is not torch.float8_e4m3fn or v_codes.dtype is not torch.float8_e4m3fn:
-        raise TypeError("codes must be float8_e4m3fn [B, Hkv, Smax, D]")
-    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
-        raise ValueError("codes must be [B, Hkv, Smax, D], K and V alike")
-    if block not in F8_BLOCKS:
-        raise ValueError(f"block must be one of {F8_BLOCKS}")
-    B, Hkv, Smax, D = k_codes.shape
-    if k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32:
-        raise TypeError("scales must be float32")
-    if k_scales.shape != (B, Hkv, -(-Smax // block)) or v_scales.shape != k_scales.shape:
-        raise ValueError("scales must be [B, Hkv, ceil(Smax / block)]")
-    if seq_lens.dtype is not torch.int32 or seq_lens.shape != (B,):
-        raise TypeError("seq_lens must be int32 [B]")
-    return B, Hkv, Smax, D
-
-
-def _check_status_word(dev_status):
-    if dev_status is not None and (dev_status.dtype is not torch.int32 or dev_status.numel() < 1):
-        raise TypeError("dev_status must be an int32 tensor")
-
-
-def _launch_stream(stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _guard(dev: int):
-    return contextlib.nullcontext() if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
-
-
-def _on_stream(stream, dev: int):
-    """Allocations of a call belong to the stream it launches on."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(ptr, device=dev) if ptr else torch.cuda.default_stream(dev)
-    return torch.cuda.stream(stream)
+def _load_f8():
+    global _f8
+    _f8 = torch_binding()
+    return _f8
 
 
 def make_f8_cache(B: int, Hkv: int, Smax: int, D: int, block: int, device=None):
@@ -494,33 +445,13 @@ def make_f8_cache(B: int, Hkv: int, Smax: int, D: int, block: int, device=None):
     return codes[0], scales[0], codes[1], scales[1]
 
 
-def _f8_new_rows(k_new, v_new, B, Hkv, D):
-    if k_new.dim() != 4 or v_new.shape != k_new.shape:
-        raise ValueError("new rows must be [B, Hkv, T, D], K and V alike")
-    T = k_new.shape[2]
-    if k_new.shape != (B, Hkv, T, D):
-        raise ValueError("shape mismatch between new rows and caches")
-    if v_new.dtype is not k_new.dtype:
-        raise TypeError("new rows must share a dtype")
-    return T
-
-
 def td_kv_append_f8(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, advance: bool = True,
                     dev_status=None, stream=None) -> None:
     """Quantise k_new/v_new [B,Hkv,T,D] (float32 or bfloat16) into a block-scaled cache at rows
     seq_lens[b].. (td.h; td_kv_append's rules): codes float8_e4m3fn [B,Hkv,Smax,D], scales float32
     [B,Hkv,ceil(Smax/block)], block 16, 32, 64 or 128."""
-    dev = _same_device("td_kv_append_f8", k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, dev_status)
-    B, Hkv, Smax, D = _f8_cache(k_codes, k_scales, v_codes, v_scales, seq_lens, block)
-    T = _f8_new_rows(k_new, v_new, B, Hkv, D)
-    _check_status_word(dev_status)
-    with _guard(dev):
-        st = lib().td_kv_append_f8(_code(k_new), k_new.data_ptr(), v_new.data_ptr(), k_codes.data_ptr(),
-                                   k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), seq_lens.data_ptr(), B,
-                                   Hkv, T, Smax, D, block, int(bool(advance)), _ptr(dev_status),
-                                   _launch_stream(stream, dev))
-    if st:
-        check("td_kv_append_f8", st)
+    (_f8 or _load_f8()).append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, advance, dev_status,
+                               stream)
 
 
 def td_rope_kv_append_f8(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, cos_t, sin_t,
@@ -530,46 +461,8 @@ def td_rope_kv_append_f8(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq
     way (into q_out, which may be q). Tables float32 [positions, D/2]. Pair i of token t turns by
     table row seq_lens[b]+t, or with positions int32 [B,T,A] by row positions[b,t,axes[i]] (axes int32
     [D/2], None for axis 0): time, height and width of image or video tokens."""
-    dev = _same_device("td_rope_kv_append_f8", k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, cos_t,
-                       sin_t, positions, axes, q, q_out, dev_status)
-    B, Hkv, Smax, D = _f8_cache(k_codes, k_scales, v_codes, v_scales, seq_lens, block)
-    T = _f8_new_rows(k_new, v_new, B, Hkv, D)
-    _check_status_word(dev_status)
-    if cos_t.dtype is not torch.float32 or sin_t.dtype is not torch.float32 or cos_t.dim() != 2 or \
-            cos_t.shape[1] != D // 2 or sin_t.shape != cos_t.shape:
-        raise TypeError("rope tables must be float32 [rows, D/2], alike")
-    A = 0
-    if positions is not None:
-        if positions.dtype is not torch.int32 or positions.dim() != 3 or positions.shape[:2] != (B, T):
-            raise TypeError("positions must be int32 [B, T, axes]")
-        A = positions.shape[2]
-        if axes is not None and (axes.dtype is not torch.int32 or axes.shape != (D // 2,)):
-            raise TypeError("axes must be int32 [D/2]")
-    elif axes is not None:
-        raise ValueError("axes need positions")
-    elif cos_t.shape[0] < Smax:
-        raise TypeError("rope tables must have a row for every cache row")
-    Hq = 0
-    if q is not None:
-        if q.dim() != 4 or q.shape[0] != B or q.shape[2:] != (T, D) or q.dtype is not k_new.dtype:
-            raise ValueError("q must be [B, Hq, T, D] in the new rows' dtype")
-        Hq = q.shape[1]
-        if q_out is None:
-            with _on_stream(stream, dev):
-                q_out = torch.empty_like(q)
-        elif q_out.shape != q.shape or q_out.dtype is not q.dtype:
-            raise TypeError("q_out must match q")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    with _guard(dev):
-        st = lib().td_rope_kv_append_f8(_code(k_new), _ptr(q), _ptr(q_out), Hq, k_new.data_ptr(), v_new.data_ptr(),
-                                        cos_t.data_ptr(), sin_t.data_ptr(), cos_t.shape[0], _ptr(positions), _ptr(axes),
-                                        A, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                        v_scales.data_ptr(), seq_lens.data_ptr(), B, Hkv, T, Smax, D, block,
-                                        int(bool(advance)), _ptr(dev_status), _launch_stream(stream, dev))
-    if st:
-        check("td_rope_kv_append_f8", st)
-    return q_out
+    return (_f8 or _load_f8()).rope_append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, cos_t,
+                                           sin_t, positions, axes, q, q_out, advance, dev_status, stream)
 
 
 def td_kv_read_f8(k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, rows: int | None = None, start=None,
@@ -578,91 +471,8 @@ def td_kv_read_f8(k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, ro
     code * scale: (k_out, v_out) [B,Hkv,rows,D] in dtype (or that of the outputs passed, whose third
     size is then the number of rows). Rows outside the sequence are left as they were, zero in
     outputs made here. Read whole, the outputs are the bfloat16 caches td_prefill_attn takes."""
-    dev = _same_device("td_kv_read_f8", k_codes, k_scales, v_codes, v_scales, seq_lens, start, k_out, v_out, dev_status)
-    B, Hkv, Smax, D = _f8_cache(k_codes, k_scales, v_codes, v_scales, seq_lens, block)
-    _check_status_word(dev_status)
-    if (k_out is None) != (v_out is None):
-        raise ValueError("give both outputs or neither")
-    if k_out is None:
-        shape = (B, Hkv, Smax if rows is None else rows, D)
-        with _on_stream(stream, dev):
-            k_out = torch.zeros(shape, dtype=dtype, device=k_codes.device)
-            v_out = torch.zeros(shape, dtype=dtype, device=k_codes.device)
-    N = k_out.shape[2] if k_out.dim() == 4 else -1
-    if k_out.shape != (B, Hkv, N, D) or v_out.shape != k_out.shape or v_out.dtype is not k_out.dtype:
-        raise ValueError("outputs must be [B, Hkv, rows, D], alike")
-    if rows is not None and rows != N:
-        raise ValueError("rows and the outputs disagree")
-    if start is not None and (start.dtype is not torch.int32 or start.shape != (B,)):
-        raise TypeError("start must be int32 [B]")
-    with _guard(dev):
-        st = lib().td_kv_read_f8(_code(k_out), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                 v_scales.data_ptr(), seq_lens.data_ptr(), _ptr(start), B, Hkv, N, Smax, D, block,
-                                 k_out.data_ptr(), v_out.data_ptr(), _ptr(dev_status), _launch_stream(stream, dev))
-    if st:
-        check("td_kv_read_f8", st)
-    return k_out, v_out
-
-
-def _f8_workspace(dev: int, sp: int, stream, device, key: tuple) -> torch.Tensor:
-    """The zero-filled workspace kept for a (device, stream, call shape), made on first use."""
-    full = (dev, sp, "f8") + key
-    with _ws_lock:
-        ws = _ws_cache.pop(full, None)
-        if ws is not None:
-            _ws_cache[full] = ws  # most recently used last
-    with _on_stream(stream, dev):
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("pass a workspace of its own to a call that is captured in a graph")
-        if ws is None:
-            ws = torch.zeros(max(td_decode_workspace_bytes(*key), 256), dtype=torch.uint8, device=device)
-    return _keep_workspace(full, ws)
-
-
-def _keep_workspace(key: tuple, ws: torch.Tensor) -> torch.Tensor:
-    with _ws_lock:
-        _ws_cache[key] = ws
-        while len(_ws_cache) > _WS_CACHE_MAX:
-            _ws_cache.pop(next(iter(_ws_cache)))
-    return ws
-
-
-def _attn_f8(name, q, T, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse, workspace,
-             dev_status, stream, return_lse):
-    dev = _same_device(name, q, k_codes, k_scales, v_codes, v_scales, seq_lens, out, lse, workspace, dev_status)
-    B, Hkv, Smax, D = _f8_cache(k_codes, k_scales, v_codes, v_scales, seq_lens, block)
-    shape = q.shape
-    if q.dtype is not torch.bfloat16:
-        raise TypeError("q must be bfloat16")
-    if shape[0] != B or shape[-1] != D:
-        raise ValueError("q and cache shapes disagree")
-    _check_status_word(dev_status)
-    Hq = shape[1]
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if out is None or (lse is None and return_lse):
-        with _on_stream(stream, dev):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None and return_lse:
-                lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    if out.shape != shape or out.dtype is not torch.bfloat16:
-        raise TypeError("out must match q")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != shape[:-1]):
-        raise TypeError("lse must be float32 in q's shape without D")
-    with _guard(dev):
-        sp = _launch_stream(stream, dev)
-        if workspace is None:
-            workspace = _f8_workspace(dev, sp, stream, q.device, (B, Hq, Hkv, Smax, D, T, split))
-        elif workspace.dtype is not torch.uint8:
-            raise TypeError("workspace must be a uint8 tensor")
-        st = lib().td_verify_attn_f8(q.data_ptr(), k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                                     v_scales.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, T, Smax, D, block, scale,
-                                     split, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
-                                     _ptr(dev_status), sp)
-    if st:
-        check(name, st)
-    return out if lse is None else (out, lse)
+    return (_f8 or _load_f8()).read(k_codes, k_scales, v_codes, v_scales, seq_lens, block, rows, start, dtype, k_out,
+                                    v_out, dev_status, stream)
 
 
 def td_decode_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, scale: float | None = None,
@@ -671,8 +481,8 @@ def td_decode_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: 
     """Single-token decode over a block-scaled cache: q [B,Hq,D] bf16 -> out [B,Hq,D] (+ lse [B,Hq])."""
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
-    return _attn_f8("td_decode_attn_f8", q, 1, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out,
-                    lse, workspace, dev_status, stream, return_lse)
+    return (_f8 or _load_f8()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
+                                    workspace, dev_status, stream, return_lse)
 
 
 def td_verify_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, scale: float | None = None,
@@ -682,8 +492,8 @@ def td_verify_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: 
     tokens) -> out [B,Hq,T,D] (+ lse [B,Hq,T])."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, T, D]")
-    return _attn_f8("td_verify_attn_f8", q, q.shape[2], k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale,
-                    split, out, lse, workspace, dev_status, stream, return_lse)
+    return (_f8 or _load_f8()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
+                                    workspace, dev_status, stream, return_lse)
 
 
 def td_prefill_attn(q, k_cache, v_cache, seq_lens, scale: float | None = None, out=None, lse=None, dev_status=None,

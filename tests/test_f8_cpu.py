@@ -125,31 +125,87 @@ def test_attention_refuses(lib, kw, expect):
         assert _call(lib.td_decode_attn_f8, tuple(k for k in VERIFY if k != "T"), d, kw) == expect
 
 
-def test_binding_refuses_cpu_tensors():
-    k = torch.zeros(1, 2, 32, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
-    s = torch.zeros(1, 2, 2)
-    n = torch.zeros(1, dtype=torch.int32)
-    x = torch.zeros(1, 2, 1, 64)
-    for call in (lambda: api.td_kv_append_f8(x, x, k, s, k, s, n, 16),
-                 lambda: api.td_rope_kv_append_f8(x, x, k, s, k, s, n, 16, torch.zeros(32, 32), torch.zeros(32, 32)),
-                 lambda: api.td_kv_read_f8(k, s, k, s, n, 16),
-                 lambda: api.td_decode_attn_f8(torch.zeros(1, 4, 64, dtype=torch.bfloat16), k, s, k, s, n, 16)):
-        with pytest.raises(ValueError):
-            call()
+def _args():
+    codes = torch.zeros(1, 2, 32, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    return dict(k_codes=codes, k_scales=torch.zeros(1, 2, 2), v_codes=codes.clone(), v_scales=torch.zeros(1, 2, 2),
+                seq_lens=torch.zeros(1, dtype=torch.int32), block=16)
+
+
+def _calls():
+    """The four calls with arguments that a GPU's tensors would pass."""
+    x, t, q = torch.zeros(1, 2, 1, 64), torch.zeros(32, 32), torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    return {
+        "append": (api.td_kv_append_f8, dict(k_new=x, v_new=x.clone())),
+        "rope": (api.td_rope_kv_append_f8, dict(k_new=x, v_new=x.clone(), cos_t=t, sin_t=t.clone())),
+        "read": (api.td_kv_read_f8, dict()),
+        "decode": (api.td_decode_attn_f8, dict(q=q)),
+        "verify": (api.td_verify_attn_f8, dict(q=q[:, :, None])),
+    }
+
+
+@pytest.mark.parametrize("name", ["append", "rope", "read", "decode", "verify"])
+def test_binding_refuses_cpu_tensors(name):
+    """Shapes and types are checked first: what is left to refuse is the device."""
+    fn, own = _calls()[name]
+    with pytest.raises(ValueError, match="CUDA"):
+        fn(**own, **_args())
 
 
 @pytest.mark.parametrize("change", [
-    dict(block=48), dict(block=32), dict(k_scales=torch.zeros(1, 2, 3)), dict(k_scales=torch.zeros(1, 2, 2).double()),
-    dict(k_codes=torch.zeros(1, 2, 32, 64, dtype=torch.int8)), dict(seq_lens=torch.zeros(1, dtype=torch.int64)),
-    dict(seq_lens=torch.zeros(2, dtype=torch.int32)), dict(v_codes=torch.zeros(1, 2, 16, 64, dtype=torch.float8_e4m3fn)),
+    dict(block=48), dict(block=32), dict(block=16.0), dict(block=None),
+    dict(k_scales=torch.zeros(1, 2, 3)), dict(v_scales=torch.zeros(1, 2, 1)), dict(k_scales=torch.zeros(1, 2, 2).double()),
+    dict(k_codes=torch.zeros(1, 2, 32, 64, dtype=torch.int8)), dict(k_codes=None), dict(k_codes=[1.0]),
+    dict(seq_lens=torch.zeros(1, dtype=torch.int64)), dict(seq_lens=torch.zeros(2, dtype=torch.int32)),
+    dict(v_codes=torch.zeros(1, 2, 16, 64, dtype=torch.float8_e4m3fn)),
+    dict(k_codes=torch.zeros(2, 32, 64, dtype=torch.float8_e4m3fn)),
+    dict(dev_status=torch.zeros(1)), dict(dev_status=torch.zeros(0, dtype=torch.int32)),
 ])
-def test_binding_checks_the_cache(change):
-    codes = torch.zeros(1, 2, 32, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
-    a = dict(k_codes=codes, k_scales=torch.zeros(1, 2, 2), v_codes=codes, v_scales=torch.zeros(1, 2, 2),
-             seq_lens=torch.zeros(1, dtype=torch.int32), block=16)
-    assert api._f8_cache(**a) == (1, 2, 32, 64)
-    with pytest.raises((TypeError, ValueError)):
-        api._f8_cache(**{**a, **change})
+@pytest.mark.parametrize("name", ["append", "rope", "read", "decode", "verify"])
+def test_binding_checks_the_cache(name, change):
+    fn, own = _calls()[name]
+    with pytest.raises((TypeError, ValueError)) as e:
+        fn(**own, **{**_args(), **change})
+    assert "CUDA" not in str(e.value)
+
+
+@pytest.mark.parametrize("name,change", [
+    ("append", dict(v_new=torch.zeros(1, 2, 1, 64).bfloat16())),
+    ("append", dict(k_new=torch.zeros(1, 1, 1, 64), v_new=torch.zeros(1, 1, 1, 64))),
+    ("append", dict(k_new=torch.zeros(1, 2, 64), v_new=torch.zeros(1, 2, 64))),
+    ("append", dict(k_new=torch.zeros(1, 2, 1, 64).half(), v_new=torch.zeros(1, 2, 1, 64).half())),
+    ("rope", dict(cos_t=torch.zeros(31, 32), sin_t=torch.zeros(31, 32))),
+    ("rope", dict(sin_t=torch.zeros(32, 16))),
+    ("rope", dict(axes=torch.zeros(32, dtype=torch.int32))),
+    ("rope", dict(positions=torch.zeros(1, 1, 3))),
+    ("rope", dict(positions=torch.zeros(1, 2, 3, dtype=torch.int32))),
+    ("rope", dict(positions=torch.zeros(1, 1, 3, dtype=torch.int32), axes=torch.zeros(31, dtype=torch.int32))),
+    ("rope", dict(q=torch.zeros(1, 4, 1, 64).bfloat16())),
+    ("rope", dict(q=torch.zeros(1, 4, 2, 64))),
+    ("rope", dict(q_out=torch.zeros(1, 4, 1, 64))),
+    ("rope", dict(q=torch.zeros(1, 4, 1, 64), q_out=torch.zeros(1, 5, 1, 64))),
+    ("read", dict(k_out=torch.zeros(1, 2, 5, 64))),
+    ("read", dict(k_out=torch.zeros(1, 2, 5, 64), v_out=torch.zeros(1, 2, 6, 64))),
+    ("read", dict(k_out=torch.zeros(1, 2, 5, 64), v_out=torch.zeros(1, 2, 5, 64), rows=6)),
+    ("read", dict(rows=0)),
+    ("read", dict(dtype=torch.float16)),
+    ("read", dict(dtype=None)),
+    ("read", dict(start=torch.zeros(1, dtype=torch.int64))),
+    ("decode", dict(q=torch.zeros(1, 4, 64))),
+    ("decode", dict(q=torch.zeros(2, 4, 64, dtype=torch.bfloat16))),
+    ("decode", dict(q=torch.zeros(1, 4, 32, dtype=torch.bfloat16))),
+    ("decode", dict(q=torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16))),
+    ("decode", dict(out=torch.zeros(1, 4, 64))),
+    ("decode", dict(lse=torch.zeros(1, 3))),
+    ("decode", dict(workspace=torch.zeros(64))),
+    ("decode", dict(scale="x")),
+    ("decode", dict(split=1 << 40)),
+    ("verify", dict(q=torch.zeros(1, 4, 64, dtype=torch.bfloat16))),
+])
+def test_binding_checks_the_rest(name, change):
+    fn, own = _calls()[name]
+    with pytest.raises((TypeError, ValueError)) as e:
+        fn(**{**own, **_args(), **change})
+    assert "CUDA" not in str(e.value)
 
 
 def test_binding_names_stand_in_the_package():
