@@ -45,7 +45,8 @@ struct F8Cfg {
   static constexpr int CODE_BYTES = TK * D;     // one code tile
   static constexpr int STAGE_BYTES = 2 * CODE_BYTES;
   static constexpr int RING_BYTES = NST * STAGE_BYTES;
-  static constexpr int SMEM_BYTES = RING_BYTES + 1024;  // + alignment slack
+  static constexpr int Q_BYTES = kMaxTileRows * D * 2;  // query fragments of two or three n tiles
+  static constexpr int SMEM_BYTES = RING_BYTES + Q_BYTES + 1024;  // + alignment slack
   static_assert(CODE_BYTES % 1024 == 0, "code tiles keep the swizzle's 1024-byte alignment");
   static_assert(kWarps * kMaxTileRows * (D + 6) * 4 + (2 + kWarps) * kMaxTileRows * 4 <= RING_BYTES, "combine area fits");
   static_assert((merge_fixed_floats<D, kMaxTileRows>() + part_block_floats(kMaxTileRows, D)) * 4 <= RING_BYTES,
@@ -83,6 +84,12 @@ __device__ __forceinline__ uint32_t ones_of(uint32_t n, int odd) {
   return ((n >> (8 * odd)) & 0x80u ? 0x3c00u : 0u) | ((n >> (8 * odd + 16)) & 0x80u ? 0x3c000000u : 0u);
 }
 
+__device__ __forceinline__ void add_scaled(float (&o)[4], const float (&x)[4], float s) {
+  const float2 a = ffma2(make_float2(x[0], x[1]), make_float2(s, s), make_float2(o[0], o[1]));
+  const float2 b = ffma2(make_float2(x[2], x[3]), make_float2(s, s), make_float2(o[2], o[3]));
+  o[0] = a.x, o[1] = a.y, o[2] = b.x, o[3] = b.y;
+}
+
 // One warp's step over 32 keys (rows kr .. kr+31 of the code tiles kt / vt; keys key0 ..) for the
 // NT * 8 query rows of the block. Fragment orders (mma m16n8k16, g = lane / 4, c = lane % 4):
 //  - scores S^T = K Q^T: ldmatrix gives thread (g, c) codes 4c .. 4c+3 of a 16-dim block of keys g
@@ -93,10 +100,13 @@ __device__ __forceinline__ uint32_t ones_of(uint32_t n, int odd) {
 //    with the middle bytes swapped the two conversions give dim 2g's pair (tile o[2i]) and dim
 //    2g+1's (tile o[2i+1]). o[nt][2i] holds dims 32i + 2g and 32i + 16 + 2g of rows 8 nt + 2c, + 1,
 //    o[nt][2i+1] the dims after them.
+// Query fragments: qn in registers for one n tile; of more, q_mem in shared memory (8 bytes per tile,
+// k step and lane), which leaves the registers to fragments in flight.
 // ksc / vsc: the halves' scales; qs: the rows' score scale (base 2); lim: the rows' visible keys
 // (index 2 nt + e); kend: the sequence's end. MASK: some key lies past a row's limit or the end.
 template <int D, int NT, bool MASK>
-__device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[NT][D / 16][2], uint32_t kt, uint32_t vt, int kr,
+__device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2], const uint2 *q_mem,
+                                               uint32_t kt, uint32_t vt, int kr,
                                                int key0, int kend, const int (&lim)[2 * NT], const float (&qs)[2 * NT],
                                                const float (&ksc)[2], const float (&vsc)[2],
                                                float (&o)[NT][D / 16][4], float (&m_run)[2 * NT],
@@ -110,7 +120,19 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[NT][D / 16][
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) sc[nt][hf][0] = sc[nt][hf][1] = sc[nt][hf][2] = sc[nt][hf][3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < NX; ++i)
+  for (int i = 0; i < NX; ++i) {
+    uint32_t qf[NT][2][2];  // the query fragments of dims 32i .. 32i+31
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        if constexpr (NT == 1) {
+          qf[nt][blk][0] = qn[nt][2 * i + blk][0], qf[nt][blk][1] = qn[nt][2 * i + blk][1];
+        } else {
+          const uint2 w = q_mem[(nt * (D / 16) + 2 * i + blk) * 32 + lane];
+          qf[nt][blk][0] = w.x, qf[nt][blk][1] = w.y;
+        }
+      }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t r[4];  // keys 0-7 / 8-15 of dims 32i .. 32i+15, then of dims 32i+16 .. 32i+31
@@ -120,59 +142,78 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[NT][D / 16][
         const uint32_t ak[4] = {lo_pair(r[2 * blk]), lo_pair(r[2 * blk + 1]), hi_pair(r[2 * blk]),
                                 hi_pair(r[2 * blk + 1])};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt][hf], ak, qn[nt][2 * i + blk][0], qn[nt][2 * i + blk][1]);
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sc[nt][hf], ak, qf[nt][blk][0], qf[nt][blk][1]);
       }
     }
-  float alpha[2 * NT];
-  bool moved = false;
+  }
+  // Online softmax with a lazy reference maximum (see warp_keys16): it moves when some key of the
+  // warp rises more than kMaxGap above its row's, which one vote finds; only then are the rows'
+  // maxima reduced over their 8 lanes and the sums rescaled. The score scales are not negative.
+  float kss[2 * NT][2], top[2 * NT];
+  bool over = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int ri = 2 * nt + e;
-      float mx = -INFINITY;
+      float half_top[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const float kss = ksc[hf] * qs[ri];
+        kss[ri][hf] = ksc[hf] * qs[ri];
+        if constexpr (MASK) {
 #pragma unroll
-        for (int hk = 0; hk < 2; ++hk) {
-          const int key = key0 + 16 * hf + 8 * hk + gid;
-          const float v = !MASK || key < lim[ri] ? sc[nt][hf][2 * hk + e] * kss : -INFINITY;
-          sc[nt][hf][2 * hk + e] = v;
-          mx = fmaxf(mx, v);
+          for (int hk = 0; hk < 2; ++hk) {
+            const int key = key0 + 16 * hf + 8 * hk + gid;
+            sc[nt][hf][2 * hk + e] = key < lim[ri] ? sc[nt][hf][2 * hk + e] * kss[ri][hf] : -INFINITY;
+          }
+          half_top[hf] = fmaxf(sc[nt][hf][e], sc[nt][hf][2 + e]);
+        } else {
+          half_top[hf] = fmaxf(sc[nt][hf][e], sc[nt][hf][2 + e]) * kss[ri][hf];
         }
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      // lazy reference maximum (see warp_keys16): rows with no visible key are never rescaled
-      const bool move = mx > m_run[ri] + kMaxGap;
-      alpha[ri] = move ? exp2_approx(m_run[ri] - mx) : 1.f;
-      if (move) m_run[ri] = mx;
-      moved |= move;
+      top[ri] = fmaxf(half_top[0], half_top[1]);
+      over |= top[ri] > m_run[ri] + kMaxGap;
+    }
+  if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float alpha[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ri = 2 * nt + e;
+        float mx = fmaxf(top[ri], __shfl_xor_sync(0xffffffffu, top[ri], 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const bool move = mx > m_run[ri] + kMaxGap;
+        alpha[e] = move ? exp2_approx(m_run[ri] - mx) : 1.f;
+        if (move) m_run[ri] = mx;
+        l_run[ri] *= alpha[e];
+      }
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        o[nt][t][0] *= alpha[0];
+        o[nt][t][1] *= alpha[1];
+        o[nt][t][2] *= alpha[0];
+        o[nt][t][3] *= alpha[1];
+      }
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int ri = 2 * nt + e;
       const float base = m_run[ri] == -INFINITY ? 0.f : m_run[ri] - kPShift;
-      float ps = 0.f;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int hk = 0; hk < 2; ++hk) {
-          const float pv = exp2_approx(sc[nt][hf][2 * hk + e] - base);
-          sc[nt][hf][2 * hk + e] = pv;
-          ps += pv;
+          float &x = sc[nt][hf][2 * hk + e];
+          x = exp2_approx(MASK ? x - base : fmaf(x, kss[ri][hf], -base));
         }
-      l_run[ri] = l_run[ri] * alpha[ri] + ps;  // this thread's keys; lanes summed at the end
+      // this thread's keys; lanes summed at the end
+      l_run[ri] += (sc[nt][0][e] + sc[nt][0][2 + e]) + (sc[nt][1][e] + sc[nt][1][2 + e]);
     }
-  if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int t = 0; t < D / 16; ++t) {
-        o[nt][t][0] *= alpha[2 * nt];
-        o[nt][t][1] *= alpha[2 * nt + 1];
-        o[nt][t][2] *= alpha[2 * nt];
-        o[nt][t][3] *= alpha[2 * nt + 1];
-      }
-  }
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     // P^T as B operands: keys 2c, 2c+1 (+8) of row 8 nt + g
@@ -240,11 +281,8 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[NT][D / 16][
         float te[4] = {0.f, 0.f, 0.f, 0.f}, to[4] = {0.f, 0.f, 0.f, 0.f};
         mma_f16_16816(te, ae, pb[nt][0], pb[nt][1]);
         mma_f16_16816(to, ao, pb[nt][0], pb[nt][1]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          o[nt][2 * i][y] = fmaf(te[y], vsc[hf], o[nt][2 * i][y]);
-          o[nt][2 * i + 1][y] = fmaf(to[y], vsc[hf], o[nt][2 * i + 1][y]);
-        }
+        add_scaled(o[nt][2 * i], te, vsc[hf]);
+        add_scaled(o[nt][2 * i + 1], to, vsc[hf]);
       }
     }
   }
@@ -292,7 +330,8 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
   // query row 8 nt + g of this block as fp16 B fragments (slots 2c, 2c+1 <- dims 4c, 4c+1; slots
   // 2c+8, 2c+9 <- dims 4c+2, 4c+3), brought to a largest element in [2^14, 2^15); the limits and
   // score scales of rows 8 nt + 2c, + 1
-  uint32_t qn[NT][D / 16][2];
+  uint32_t qn[1][D / 16][2];
+  uint2 *q_mem = reinterpret_cast<uint2 *>(smem + C::RING_BYTES);
   int lim[2 * NT];
   float qs[2 * NT];
 #pragma unroll
@@ -316,18 +355,23 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
     // with an infinity or NaN stay as they are
     const int ex = (int)(top >> 7);
     const int k = top == 0u || ex == 255 ? 0 : min(14 - (ex - 127), 126);
-    const float up = __uint_as_float((uint32_t)(127 + k) << 23), down = __uint_as_float((uint32_t)(127 - k) << 23);
+    // (the sign of the scale goes with the query, so the scores' scales are not negative)
+    const float up = copysignf(__uint_as_float((uint32_t)(127 + k) << 23), p.qscale);
+    const float down = __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       float f[4];
       widen_bf16x2(w[ks].x, f[0], f[1]);
       widen_bf16x2(w[ks].y, f[2], f[3]);
-      qn[nt][ks][0] = pack_f16x2(f[0] * up, f[1] * up);
-      qn[nt][ks][1] = pack_f16x2(f[2] * up, f[3] * up);
+      const uint2 w2 = make_uint2(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up));
+      if constexpr (NT == 1)
+        qn[nt][ks][0] = w2.x, qn[nt][ks][1] = w2.y;
+      else if (warp == ks % kWarps)
+        q_mem[(nt * (D / 16) + ks) * 32 + lane] = w2;
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      qs[2 * nt + e] = p.qscale * __shfl_sync(0xffffffffu, down, 4 * (2 * tig + e));
+      qs[2 * nt + e] = fabsf(p.qscale) * __shfl_sync(0xffffffffu, down, 4 * (2 * tig + e));
       const int lr = 8 * nt + 2 * tig + e, lgr = rb * p.R + lr;
       lim[2 * nt + e] = lr < p.R && lgr < GT ? min(max(L - p.T + lgr % p.T + 1, 0), c1) : 0;
     }
@@ -364,9 +408,9 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
       const float ksc[2] = {__shfl_sync(0xffffffffu, s_mine, 0), __shfl_sync(0xffffffffu, s_mine, 1)};
       const float vsc[2] = {__shfl_sync(0xffffffffu, s_mine, 2), __shfl_sync(0xffffffffu, s_mine, 3)};
       if (key0 + 32 <= lim_all)
-        warp_keys32_f8<D, NT, false>(qn, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
+        warp_keys32_f8<D, NT, false>(qn, q_mem, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
       else
-        warp_keys32_f8<D, NT, true>(qn, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
+        warp_keys32_f8<D, NT, true>(qn, q_mem, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
     }
     consumed = st + 1;
   }
