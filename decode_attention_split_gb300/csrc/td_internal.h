@@ -28,6 +28,8 @@ struct SplitPlan {
   int counters_n;  // completion and slice-merge counters before the fused step's read count in the workspace
   bool q8;       // int8 cache (codes + per-row scales): the quantised-cache kernel
   bool f8;       // block-scaled e4m3 cache: its kernel
+  bool runs;     // its work cut into equal runs of stages instead of chunks
+  bool merge_apart;  // its partials merged by a second launch
   size_t off_part, bytes;  // workspace layout: counters, then partial blocks
 };
 

@@ -415,15 +415,19 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
     const long long by_grid = (p_target + U - 1) / U;
     ns = by_size < by_grid ? by_size : by_grid;
     if (ns < 1) ns = 1;
-    // the block-scaled kernel may cut the keys into equal runs of 128-key stages, one per CTA, that
-    // cross from group to group: a group then meets one CTA more
+    // the block-scaled kernel cuts the keys into equal runs of 128-key stages, one per CTA, that cross
+    // from group to group: a group then meets one CTA more
     if (f8) ns = std::max(ns, std::min(((long long)Smax + 127) / 128, by_grid + 1));
   }
   const long long items_max = (long long)B * U * ns;
   if (items_max >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
+  // the block-scaled kernel counts stages, with a few units more a group, in 32 bits
+  if (f8 && (long long)B * U * ((Smax + 127) / 128 + 8) >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
   plan->mma = mma;
   plan->q8 = q8;
   plan->f8 = f8;
+  plan->runs = f8 && split == 0;
+  plan->merge_apart = f8 && R > 8;
   plan->RP = variant;
   plan->R = R;
   plan->RB = (int)RB;

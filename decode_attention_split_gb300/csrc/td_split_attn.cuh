@@ -69,6 +69,7 @@ struct SplitParams {
   const float *k_scales;
   const float *v_scales;
   int block_log2, n_blocks;
+  int runs, merge_apart;  // e4m3: work cut into equal runs of stages; a second launch merges (td_split_f8.cu)
 };
 
 // Attended length of a sequence whose stored length is `raw`, with the status bits its

@@ -3,8 +3,14 @@
 //
 //   out = sum_j p_j vs_j v_j / sum_j p_j,   p_j = 2^(scale log2(e) ks_j (q . k_j) - m)
 // with codes k_j, v_j and the scales ks_j, vs_j of the blocks that hold row j. The method is the
-// split attention of split_attn_mma_kernel: the plan, the chunks, the L2 warm-up before the wait
-// for the previous kernel and the fused merge are its own.
+// split attention of split_attn_mma_kernel, with the L2 warm-up before the wait for the previous
+// kernel, the partial blocks and the fused merge of that kernel and a plan of its own.
+//
+// Bound by the codes' bytes at few query rows, and by the warps' latency at many. Measured (GPU time
+// in a graph, inputs past L2): 3B-style layer, 32k keys, batch of 8, 80 us, 6.7 TB/s; ragged batch
+// of 32 (277 MB) 48 us; verify chunk of six over 16k keys, batch of 8 (24 rows), 63 us, 4.2 TB/s; one
+// sequence of 32k keys 14.7 us, of 4096 keys in the 360M-style layer 7.3 us (calls this short are a
+// chain of launch, lengths, first stage, ticket and merge).
 //
 // Design:
 //  * Stages of 128 rows of K and V cross by TMA as code tiles (128-byte swizzle for D = 128,
@@ -19,6 +25,9 @@
 //    uniform over each 16-key half of a warp's step: the key scale multiplies the half's scores,
 //    the value scale its p V product, in fp32, on the way into the running sums. Nothing of a
 //    scale reaches the fp16 operands, so any scale is as good as another.
+//  * The CTA that finishes a group's last segment merges its partials (finish_item); blocks of more
+//    than 8 rows are merged by a second launch. Either way no CTA waits for another, so calls on
+//    several streams cannot block one another.
 //  * fp16 has 11 significant bits but a short range: a query row is first brought to a largest
 //    element in [2^14, 2^15) by a power of two (undone with the scores' scale), and probabilities
 //    are kept 2^7 above their usual place (at most 2^15), which puts the least normal fp16 at
@@ -315,6 +324,19 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
     tma_load_3d(dst, &a.kmap, 0, y, zc, bar, policy);
     tma_load_3d(dst + C::CODE_BYTES, &a.vmap, 0, y, zc, bar, policy);
   };
+  // this thread's share of query rows 8 nt + g, asked for ahead of the stages: behind them, in a full
+  // memory system, they took 5 us to come
+  uint2 q[NT][D / 16];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = 8 * nt + gid, gr = rb * p.R + r;
+    const bool valid = r < p.R && gr < GT;
+    const int hq = kvh * p.G + (valid ? gr / p.T : 0), t = valid ? gr % p.T : 0;
+    const uint2 *qrow = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) +
+                                                        (((size_t)b * p.Hq + hq) * p.T + t) * D);
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) q[nt][ks] = valid ? qrow[ks * 4 + tig] : make_uint2(0u, 0u);
+  }
   if (tid == 0) {
     for (int s2 = 0; s2 < min(NST - 1, nstages); ++s2) issue(s2);
   }
@@ -336,18 +358,12 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
   float qs[2 * NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + gid, gr = rb * p.R + r;
-    const bool valid = r < p.R && gr < GT;
-    const int hq = kvh * p.G + (valid ? gr / p.T : 0), t = valid ? gr % p.T : 0;
-    const uint2 *qrow = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) +
-                                                        (((size_t)b * p.Hq + hq) * p.T + t) * D);
-    uint2 w[D / 16];
     uint32_t top = 0;
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      w[ks] = valid ? qrow[ks * 4 + tig] : make_uint2(0u, 0u);
-      top = max(max(top, w[ks].x & 0x7fffu), (w[ks].x >> 16) & 0x7fffu);
-      top = max(max(top, w[ks].y & 0x7fffu), (w[ks].y >> 16) & 0x7fffu);
+      const uint2 w = q[nt][ks];
+      top = max(max(top, w.x & 0x7fffu), (w.x >> 16) & 0x7fffu);
+      top = max(max(top, w.y & 0x7fffu), (w.y >> 16) & 0x7fffu);
     }
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -361,8 +377,8 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       float f[4];
-      widen_bf16x2(w[ks].x, f[0], f[1]);
-      widen_bf16x2(w[ks].y, f[2], f[3]);
+      widen_bf16x2(q[nt][ks].x, f[0], f[1]);
+      widen_bf16x2(q[nt][ks].y, f[2], f[3]);
       const uint2 w2 = make_uint2(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up));
       if constexpr (NT == 1)
         qn[nt][ks][0] = w2.x, qn[nt][ks][1] = w2.y;
@@ -457,15 +473,129 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
   return ok;
 }
 
-// The plan of plan_items (chunks of one size, an item per chunk), or, where that leaves CTAs idle,
-// the balanced one: the stages of 128 keys of every group (sequence, kv head, row block), one group
-// after another, cut into equal runs, one run per CTA. Starting and finishing a segment of a group
-// takes a CTA about as long as kSegmentStages stages, so each group counts that many more, ahead
-// of its own (without them the CTAs that hold several short groups end last: 67.5 us instead of
-// 56). s_prefix then counts these units and *s_chunk is minus the run's length. Chunks that are
-// longer than a run by at most a segment's cost are kept (few groups, which they divide evenly; the
-// early-plan kernel, whose groups are at most 1/16 of the CTAs, does not ask).
-// Ragged batch of 32 (256 groups of 1 to 8192 keys, D = 128): one chunk per group 68 us, runs 56.
+// Four dims of an output row and, with its first, the row's lse.
+template <int D>
+__device__ __forceinline__ void store_row_f8(const SplitParams &p, long long row, int d, float4 A, float M, float Ls) {
+  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + row * D + d;
+  *reinterpret_cast<uint2 *>(o) = make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
+  if (d == 0 && p.lse != nullptr) p.lse[row] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+}
+
+// Leaves a segment's result: the four warps' partials combined, to out and lse if it is its group's
+// only one, else as partial block c for merge_f8_kernel. Block 0's first row carries, in its padding,
+// the number of its group's blocks (also where that is one). Ends with a barrier.
+template <int D, int ROWS>
+__device__ void publish_f8(const SplitParams &p, const float *combine, int b, int kvh, int rb, int c, int NC) {
+  constexpr int D4 = D / 4, RF = part_row_floats(D), CAS = combine_stride<D>();
+  const float *cm = combine, *cl = combine + kWarps * ROWS, *ca = combine + 2 * kWarps * ROWS;
+  const int nv = min(p.R, p.G * p.T - rb * p.R);  // rows of this block that exist
+  const long long g = ((long long)b * p.Hkv + kvh) * p.RB + rb;
+  float *blk = p.ws_part + (g * p.ns_ws + c) * (long long)part_block_floats(p.R, D);
+  if (c == 0 && threadIdx.x == 0) blk[D + 2] = __int_as_float(NC);
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < nv * D4; idx += kThreads) {
+    const int r = idx / D4, d = (idx % D4) * 4;
+    float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cm[w * ROWS + r]);
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = cm[w * ROWS + r];
+      const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+      const float4 v = *reinterpret_cast<const float4 *>(ca + (w * ROWS + r) * CAS + d);
+      Ls = fmaf(cl[w * ROWS + r], f, Ls);
+      A.x = fmaf(v.x, f, A.x), A.y = fmaf(v.y, f, A.y), A.z = fmaf(v.z, f, A.z), A.w = fmaf(v.w, f, A.w);
+    }
+    if (NC == 1) {
+      store_row_f8<D>(p, out_row_of(p, b, kvh, rb, r), d, A, M, Ls);
+    } else {
+      *reinterpret_cast<float4 *>(blk + r * RF + d) = A;
+      if (d == 0) *reinterpret_cast<float2 *>(blk + r * RF + D) = make_float2(Ls > 0.f ? M : -INFINITY, Ls);
+    }
+  }
+  __syncthreads();
+}
+
+// Log-sum-exp merge of the partial blocks that publish_f8 left, one warp per query row of every
+// group of more than one: its lanes hold the blocks' maxima and sums (32 a pass), then four dims of
+// the weighted sum. Launched after the attention for row blocks of more than 8 rows: the CTA that
+// finished such a group last would merge it alone, row after row, while the others have ended
+// (24 rows: 4 us of 5 blocks, 8 of 13, 25 of 38). No CTA waits for another.
+constexpr int kMergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_f8_kernel(const SplitParams p) {
+  constexpr int RF = part_row_floats(D), PER = D / 32;  // PER: dims of a lane
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int g = blockIdx.x, rb = g % p.RB, kvh = g / p.RB % p.Hkv, b = g / p.RB / p.Hkv;
+  if (r >= min(p.R, p.G * p.T - rb * p.R)) return;
+  const int BF = part_block_floats(p.R, D);
+  const float *blk = p.ws_part + (long long)g * p.ns_ws * BF, *row = blk + r * RF;
+  uint32_t bits = 0;
+  const int L = attended_len(p, p.seq_lens[b], bits);
+  const int NC = __float_as_int(__ldcg(blk + D + 2));  // of this call if the sequence has keys
+  if (L == 0 || NC == 1) return;
+  float M = -INFINITY, Ls = 0.f;
+  float acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < NC; c0 += 32) {
+    const int nb = min(32, NC - c0);
+    const float *src = row + (long long)c0 * BF;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < nb) ml = __ldcg(reinterpret_cast<const float2 *>(src + (long long)lane * BF + D));
+    const bool some = ml.y > 0.f;
+    float Mn = some ? fmaxf(M, ml.x) : M;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+    const float base = Mn == -INFINITY ? 0.f : Mn;
+    const float f = some ? exp2f(ml.x - base) : 0.f, a = exp2f(M - base);
+    float ls = some ? ml.y * f : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+    Ls = Ls * a + ls;
+    M = Mn;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= a;
+#pragma unroll 8
+    for (int c = 0; c < nb; ++c) {
+      const float w = __shfl_sync(0xffffffffu, f, c);
+      const float *v = src + (long long)c * BF + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
+        acc[0] = fmaf(x.x, w, acc[0]), acc[1] = fmaf(x.y, w, acc[1]);
+        acc[2] = fmaf(x.z, w, acc[2]), acc[3] = fmaf(x.w, w, acc[3]);
+      } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
+        acc[0] = fmaf(x.x, w, acc[0]), acc[1] = fmaf(x.y, w, acc[1]);
+      }
+    }
+  }
+  const long long orow = out_row_of(p, b, kvh, rb, r);
+  const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + orow * D + lane * PER;
+  if constexpr (PER == 4)
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[orow] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+}
+
+// How work is cut. A split the caller chose: chunks of that size, an item per chunk (plan_items).
+// Else runs: the stages of 128 keys of every group (sequence, kv head, row block), one group after
+// another, cut into equal runs, one per CTA, whatever the lengths. Starting and finishing a segment
+// of a group takes a CTA about as long as kSegmentStages stages, so each group counts that many
+// units more, ahead of its own. Measured, ragged batch of 32 (256 groups of 1 to 8192 keys,
+// D = 128): plan_items' automatic chunks 68 us; runs without those units 68 (the CTAs that hold
+// several short groups end last), with 1, 2, 3, 4 of them 63, 57, 56, 56; 48 once the runs' plan,
+// one pass over the lengths, was made ahead of the wait for the previous kernel (plan_items' rounds
+// took 5 us after it). One sequence of 16384 keys and 8 kv heads: chunks 11.6 us, runs 11.1.
 constexpr int kSegmentStages = 3;
 
 // Units of a group of L keys.
@@ -474,93 +604,66 @@ __device__ __forceinline__ int group_units(int L) {
   return L > 0 ? (L + TK - 1) / TK + kSegmentStages : 0;
 }
 
-__device__ void plan_f8(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red) {
-  constexpr int kSeg = (TD_MAX_BATCH + kThreads - 1) / kThreads, TK = F8Cfg<128>::TK;
-  plan_items(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
-  if (p.split > 0) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b0 = tid * kSeg;
-  const int U = p.Hkv * p.RB, S = *s_chunk;
-  long long seg = 0;
-  int lmax = 0;
-#pragma unroll
-  for (int i = 0; i < kSeg; ++i) {
-    const int b = b0 + i;
-    if (b < p.B) {
-      seg += (long long)group_units(s_len[b]) * U;
-      lmax = max(lmax, s_len[b]);
-    }
+// Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]) and
+// returns the length of a run. report_bits as for plan_items. Ends with a barrier.
+__device__ int plan_runs(const SplitParams &p, int *s_len, int *s_prefix, int *s_red, bool report_bits) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int U = p.Hkv * p.RB, per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
+  int seg = 0;
+  uint32_t bits = 0;
+  for (int b = b0; b < min(b0 + per, p.B); ++b) {
+    const int L = attended_len(p, report_bits ? p.seq_lens[b] : ld_relaxed(p.seq_lens + b), bits);
+    s_len[b] = L;
+    seg += group_units(L) * U;
   }
-  long long incl = seg;
+  if (report_bits && blockIdx.x == 0) report(p.status, bits);
+  int incl = seg;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  lmax = __reduce_max_sync(0xffffffffu, lmax);
+  __syncthreads();  // s_red may still be read by an earlier plan
   if (lane == 31) s_red[warp] = incl;
-  if (lane == 0) s_red[kWarps + warp] = lmax;
   __syncthreads();
-  long long W = 0, before = incl - seg;
-  int longest = 0;
+  int W = 0, before = incl - seg;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_red[w];
     W += s_red[w];
-    longest = max(longest, (int)s_red[kWarps + w]);
   }
-  const long long run = (W + gridDim.x - 1) / gridDim.x;
-  if (W > 0x7fffffffLL || (min(S, longest) + TK - 1) / TK <= run) return;  // the same in every thread
-#pragma unroll
-  for (int i = 0; i < kSeg; ++i) {
-    const int b = b0 + i;
-    if (b < p.B) {
-      s_prefix[b] = (int)before;
-      before += (long long)group_units(s_len[b]) * U;
-    }
+  for (int b = b0; b < min(b0 + per, p.B); ++b) {
+    s_prefix[b] = before;
+    before += group_units(s_len[b]) * U;
   }
-  if (tid == 0) {
-    s_prefix[p.B] = (int)W;
-    *s_chunk = -(int)run;
-  }
+  if (tid == 0) s_prefix[p.B] = W;
   __syncthreads();
+  return max((W + (int)gridDim.x - 1) / (int)gridDim.x, 1);
 }
 
 // Run by one thread before the wait for the previous kernel: warms L2 with the start of this CTA's
-// first segment, as prefetch_first_item does, on a guess of plan_f8's choice (without its second
-// look at chunks that overshoot the grid). Batches of up to 8 sequences.
+// run, as prefetch_first_item does for chunks, on a guess of the lengths. Batches of up to 8.
 template <int D>
-__device__ void prefetch_first_f8(const SplitParams &p) {
+__device__ void prefetch_first_run(const SplitParams &p) {
   constexpr int TK = F8Cfg<D>::TK;
   if (p.B > 8) return;
   const int U = p.Hkv * p.RB;
-  long long all = 0, W = 0, items = 0;
-  int len[8], longest = 0;
+  int len[8], W = 0;
   uint32_t bits = 0;
 #pragma unroll
   for (int b = 0; b < 8; ++b) len[b] = b < p.B ? attended_len(p, ld_relaxed(p.seq_lens + b), bits) : 0;
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
-    all += len[b];
-    longest = max(longest, len[b]);
-    W += (long long)group_units(len[b]) * U;
-  }
-  const int S = first_chunk_size(p, all, longest);
-#pragma unroll
-  for (int b = 0; b < 8; ++b) items += (long long)((len[b] + S - 1) / S) * U;
-  const long long grown = items > p.p_target ? S * items / p.p_target : S;
-  const long long run = (W + gridDim.x - 1) / gridDim.x;
-  if (p.split > 0 || (min(grown, (long long)longest) + TK - 1) / TK <= run) {
-    prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
-    return;
-  }
-  long long at = blockIdx.x * run;
+  for (int b = 0; b < 8; ++b) W += group_units(len[b]) * U;
+  const int run = (W + (int)gridDim.x - 1) / (int)gridDim.x;
+  int at = min(blockIdx.x * (long long)run, (long long)W);
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
     const int K = group_units(len[b]);
-    if (at >= 0 && at < (long long)K * U) {
-      const int st = max((int)(at % K) - kSegmentStages, 0), kvh = (int)(at / K) / p.RB;
-      prefetch_chunk_l2<D, kWarmF8>(p, b, kvh, st * TK, min((int)(st + run) * TK, len[b]), prefetch_stages(p));
+    if (at >= 0 && at < K * U) {
+      const int st = max(at % K - kSegmentStages, 0), kvh = at / K / p.RB;
+      prefetch_chunk_l2<D, kWarmF8>(p, b, kvh, st * TK, min((st + run) * TK, len[b]), prefetch_stages(p));
     }
-    at -= (long long)K * U;
+    at -= K * U;
   }
 }
 
@@ -575,10 +678,8 @@ __device__ __forceinline__ int sequence_of(const int *s_prefix, int B, int at) {
 }
 
 // Persistent kernel over a block-scaled cache: the items, chunks and fused merge of
-// split_attn_mma_kernel. EARLY_PLAN: planned before the wait for the previous kernel and kept if
-// the lengths read the same after it (launched when the plan leaves slots free for that kernel's
-// merging CTAs).
-template <int D, int NT, bool EARLY_PLAN>
+// split_attn_mma_kernel, or runs.
+template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid_constant__ F8Args a) {
   using C = F8Cfg<D>;
   using E = __nv_bfloat16;
@@ -588,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   __shared__ int s_len[TD_MAX_BATCH];
   __shared__ int s_prefix[TD_MAX_BATCH + 1];
   __shared__ long long s_red[2 * kWarps];
-  __shared__ int s_chunk, s_last;
+  __shared__ int s_chunk, s_last, s_sum[kWarps];
   __shared__ __align__(8) uint64_t s_merge_bar;
   __shared__ __align__(8) uint64_t s_bars[NST];
 
@@ -604,19 +705,28 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   uint32_t merge_phase = 0;
   uint32_t seq = 0;
   if (tid == 0) {
-    if constexpr (EARLY_PLAN)
-      prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
+    if (p.runs)
+      prefetch_first_run<D>(p);
     else
-      prefetch_first_f8<D>(p);
+      prefetch_first_item<D, kWarmF8>(p, prefetch_stages(p), blockIdx.x);
   }
-  if constexpr (EARLY_PLAN) plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
+  // the plan is made before the wait for the previous kernel, on the lengths as they read then, and
+  // kept if they read the same after it
+  const bool runs = p.runs;
+  int S = 0;  // keys of a chunk, or units of a run
+  if (runs)
+    S = plan_runs(p, s_len, s_prefix, s_sum, false);
+  else
+    plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
-  if constexpr (EARLY_PLAN)
-    confirm_plan(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
-  else
-    plan_f8(p, s_len, s_prefix, &s_chunk, s_red);
-  const int S = s_chunk;
+  if (!lengths_unchanged(p, s_len)) {
+    if (runs)
+      S = plan_runs(p, s_len, s_prefix, s_sum, true);
+    else
+      plan_items(p, s_len, s_prefix, &s_chunk, s_red);
+  }
+  if (!runs) S = s_chunk;
   const int W = s_prefix[p.B];
   const int rows = p.Hq * p.T;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -627,9 +737,8 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
       for (int r = tid; r < rows; r += kThreads) p.lse[(long long)b * rows + r] = -INFINITY;
   }
   // chunks: items blockIdx.x, + gridDim.x, ...; runs: segments of stages [at, end)
-  const bool runs = !EARLY_PLAN && S < 0;
-  int at = runs ? min((long long)blockIdx.x * -S, (long long)W) : blockIdx.x;
-  const int end = runs ? min((long long)at - S, (long long)W) : W;
+  int at = runs ? min((long long)blockIdx.x * S, (long long)W) : blockIdx.x;
+  const int end = runs ? min((long long)at + S, (long long)W) : W;
   while (at < end) {
     const int b = sequence_of(s_prefix, p.B, at);
     const int L = s_len[b];
@@ -642,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
       const int first = at - in + kSegmentStages, last = at - in + K - 1;  // units of the group's stages
       at += n;
       if (in + n <= kSegmentStages) continue;  // the run ends ahead of the group's first stage
-      c = (int)blockIdx.x - first / -S;
-      NC = last / -S - first / -S + 1;
+      c = (int)blockIdx.x - first / S;
+      NC = last / S - first / S + 1;
       c0 = max(in - kSegmentStages, 0) * C::TK;
       c1 = min((in + n - kSegmentStages) * C::TK, L);
     } else {
@@ -656,8 +765,11 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
     }
     const int rb = unit % p.RB, kvh = unit / p.RB;
     const bool ok = stream_chunk_f8<D, NT>(a, smem, s_bars, seq, b, kvh, rb, L, c0, c1);
-    finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
-                                                       rb, c, NC, &s_last, !runs && W <= (int)gridDim.x);
+    if (p.merge_apart)
+      publish_f8<D, TR>(p, combine, b, kvh, rb, c, NC);
+    else
+      finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
+                                                         rb, c, NC, &s_last, false);
     fence_proxy_async_smem();
     __syncthreads();
     if (!ok) break;
@@ -665,14 +777,10 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
 }
 
 template <int D>
-const void *kernel_of(int nt, bool early) {
-  switch (nt) {
-    case 1:
-      return early ? reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 1, true>)
-                   : reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 1, false>);
-    case 2: return reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 2, false>);
-    default: return reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 3, false>);
-  }
+const void *kernel_of(int nt) {
+  return nt == 1   ? reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 1>)
+         : nt == 2 ? reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 2>)
+                   : reinterpret_cast<const void *>(&split_attn_f8_kernel<D, 3>);
 }
 
 bool encode_code_map(CUtensorMap *m, const void *base, const SplitParams &p, int D) {
@@ -693,6 +801,8 @@ cudaError_t launch(const SplitPlan &plan, const SplitParams &p, cudaStream_t str
   F8Args a;
   if (!encode_code_map(&a.kmap, p.k, p, D) || !encode_code_map(&a.vmap, p.v, p, D)) return cudaErrorInvalidValue;
   a.p = p;
+  a.p.runs = plan.runs;
+  a.p.merge_apart = plan.merge_apart;
   {
     // every instantiation's shared-memory opt-in, once per device
     static std::mutex mu;
@@ -701,19 +811,25 @@ cudaError_t launch(const SplitPlan &plan, const SplitParams &p, cudaStream_t str
     if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[device]) {
-      for (const void *fn : {kernel_of<D>(1, true), kernel_of<D>(1, false), kernel_of<D>(2, false), kernel_of<D>(3, false)}) {
-        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem);
+      for (int nt = 1; nt <= 3; ++nt) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel_of<D>(nt), cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem);
         if (e != cudaSuccess) return e;
       }
       done[device] = true;
     }
   }
   const dim3 grid(plan.grid), block(kThreads);
+  cudaError_t e;
   if (p.R <= 8)
-    return plan.spare ? launch_pdl(split_attn_f8_kernel<D, 1, true>, grid, block, plan.smem, stream, a)
-                      : launch_pdl(split_attn_f8_kernel<D, 1, false>, grid, block, plan.smem, stream, a);
-  if (p.R <= 16) return launch_pdl(split_attn_f8_kernel<D, 2, false>, grid, block, plan.smem, stream, a);
-  return launch_pdl(split_attn_f8_kernel<D, 3, false>, grid, block, plan.smem, stream, a);
+    e = launch_pdl(split_attn_f8_kernel<D, 1>, grid, block, plan.smem, stream, a);
+  else if (p.R <= 16)
+    e = launch_pdl(split_attn_f8_kernel<D, 2>, grid, block, plan.smem, stream, a);
+  else
+    e = launch_pdl(split_attn_f8_kernel<D, 3>, grid, block, plan.smem, stream, a);
+  if (e == cudaSuccess && a.p.merge_apart)
+    e = launch_pdl(merge_f8_kernel<D>, dim3((unsigned)(p.B * p.Hkv * p.RB), (p.R + kMergeWarps - 1) / kMergeWarps),
+                   dim3(kMergeWarps * 32), 0, stream, a.p);
+  return e;
 }
 
 }  // namespace
@@ -721,7 +837,7 @@ cudaError_t launch(const SplitPlan &plan, const SplitParams &p, cudaStream_t str
 const void *f8_kernel(int D, int R, int *smem) {
   const int nt = (R + 7) / 8;
   *smem = D == 64 ? F8Cfg<64>::SMEM_BYTES : F8Cfg<128>::SMEM_BYTES;
-  return D == 64 ? kernel_of<64>(nt, false) : kernel_of<128>(nt, false);
+  return D == 64 ? kernel_of<64>(nt) : kernel_of<128>(nt);
 }
 
 cudaError_t launch_split_f8(int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
