@@ -526,7 +526,7 @@ __device__ void publish_f8(const SplitParams &p, const float *combine, int b, in
 constexpr int kMergeWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) merge_f8_kernel(const SplitParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) merge_f8_kernel(const SplitParams p) {
   constexpr int RF = part_row_floats(D), PER = D / 32;  // PER: dims of a lane
   griddep_wait();
   griddep_launch_dependents();
@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_f8_kernel(const SplitP
   const float *blk = p.ws_part + (long long)g * p.ns_ws * BF, *row = blk + r * RF;
   uint32_t bits = 0;
   const int L = attended_len(p, p.seq_lens[b], bits);
-  const int NC = __float_as_int(__ldcg(blk + D + 2));  // of this call if the sequence has keys
+  // this call's if the sequence has keys and no copy timed out, which leaves a group unpublished
+  const int NC = min(max(__float_as_int(__ldcg(blk + D + 2)), 0), p.ns_ws);
   if (L == 0 || NC == 1) return;
   float M = -INFINITY, Ls = 0.f;
   float acc[PER];

@@ -1,6 +1,7 @@
 """The block-scaled 8-bit cache without a GPU: what the C calls and the binding refuse before any
 launch, and the plain reference against itself."""
 import inspect
+import re
 
 import numpy as np
 import pytest
@@ -221,6 +222,16 @@ def test_make_f8_cache_shapes():
     assert ks.shape == vs.shape == (2, 3, 4) and ks.dtype == torch.float32
     with pytest.raises(ValueError):
         api.make_f8_cache(2, 3, 100, 64, 20, device="cpu")
+
+
+def test_f8_kernels_have_no_spills(lib):
+    """Register gate (ptxas), as for the other kernels."""
+    log = open(td_build.PTXAS_LOG).read()
+    entries = re.findall(r"Compiling entry function '(\w+)'.*?\n(?:.*?\n)*?\s+(\d+) bytes stack frame, (\d+) bytes "
+                         r"spill stores, (\d+) bytes spill loads", log)
+    seen = [n for n, _, st, ld in entries if re.search(r"_f8_|_f8E|merge_f8", n) and (int(st), int(ld)) == (0, 0)]
+    for k, n in (("split_attn_f8_kernel", 6), ("merge_f8_kernel", 2), ("read_f8_kernel", 4), ("append_f8_tiles_kernel", 8)):
+        assert sum(k in x for x in seen) == n, k
 
 
 def test_reference_codes_agree_with_torch():

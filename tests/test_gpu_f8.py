@@ -44,10 +44,13 @@ def rows(rng, *shape, dtype="bf16", spread=1.0):
 
 def filled(rng, B, H, S, D, block, lens=None):
     """A cache as appends leave it (numpy codes, scales), random bytes and NaN scales behind the lengths."""
-    codes = np.zeros((B, H, S, D), np.uint8)
-    scales = np.full((B, H, -(-S // block)), np.nan, np.float32)
-    x = rows(rng, B, H, S, D).double().numpy()
-    f8_ref.append(codes, scales, x, [0] * B, block)
+    NB = -(-S // block)
+    x = np.zeros((B, H, NB * block, D))
+    x[:, :, :S] = rows(rng, B, H, S, D).double().numpy()
+    x = x.reshape(B, H, NB, block, D)
+    m, e = np.frexp(np.abs(x).max(axis=(3, 4)))        # f8_ref.pow2_scale of every block
+    scales = np.ldexp(1.0, e - 9 + (m > 0.875)).astype(np.float32)
+    codes = f8_ref.encode(x / scales[..., None, None]).reshape(B, H, NB * block, D)[:, :, :S].copy()
     if lens is not None:
         for b, L in enumerate(lens):
             L = min(max(int(L), 0), S)
@@ -147,6 +150,15 @@ def test_append_extremes(td, dtype, T):
     f8_ref.append(kc, ks, x.double().numpy(), [0] * B, block)
     assert np.array_equal(d[1].cpu().numpy(), ks)
     assert same_bits(codes_of(d[0]), kc)
+
+
+def test_filled_is_an_append(td):
+    """The tests' caches are what the reference's append stores."""
+    codes, scales = filled(np.random.default_rng(1), 1, 2, 70, 64, 16)
+    x = rows(np.random.default_rng(1), 1, 2, 70, 64).double().numpy()
+    kc, ks = np.zeros_like(codes), np.zeros_like(scales)
+    f8_ref.append(kc, ks, x, [0], 16)
+    assert np.array_equal(kc, codes) and np.array_equal(ks, scales)
 
 
 def test_append_nothing_else_is_written(td):
@@ -384,11 +396,33 @@ ATTN = [
     (128, 2, 2, 1, 1, 16, [1, 0], 0),                # a cache of one row
     (128, 24, 8, 600, 1, 64, [(37 * i) % 601 for i in range(40)], 0),
     # ragged: equal runs of stages that cross from group to group, several groups in one run
-    (128, 16, 8, 4096, 1, 64, [4096, 130, 128, 0, 1, 2999, 640] + [(331 * i) % 1500 for i in range(33)], 0),
-    (64, 24, 8, 5000, 3, 16, [5000, 127, 4097] + [(97 * i) % 700 for i in range(30)], 0),    # 9 rows
-    (128, 32, 8, 6000, 6, 32, [6000, 5, 300, 4500, 77, 1000, 129, 0], 0),                    # 24 rows, a batch of 8
-    (64, 2, 2, 9000, 1, 128, [9000] + [5] * 200, 0),
+    (128, 16, 8, 2048, 1, 64, [2048, 130, 128, 0, 1, 1999, 640] + [(331 * i) % 1500 for i in range(33)], 0),
+    (64, 24, 8, 2000, 3, 16, [2000, 127, 1025] + [(97 * i) % 700 for i in range(30)], 0),    # 9 rows
+    (128, 32, 8, 3000, 6, 32, [3000, 5, 300, 2500, 77, 1000, 129, 0], 0),                    # 24 rows, a batch of 8
+    (64, 2, 2, 3000, 1, 128, [3000] + [5] * 100, 0),
 ]
+
+
+@pytest.mark.parametrize("T", [1, 6])
+def test_captured_attention(td, T):
+    """Captured alone, with its merge, and replayed on changed queries."""
+    rng = np.random.default_rng(20 + T)
+    lens, block = [1500, 40], 64
+    kc, ks = filled(rng, 2, 2, 1500, 128, block, lens)
+    d = [f8(kc), torch.from_numpy(ks).cuda(), f8(kc), torch.from_numpy(ks).cuda(),
+         torch.tensor(lens, dtype=torch.int32, device="cuda")]
+    q = rows(rng, 2, 8, T, 128).cuda()
+    out, ws = torch.empty_like(q), td.make_workspace(2, 8, 2, 1500, 128, T)
+    td.td_verify_attn_f8(q, *d, block, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        td.td_verify_attn_f8(q, *d, block, out=out, workspace=ws)
+    for _ in range(3):
+        q.copy_(rows(rng, 2, 8, T, 128))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, td.td_verify_attn_f8(q, *d, block))
 
 
 @pytest.mark.parametrize("D,Hq,Hkv,S,T,block,lens,split", ATTN)
@@ -637,6 +671,95 @@ def test_two_streams(td):
             o.append(td.td_decode_attn_f8(q, *d, block, stream=s))
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for got in outs for o in got)
+
+
+def test_two_streams_many_rows(td):
+    """Verify chunks of 24 rows that fill the GPU, on two streams at once: neither waits for the other."""
+    rng = np.random.default_rng(16)
+    lens, block = [2048, 1500, 2047], 32
+    kc, ks = filled(rng, 3, 4, 2048, 64, block, lens)
+    d = [f8(kc), torch.from_numpy(ks).cuda(), f8(kc), torch.from_numpy(ks).cuda(),
+         torch.tensor(lens, dtype=torch.int32, device="cuda")]
+    q = rows(rng, 3, 16, 6, 64).cuda()
+    st = status()
+    want, wl = td.td_verify_attn_f8(q, *d, block, return_lse=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(30):
+        for s in streams:
+            outs.append(td.td_verify_attn_f8(q, *d, block, stream=s, return_lse=True, dev_status=st))
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert all(torch.equal(o, want) and torch.equal(l, wl) for o, l in outs)
+
+
+def test_streams_are_taken_as_torch_streams_or_handles(td):
+    rng = np.random.default_rng(17)
+    s = torch.cuda.Stream()
+    x = rows(rng, 2, 2, 20, 64).cuda()
+    torch.cuda.synchronize()
+    got = []
+    for stream in (None, s, s.cuda_stream, 0, torch.cuda.default_stream()):
+        cache = td.make_f8_cache(2, 2, 64, 64, 16)
+        lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        td.td_kv_append_f8(x, x, *cache, lens, 16, stream=stream)
+        k, v = td.td_kv_read_f8(*cache, lens, 16, stream=stream)
+        out = td.td_decode_attn_f8(x[:, :, 0].contiguous(), *cache, lens, 16, stream=stream)
+        torch.cuda.synchronize()
+        got.append((lens, k, v, out))
+    assert got[0][0].tolist() == [20, 20]
+    for g in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(g, got[0]))
+    with pytest.raises((TypeError, ValueError)):
+        td.td_kv_append_f8(x, x, *cache, lens, 16, stream="x")
+
+
+def test_one_workspace_for_calls_of_one_shape(td):
+    """A workspace serves one shape's calls in turn, decode kinds mixed: each leaves it as it found it."""
+    rng = np.random.default_rng(18)
+    B, Hq, Hkv, S, D, block = 3, 32, 4, 900, 128, 16
+    lens = [900, 250, 0]
+    kc, ks = filled(rng, B, Hkv, S, D, block, lens)
+    for T in (1, 3):
+        ws = td.make_workspace(B, Hq, Hkv, S, D, T)
+        q = rows(rng, B, Hq, T, D).cuda()
+        d = [f8(kc), torch.from_numpy(ks).cuda(), f8(kc), torch.from_numpy(ks).cuda()]
+        bf = torch.from_numpy(rng.normal(size=(B, Hkv, S, D))).to(torch.bfloat16).cuda()
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        first = None
+        for _ in range(3):
+            a = td.td_verify_attn_f8(q, *d, n, block, workspace=ws)
+            b = td.td_verify_attn(q, bf, bf, n, workspace=ws, split=0)
+            first = first or (a, b)
+            assert torch.equal(a, first[0]) and torch.equal(b, first[1])
+
+
+def test_largest_batch(td):
+    rng = np.random.default_rng(19)
+    B, Hkv, S, D, block = 1024, 1, 40, 64, 16
+    lens = [(7 * i) % 41 for i in range(B)]
+    kc, ks = filled(rng, B, Hkv, S, D, block, lens)
+    check(td, rows(rng, B, 3, 1, D, spread=0.3), (kc, ks, kc, ks), lens, block, 0.125)
+
+
+def test_misaligned_pointers_are_refused(td):
+    from decode_attention_split_gb300._lib import TDError
+    kc, ks, vc, vs = td.make_f8_cache(1, 2, 64, 64, 16)
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    buf = torch.zeros(2 * 64 + 4, device="cuda")
+    x = buf[1:-3].view(1, 2, 1, 64)
+    y = buf[:-4].view(1, 2, 1, 64)
+    raw = torch.zeros(2 * 64 * 64 + 16, dtype=torch.uint8, device="cuda")
+    odd = raw[8:-8].view(torch.float8_e4m3fn).view(1, 2, 64, 64)
+    for call in (lambda: td.td_kv_append_f8(x, y, kc, ks, vc, vs, lens, 16),
+                 lambda: td.td_kv_append_f8(y, y, odd, ks, vc, vs, lens, 16),
+                 lambda: td.td_kv_read_f8(kc, ks, odd, vs, lens, 16),
+                 lambda: td.td_decode_attn_f8(torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda"), kc, ks, odd, vs, lens, 16)):
+        with pytest.raises(TDError) as e:
+            call()
+        assert e.value.status == 2
 
 
 def test_repeat_calls_are_equal(td):
