@@ -10,16 +10,15 @@
 //
 // Two kernels share the arithmetic. Both are bound by memory: a long chunk by its bytes, a
 // token's rows by the chain of dependent loads (length, then scale and table row).
-//  * rows (T <= kRowsT): one CTA per sequence, a warp per (head, block) or query row, which
-//    advances the length itself once its warps have read it;
+//  * rows (a few rows a sequence, see takes_rows): a warp per (head, block) or query row; where one CTA holds a sequence's
+//    warps, it also advances the length once they have read it;
 //  * tiles: a team of warps per (block, head) with the block's rows held in registers between the
-//    maximum and the conversion (128 bytes a thread in flight), so the rows cross once; the lengths
-//    are advanced by a second launch, after every read of them. Plain appends take one team per
+//    maximum and the conversion (128 bytes a thread in flight), so the rows cross once. Plain appends take one team per
 //    CTA. A rotation's CTA gathers the block's table rows into shared memory once and turns several
 //    heads by them, fetching each head's rows a round ahead. Measured (GPU time in a graph):
 //    a 4096-token chunk of 8 heads of 128, bf16, 6.0 us (25.2 MB, 4.2 TB/s); an 8000-token chunk
 //    rotated with 24 query heads 29 us (150 MB, 5.1 TB/s), where rotating from the tables in L1,
-//    head by head, took 39; three position axes, 4 x 1531 tokens, 31 us (83).
+//    head by head, took 39; three position axes, 4 x 1531 tokens, 30 us (83).
 #include <math.h>
 
 #include "td_f8.cuh"
@@ -164,14 +163,15 @@ __device__ __forceinline__ float block_scale(uint32_t amax, bool held, float s_o
 template <typename E, int D, bool ROPE>
 __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const AppendF8 p) {
   constexpr int N = D / 64, H = D / 2;
-  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int warp = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5), warps = gridDim.y * (blockDim.x >> 5);
   griddep_wait();
   griddep_launch_dependents();
   const long long L64 = p.seq_lens[b];
   const bool fits = L64 >= 0 && L64 + p.T <= p.Smax;
   const int L = (int)L64, T = p.T;
   if (!fits) {
-    if (threadIdx.x == 0) report(p.status, TD_DEV_APPEND_OVERFLOW);
+    if (threadIdx.x == 0 && blockIdx.y == 0) report(p.status, TD_DEV_APPEND_OVERFLOW);
     return;
   }
   const int j0 = L >> p.block_log2, nblk = ((L + T - 1) >> p.block_log2) - j0 + 1;
@@ -203,8 +203,7 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
     const bool held = r0 > base;
     const float s_old = held ? *scale : 0.f;
     float lo[N], hi[N];
-    float big = 0.f;
-    for (int r = r0; r < r1; ++r) {
+    auto load_row = [&](int r) {
       load_n<E, N>(x + (long long)(r - r0) * D, lo);
       load_n<E, N>(x + (long long)(r - r0) * D + H, hi);
       if (ROPE && !isv) {
@@ -212,6 +211,10 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
         load_turn<D, N>(p, b, r - L, L, lane * N, c, s);
         rotate<N>(lo, hi, c, s);
       }
+    };
+    float big = 0.f;
+    for (int r = r0; r < r1; ++r) {
+      load_row(r);
       big = finite_max<N>(finite_max<N>(big, lo), hi);
     }
     const uint32_t amax = warp_amax(big);
@@ -223,15 +226,7 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
       for (int i = lane; i < (r0 - base) * (D / 4); i += 32) w[i] = rescale4_e4m3(w[i], ratio);
     }
     for (int r = r0; r < r1; ++r) {
-      if (r1 - r0 > 1) {  // one row is still in registers
-        load_n<E, N>(x + (long long)(r - r0) * D, lo);
-        load_n<E, N>(x + (long long)(r - r0) * D + H, hi);
-        if (ROPE && !isv) {
-          float c[N], s[N];
-          load_turn<D, N>(p, b, r - L, L, lane * N, c, s);
-          rotate<N>(lo, hi, c, s);
-        }
-      }
+      if (r1 - r0 > 1) load_row(r);  // one row is still in registers
       uint8_t *dst = codes + (long long)(r - base) * D + lane * N;
       store_codes<N>(dst, lo, inv);
       store_codes<N>(dst + H, hi, inv);
@@ -454,14 +449,37 @@ __global__ void advance_f8_kernel(int32_t *seq_lens, int B, int T, int Smax) {
   if (L >= 0 && L + T <= Smax) seq_lens[b] = (int32_t)(L + T);
 }
 
+// Whether T rows of each of `heads` heads (of all sequences) go to the rows kernel. A warp there
+// takes its rows one after another, whatever the number of sequences; the tiles kernel takes a
+// block's rows at once, in more rounds the more heads there are. Measured in us, rows / tiles, 48
+// heads a sequence rotated: 1 sequence T = 1 3.2 / 3.4, T = 4 5.2 / 3.8; 24 sequences T = 4 5.3 / 7.0,
+// T = 8 8.1 / 7.3; 64 sequences T = 12 11.2 / 12, T = 16 16.5 / 12.8. 16 heads, plain: 1 sequence T = 4
+// 3.1 / 3.5, T = 8 3.6 / 3.3; 64 sequences T = 8 3.9 / 5.3, T = 16 4.8 / 5.6.
+bool takes_rows(bool rope, int T, long long heads) {
+  return T <= kF8RowsT && T <= (rope ? 1 + heads / 240 : 4 + heads / 50);
+}
+
+cudaError_t launch_advance(const AppendF8 &p, cudaStream_t stream) {
+  return launch_pdl(advance_f8_kernel, dim3((p.B + 255) / 256), dim3(256), 0, stream, p.seq_lens, p.B, p.T, p.Smax);
+}
+
 template <typename E, int D, bool ROPE>
 cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
   AppendF8 p = args;
   const int units = 2 * p.Hkv + (p.q != nullptr ? p.Hq : 0);
-  if (p.T <= kF8RowsT) {
-    const int most = 2 * p.Hkv + (p.q != nullptr ? p.Hq * p.T : 0);  // warps with work, one block touched
-    const int threads = 32 * (most > kF8RowsThreads / 32 ? kF8RowsThreads / 32 : most);
-    return launch_pdl(append_f8_rows_kernel<E, D, ROPE>, dim3(p.B), dim3(threads), 0, stream, p);
+  if (takes_rows(ROPE, p.T, (long long)p.B * units)) {
+    // warps with work (one block touched). A CTA that holds them all in one round can advance the
+    // length; else they spread over CTAs of 8 and a second launch advances (32 sequences, one token,
+    // 16 K/V and 32 query heads: 4.1 us in one CTA a sequence, 3.2 in six, 4.0 with the second launch)
+    const long long work = 2 * p.Hkv + (p.q != nullptr ? (long long)p.Hq * p.T : 0);
+    const bool apart = p.advance && work > kF8RowsThreads / 32;
+    const int warps = (int)(p.advance && !apart ? work : work > 8 ? 8 : work);
+    const long long spread = p.advance && !apart ? 1 : (work + warps - 1) / warps;
+    if (apart) p.advance = 0;
+    cudaError_t e = launch_pdl(append_f8_rows_kernel<E, D, ROPE>, dim3(p.B, (unsigned)(spread > 1024 ? 1024 : spread)),
+                               dim3(32 * warps), 0, stream, p);
+    if (e == cudaSuccess && apart) e = launch_advance(p, stream);
+    return e;
   }
   const int block = 1 << p.block_log2;
   const int vecs = block * D * (int)sizeof(E) / 16;
@@ -474,16 +492,16 @@ cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
   const long long tiles = (long long)nblk * p.B;
   long long per = ROPE ? tiles * units / kTilesCtas / teams * teams : 1;
   if (per < teams) per = teams;
-  p.per_cta = (int)(per > units ? units : per);
-  const int groups = (units + p.per_cta - 1) / p.per_cta;
+  int groups = per >= units ? 1 : (int)((units + per - 1) / per);
+  p.per_cta = ((units + groups - 1) / groups + teams - 1) / teams * teams;  // the groups alike
+  groups = (units + p.per_cta - 1) / p.per_cta;
   const int smem = ROPE ? block * D * (int)sizeof(float) : 0;
   const void *fn = reinterpret_cast<const void *>(&append_f8_tiles_kernel<E, D, ROPE>);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
     e = launch_pdl(append_f8_tiles_kernel<E, D, ROPE>, dim3(nblk, groups, p.B), dim3(threads), smem, stream, p);
-  if (e == cudaSuccess && p.advance)
-    e = launch_pdl(advance_f8_kernel, dim3((p.B + 255) / 256), dim3(256), 0, stream, p.seq_lens, p.B, p.T, p.Smax);
+  if (e == cudaSuccess && p.advance) e = launch_advance(p, stream);
   return e;
 }
 

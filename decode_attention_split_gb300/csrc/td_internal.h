@@ -65,8 +65,8 @@ struct AppendF8 {
   int B, Hq, Hkv, T, Smax, NB, block_log2, A, table_rows, advance;
   int per_cta, team;  // tiles kernel: heads of a CTA, threads of a head
 };
-// Longest chunk of new rows that the warp-per-row kernel takes, and its CTA's size.
-constexpr int kF8RowsT = 16;
+// Longest chunk of new rows that the warp-per-head kernel takes, and its largest CTA.
+constexpr int kF8RowsT = 12;
 constexpr int kF8RowsThreads = 1024;
 cudaError_t launch_append_f8(size_t elem_bytes, int D, const AppendF8 &p, cudaStream_t stream);
 

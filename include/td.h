@@ -295,8 +295,8 @@ td_status td_verify_attn_q8(const void *q, const int8_t *k_codes, const float *k
  */
 
 /* td_kv_append for an f8 cache (new rows [B, Hkv, T, D] of dtype TD_F32 or TD_BF16): the same
- * overflow rule, advance and status bit; 16-byte aligned rows and codes. One launch, and for
- * T > 16 with advance a second one that moves the lengths. */
+ * overflow rule, advance and status bit; 16-byte aligned rows and codes. One launch, or with
+ * advance two (the second moves the lengths, unless a few rows' CTA does it itself). */
 td_status td_kv_append_f8(td_dtype dtype, const void *k_new, const void *v_new, void *k_codes, float *k_scales,
                           void *v_codes, float *v_scales, int32_t *seq_lens, int B, int Hkv, int T, int Smax, int D,
                           int block, int advance, uint32_t *dev_status, void *stream);

@@ -81,6 +81,9 @@ APPEND = [
     ("f32", 128, 128, 200, 500, [0, 100, 300, 301]),
     ("f32", 64, 16, 33, 200, [0, 31]),
     ("bf16", 64, 128, 40, 512, [120, 128, 0]),
+    ("bf16", 128, 32, 4, 128, [0, 30, 124, 125]),                    # the most rows of the first kernel for few heads
+    ("f32", 128, 16, 12, 64, [(5 * i) % 53 for i in range(70)]),     # and for many
+    ("bf16", 64, 64, 13, 64, [(5 * i) % 53 for i in range(70)]),
 ]
 
 
@@ -196,6 +199,8 @@ ROPE = [
     ("bf16", 64, 128, 33, [120, 0], 16),
     ("f32", 64, 16, 50, [9, 0], 1),
     ("f32", 128, 128, 20, [127, 5], 3),
+    ("bf16", 128, 16, 2, [5, 15], 0),
+    ("bf16", 64, 64, 12, [(11 * i) % 200 for i in range(270)], 2),   # many heads: the first kernel's longest chunk
 ]
 
 
