@@ -5,7 +5,7 @@
 //   s    = max(s_old, c) if the block already holds rows below L, else c
 //   older codes of the block: code * (s_old / s), rounded, if s > s_old
 //   new codes: x * (1 / s), rounded to nearest even (NaN and infinities: NaN)
-// The rotation (td_rope.cuh's pairs, in fp32) is quantised directly from fp32: one rounding.
+// The rotation is quantised directly from fp32 (one rounding into e4m3, none into bf16 before it).
 // Pair i of token t turns by the table row L + t, or by positions[b, t, axes[i]].
 //
 // Two kernels share the arithmetic. Both are bound by memory: a long chunk by its bytes, a
@@ -136,6 +136,24 @@ __device__ __forceinline__ void rotate(float (&lo)[N], float (&hi)[N], const flo
     }
   }
 }
+// The keys' rotation: y = x0 c - x1 s, z = x1 c + x0 s with every product and sum rounded by itself, so
+// the codes are those of the plain formula in fp32, bit for bit, whoever evaluates it.
+template <int N>
+__device__ __forceinline__ void rotate_keys(float (&lo)[N], float (&hi)[N], const float (&c)[N], const float (&s)[N]) {
+  if constexpr (N == 1) {
+    const float a = lo[0], b = hi[0];
+    lo[0] = __fadd_rn(__fmul_rn(a, c[0]), -__fmul_rn(b, s[0]));
+    hi[0] = __fadd_rn(__fmul_rn(b, c[0]), __fmul_rn(a, s[0]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const float2 a = make_float2(lo[e], lo[e + 1]), b = make_float2(hi[e], hi[e + 1]);
+      const float2 cc = make_float2(c[e], c[e + 1]), ss = make_float2(s[e], s[e + 1]);
+      const float2 y = ffma2(fmul2(b, ss), make_float2(-1.f, -1.f), fmul2(a, cc)), z = fadd2(fmul2(b, cc), fmul2(a, ss));
+      lo[e] = y.x, lo[e + 1] = y.y, hi[e] = z.x, hi[e + 1] = z.y;
+    }
+  }
+}
 // The larger of amax and the finite |f|.
 template <int N>
 __device__ __forceinline__ float finite_max(float amax, const float (&f)[N]) {
@@ -209,7 +227,7 @@ __global__ void __launch_bounds__(kF8RowsThreads) append_f8_rows_kernel(const Ap
       if (ROPE && !isv) {
         float c[N], s[N];
         load_turn<D, N>(p, b, r - L, L, lane * N, c, s);
-        rotate<N>(lo, hi, c, s);
+        rotate_keys<N>(lo, hi, c, s);
       }
     };
     float big = 0.f;
@@ -389,7 +407,7 @@ __global__ void __launch_bounds__(sizeof(E) == 2 ? 256 : 512, (ROPE ? 2 : 4) * (
         if (ROPE && !isv) {
           float c[VE], s[VE];
           load_table<E, D>(tab, sines, i / NH, i % NH, c, s);
-          rotate<VE>(a, z, c, s);
+          rotate_keys<VE>(a, z, c, s);
           if constexpr (sizeof(E) == 4) {
             store_n<E, VE>(reinterpret_cast<E *>(&lo[k]), a);
             store_n<E, VE>(reinterpret_cast<E *>(&hi[k]), z);
@@ -421,7 +439,7 @@ __global__ void __launch_bounds__(sizeof(E) == 2 ? 256 : 512, (ROPE ? 2 : 4) * (
         if (ROPE && !isv && sizeof(E) == 2) {
           float c[VE], s[VE];
           load_table<E, D>(tab, sines, i / NH, i % NH, c, s);
-          rotate<VE>(a, z, c, s);
+          rotate_keys<VE>(a, z, c, s);
         }
         uint8_t *dst = codes + (r0 - base + i / NH) * D + (i % NH) * VE;
         store_codes<VE>(dst, a, inv);

@@ -303,7 +303,9 @@ td_status td_kv_append_f8(td_dtype dtype, const void *k_new, const void *v_new, 
 
 /*
  * td_rope_kv_append for an f8 cache: the keys (and, when q is given, the query rows of q_out,
- * which may be q) are rotated in fp32 first; the keys go from there into codes with one rounding.
+ * which may be q, as td_rope_kv_append gives them) are rotated first. The keys' rotation is
+ *   x[i] cos - x[i + D/2] sin,   x[i + D/2] cos + x[i] sin
+ * in fp32, each product and sum rounded to nearest even, and goes from there into codes.
  * Pair i of token t turns by the angle in row P of cos_t / sin_t, fp32 [table_rows, D/2]:
  *   positions NULL: P = L + t, the token's cache row (table_rows >= Smax);
  *   else            P = positions[b, t, axes[i]], positions int32 [B, T, n_axes], axes int32 [D/2]

@@ -84,6 +84,14 @@ def rotate(x, cos, sin):
     return np.concatenate([lo * cos - hi * sin, hi * cos + lo * sin], axis=-1)
 
 
+def rotate_keys(x, cos, sin):
+    """The keys' rotation as td.h states it: every product and sum rounded to fp32."""
+    h = x.shape[-1] // 2
+    lo, hi = x[..., :h].astype(np.float32), x[..., h:].astype(np.float32)
+    cos, sin = cos.astype(np.float32), sin.astype(np.float32)
+    return np.concatenate([lo * cos - hi * sin, hi * cos + lo * sin], axis=-1)
+
+
 def attention(q, k, v, lens, scale):
     """The oracle's exact attention and lse over float64 values, and per output the sums its
     tolerance needs: (out, lse, status, sum_j w_j |v_j| + 2^-21 sum_j |v_j|, largest

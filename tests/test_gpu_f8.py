@@ -243,22 +243,15 @@ def test_rope_append(td, dtype, D, block, T, lens, A, inplace):
     u = torch.finfo(DT[dtype]).eps / 2
     tol = u * np.abs(want) * (1 + 2.0 ** -10) + (1 + u) * 2.0 ** -22 * np.concatenate([pair, pair], -1)
     assert np.all(np.abs(got.double().cpu().numpy() - want) <= tol)
-    # keys: the same fp32 error, then half a step of e4m3 under the block's scale
-    y = f8_ref.rotate(kn.double().numpy(), c, s)
+    # keys: the fp32 formula's codes bit for bit, and so within its error and half a step of the exact
+    # rotation
+    exact = f8_ref.rotate(kn.double().numpy(), c, s)
+    y = f8_ref.rotate_keys(kn.double().numpy(), c, s)
     kp = np.hypot(*np.split(kn.double().numpy(), 2, axis=-1))
-    err = 2.0 ** -22 * np.concatenate([kp, kp], -1)
-    kc2, ks2 = kc.copy(), ks.copy()
-    f8_ref.append(kc2, ks2, y, lens, block)
-    sg, cg = d[1].cpu().numpy(), codes_of(d[0])
-    assert np.array_equal(sg, ks2, equal_nan=True)
-    for b, L in enumerate(lens):
-        v = f8_ref.values(cg[b:b + 1], sg[b:b + 1], block)[0, :, L:L + T]
-        sc = np.repeat(sg[b], block, axis=1)[:, L:L + T, None]
-        assert np.all(np.abs(v - y[b]) <= 2.0 ** -4 * np.abs(y[b]) + 2.0 ** -10 * sc + 1.1 * err[b])
-        # away from ties the codes are the reference's
-        assert np.mean(cg[b, :, L:L + T] != kc2[b, :, L:L + T]) < 1e-3
-        # older rows and everything behind: as an append leaves them
-        assert np.array_equal(cg[b, :, :L], kc2[b, :, :L]) and np.array_equal(cg[b, :, L + T:], kc2[b, :, L + T:])
+    assert np.all(np.abs(y - exact) <= 2.0 ** -22 * np.concatenate([kp, kp], -1))
+    f8_ref.append(kc, ks, y.astype(np.float64), lens, block)
+    assert np.array_equal(d[1].cpu().numpy(), ks, equal_nan=True)
+    assert np.array_equal(codes_of(d[0]), kc)
 
 
 @pytest.mark.parametrize("T", [1, 20])
@@ -286,12 +279,10 @@ def test_rope_append_bad_positions(td, T):
                                   block, cos.cuda(), sin.cuda(), positions=pos.cuda(), axes=axes.cuda(), dev_status=st)
     torch.cuda.synchronize()
     assert out is None and int(st.item()) == td.DEV_BAD_POSITION
-    y = f8_ref.rotate(kn.double().numpy(), c, s)
-    sg = ks.cpu().numpy()
-    v = f8_ref.values(codes_of(kc), sg, block)[:, :, :T]
-    sc = np.repeat(sg, block, axis=2)[:, :, :T, None]
-    err = 2.0 ** -21 * np.abs(kn.double().numpy()).max()
-    assert np.all(np.abs(v - y) <= 2.0 ** -4 * np.abs(y) + 2.0 ** -10 * sc + err)
+    rc, rs = np.zeros((B, H, S, D), np.uint8), np.zeros((B, H, S // block), np.float32)
+    y = f8_ref.rotate_keys(kn.double().numpy(), c, s)
+    f8_ref.append(rc, rs, y.astype(np.float64), [0] * B, block)
+    assert np.array_equal(codes_of(kc), rc) and np.array_equal(ks.cpu().numpy(), rs)
 
 
 # ------------------------------------------------------------------------------ read-back
