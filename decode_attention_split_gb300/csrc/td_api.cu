@@ -341,7 +341,7 @@ td_status append_f8(td_dtype dtype, const void *q, void *q_out, int Hq, const vo
       v_scales == nullptr || seq_lens == nullptr)
     return TD_ERR_INVALID_ARG;
   if (B < 1 || Hkv < 1 || T < 1 || Smax < 1 || (q != nullptr && Hq < 1)) return TD_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || block_log2(block) < 0 || B > 65535 || T > Smax || Smax > (1 << 30) ||
+  if ((D != 64 && D != 128) || block_log2(block) < 0 || B > 65535 || T > (1 << 30) || Smax > (1 << 30) ||
       Hkv > 16384 || (q != nullptr && Hq > 16384))
     return TD_ERR_UNSUPPORTED;
   if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(k_scales) ||

@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   const int rows = p.Hq * p.T;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (s_len[b] != 0) continue;
-    for (int idx = tid; idx < rows * D; idx += kThreads)
+    for (long long idx = tid; idx < (long long)rows * D; idx += kThreads)
       store_elem<E>(static_cast<E *>(p.out) + (long long)b * rows * D + idx, 0.f);
     if (p.lse != nullptr)
       for (int r = tid; r < rows; r += kThreads) p.lse[(long long)b * rows + r] = -INFINITY;

@@ -39,7 +39,8 @@ APPEND = ("dtype", "kn", "vn", "kc", "ks", "vc", "vs", "sl", "B", "Hkv", "T", "S
     (dict(sl=None), INVALID),
     (dict(T=0), INVALID),
     (dict(B=0), INVALID),
-    (dict(T=65), UNSUPPORTED),
+    (dict(T=(1 << 30) + 1), UNSUPPORTED),
+    (dict(Smax=(1 << 30) + 1), UNSUPPORTED),
     (dict(D=96), UNSUPPORTED),
     (dict(block=8), UNSUPPORTED),
     (dict(block=48), UNSUPPORTED),

@@ -81,6 +81,8 @@ APPEND = [
     ("f32", 128, 128, 200, 500, [0, 100, 300, 301]),
     ("f32", 64, 16, 33, 200, [0, 31]),
     ("bf16", 64, 128, 40, 512, [120, 128, 0]),
+    ("bf16", 64, 16, 70, 64, [0, 3]),                                # longer than the cache: nothing fits
+    ("bf16", 64, 16, 9, 8, [0, -1]),
     ("bf16", 128, 32, 4, 128, [0, 30, 124, 125]),                    # the most rows of the first kernel for few heads
     ("f32", 128, 16, 12, 64, [(5 * i) % 53 for i in range(70)]),     # and for many
     ("bf16", 64, 64, 13, 64, [(5 * i) % 53 for i in range(70)]),
