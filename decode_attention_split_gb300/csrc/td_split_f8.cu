@@ -599,47 +599,70 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) merge_f8_kernel(const Spl
 // took 5 us after it). One sequence of 16384 keys and 8 kv heads: chunks 11.6 us, runs 11.1.
 constexpr int kSegmentStages = 3;
 
+// A run that ends inside a group costs the merge of its pieces, about kMergeStages stages; and once
+// memory is what bounds the call, CTAs that read for a quarter longer cost less than the CTAs that
+// have nothing to read seem to. So each CTA takes whole groups while the longest is no longer than
+// an equal run with that much more (over two rounds of CTAs: the merge alone; in more rounds, 1024
+// groups of 1024 keys, whole groups took 52.5 us and runs 49.2). Measured, runs / whole groups, D =
+// 128, 8 kv heads: one sequence of 256 keys 7.0 / 5.2 us, of 512 7.1 / 6.5, of 768 7.1 / 8.1; 32
+// sequences of 512 keys 15.9 / 11.6, of 2048 27.9 / 25.3, of 8192 83.2 / 79.9; 8 of 1024 11.0 / 12.2;
+// 20 of 4096 33.1 / 34.8. 5 kv heads, D = 64: 64 sequences (two rounds) of 256 12.5 / 10.8, of 512
+// 15.1 / 14.3; 56 of 32768 190.5 / 183.2.
+constexpr int kMergeStages = 7;
+
 // Units of a group of L keys.
 __device__ __forceinline__ int group_units(int L) {
   constexpr int TK = F8Cfg<128>::TK;
   return L > 0 ? (L + TK - 1) / TK + kSegmentStages : 0;
 }
 
-// Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]) and
-// returns the length of a run. report_bits as for plan_items. Ends with a barrier.
+// Units of a run, or 0 for whole groups: W units in all, the longest group Kmax.
+__device__ __forceinline__ int run_units(const SplitParams &p, int W, int Kmax) {
+  const int G = gridDim.x, S = max((W + G - 1) / G, 1), rounds = (p.B * p.Hkv * p.RB + G - 1) / G;
+  const long long bound = (long long)S + kMergeStages + (rounds == 1 ? S / 4 : 0);
+  return !p.merge_apart && rounds <= 2 && (long long)rounds * Kmax <= bound ? 0 : S;
+}
+
+// Fills s_len (attended lengths) and s_prefix (units, or whole groups, before each sequence; their
+// total at [B]) and returns the units of a run, 0 for whole groups. report_bits as for plan_items.
+// Ends with a barrier.
 __device__ int plan_runs(const SplitParams &p, int *s_len, int *s_prefix, int *s_red, bool report_bits) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int U = p.Hkv * p.RB, per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
-  int seg = 0;
+  int seg = 0, top = 0;
   uint32_t bits = 0;
   for (int b = b0; b < min(b0 + per, p.B); ++b) {
     const int L = attended_len(p, report_bits ? p.seq_lens[b] : ld_relaxed(p.seq_lens + b), bits);
     s_len[b] = L;
     seg += group_units(L) * U;
+    top = max(top, group_units(L));
   }
   if (report_bits && blockIdx.x == 0) report(p.status, bits);
   int incl = seg;
+  top = __reduce_max_sync(0xffffffffu, top);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   __syncthreads();  // s_red may still be read by an earlier plan
-  if (lane == 31) s_red[warp] = incl;
+  if (lane == 31) s_red[warp] = incl, s_red[kWarps + warp] = top;
   __syncthreads();
   int W = 0, before = incl - seg;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_red[w];
     W += s_red[w];
+    top = max(top, s_red[kWarps + w]);
   }
+  const int S = run_units(p, W, top);
   for (int b = b0; b < min(b0 + per, p.B); ++b) {
-    s_prefix[b] = before;
+    s_prefix[b] = S > 0 ? before : b * U;
     before += group_units(s_len[b]) * U;
   }
-  if (tid == 0) s_prefix[p.B] = W;
+  if (tid == 0) s_prefix[p.B] = S > 0 ? W : p.B * U;
   __syncthreads();
-  return max((W + (int)gridDim.x - 1) / (int)gridDim.x, 1);
+  return S;
 }
 
 // Run by one thread before the wait for the previous kernel: warms L2 with the start of this CTA's
@@ -649,13 +672,18 @@ __device__ void prefetch_first_run(const SplitParams &p) {
   constexpr int TK = F8Cfg<D>::TK;
   if (p.B > 8) return;
   const int U = p.Hkv * p.RB;
-  int len[8], W = 0;
+  int len[8], W = 0, top = 0;
   uint32_t bits = 0;
 #pragma unroll
   for (int b = 0; b < 8; ++b) len[b] = b < p.B ? attended_len(p, ld_relaxed(p.seq_lens + b), bits) : 0;
 #pragma unroll
-  for (int b = 0; b < 8; ++b) W += group_units(len[b]) * U;
-  const int run = (W + (int)gridDim.x - 1) / (int)gridDim.x;
+  for (int b = 0; b < 8; ++b) W += group_units(len[b]) * U, top = max(top, group_units(len[b]));
+  const int run = run_units(p, W, top);
+  if (run == 0) {
+    const int b = blockIdx.x / U, L = b < p.B ? attended_len(p, ld_relaxed(p.seq_lens + b), bits) : 0;
+    if (L > 0) prefetch_chunk_l2<D, kWarmF8>(p, b, blockIdx.x % U / p.RB, 0, L, prefetch_stages(p));
+    return;
+  }
   int at = min(blockIdx.x * (long long)run, (long long)W);
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
@@ -690,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   __shared__ int s_len[TD_MAX_BATCH];
   __shared__ int s_prefix[TD_MAX_BATCH + 1];
   __shared__ long long s_red[2 * kWarps];
-  __shared__ int s_chunk, s_last, s_sum[kWarps];
+  __shared__ int s_chunk, s_last, s_sum[2 * kWarps];
   __shared__ __align__(8) uint64_t s_merge_bar;
   __shared__ __align__(8) uint64_t s_bars[NST];
 
@@ -713,21 +741,21 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
   }
   // the plan is made before the wait for the previous kernel, on the lengths as they read then, and
   // kept if they read the same after it
-  const bool runs = p.runs;
   int S = 0;  // keys of a chunk, or units of a run
-  if (runs)
+  if (p.runs)
     S = plan_runs(p, s_len, s_prefix, s_sum, false);
   else
     plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   if (!lengths_unchanged(p, s_len)) {
-    if (runs)
+    if (p.runs)
       S = plan_runs(p, s_len, s_prefix, s_sum, true);
     else
       plan_items(p, s_len, s_prefix, &s_chunk, s_red);
   }
-  if (!runs) S = s_chunk;
+  const bool runs = S > 0;
+  if (!runs) S = p.runs ? p.Smax : s_chunk;  // a whole group is a chunk that holds every key
   const int W = s_prefix[p.B];
   const int rows = p.Hq * p.T;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -757,6 +785,10 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
       c0 = max(in - kSegmentStages, 0) * C::TK;
       c1 = min((in + n - kSegmentStages) * C::TK, L);
     } else {
+      if (L == 0) {  // only whole groups are counted for an empty sequence
+        at += gridDim.x;
+        continue;
+      }
       NC = (L + S - 1) / S;
       unit = local / NC;
       c = local % NC;

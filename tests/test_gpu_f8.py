@@ -398,6 +398,14 @@ ATTN = [
     (64, 24, 8, 2000, 3, 16, [2000, 127, 1025] + [(97 * i) % 700 for i in range(30)], 0),    # 9 rows
     (128, 32, 8, 3000, 6, 32, [3000, 5, 300, 2500, 77, 1000, 129, 0], 0),                    # 24 rows, a batch of 8
     (64, 2, 2, 3000, 1, 128, [3000] + [5] * 100, 0),
+    # whole groups, a CTA each: a short sequence up to the longest that is left whole, and one past it
+    (128, 24, 8, 640, 1, 64, [640], 0),
+    (128, 24, 8, 641, 1, 64, [641], 0),
+    (64, 15, 5, 512, 1, 32, [1], 0),
+    (128, 32, 8, 520, 1, 16, [0] + [391 + i * 17 % 130 for i in range(31)], 0),
+    (64, 15, 5, 512, 1, 128, [(i % 7 > 0) * (300 + i * 37 % 213) for i in range(64)], 0),    # over two rounds
+    (128, 8, 8, 4000, 1, 64, [4000 - 64 * i for i in range(20)], 0),
+    (64, 6, 2, 300, 2, 16, [300, 0, 1, 2], 0),
 ]
 
 
@@ -421,6 +429,34 @@ def test_captured_attention(td, T):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, td.td_verify_attn_f8(q, *d, block))
+
+
+@pytest.mark.parametrize("B", [1, 9])
+def test_captured_attention_on_changed_lengths(td, B):
+    """Short groups left whole and long ones cut, by one captured call: the lengths are read when it runs."""
+    rng = np.random.default_rng(30 + B)
+    Hq, Hkv, S, D, block = 15, 5, 1800, 64, 32
+    kc, ks = filled(rng, B, Hkv, S, D, block)
+    lens = torch.full((B,), 100, dtype=torch.int32, device="cuda")
+    d = [f8(kc), torch.from_numpy(ks).cuda(), f8(kc), torch.from_numpy(ks).cuda(), lens]
+    q = rows(rng, B, Hq, 1, D, spread=0.3)
+    qd, ws = q[:, :, 0].contiguous().cuda(), td.make_workspace(B, Hq, Hkv, S, D, 1)
+    out = torch.empty_like(qd)
+    td.td_decode_attn_f8(qd, *d, block, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        td.td_decode_attn_f8(qd, *d, block, out=out, workspace=ws)
+    v = f8_ref.values(kc, ks, block)
+    for L in (1800, 100, 640, 0, 641, 1024, 1):
+        now = [max(L - 130 * b, 0) for b in range(B)]
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        ref, rlse, _, absv, big = f8_ref.attention(q.double().numpy(), v, v, now, 1 / math.sqrt(D))
+        tol, _ = f8_ref.bounds(ref, rlse, absv, big, D, max(max(now), 1))
+        assert np.all(np.abs(out[:, :, None].double().cpu().numpy() - ref) <= tol), L
 
 
 @pytest.mark.parametrize("D,Hq,Hkv,S,T,block,lens,split", ATTN)
