@@ -69,7 +69,9 @@ struct SplitParams {
   const float *k_scales;
   const float *v_scales;
   int block_log2, n_blocks;
-  int runs, merge_apart;  // e4m3: work cut into equal runs of stages; a second launch merges (td_split_f8.cu)
+  // e4m3 (td_split_f8.cu): work cut into equal runs of stages; a second launch merges; rounds of CTAs
+  // that the groups make left whole, 0 where they never are
+  int runs, merge_apart, rounds;
 };
 
 // Attended length of a sequence whose stored length is `raw`, with the status bits its

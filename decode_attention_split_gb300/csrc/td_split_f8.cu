@@ -34,9 +34,9 @@
 //    2^-21 of a row's reference.
 //  * A code may be NaN (a stored NaN or infinity; any byte behind a sequence's end). A step that
 //    reaches a row's limit or the sequence's end zeroes the value codes past the end, and a NaN
-//    value code that only some rows see is taken out of the product and put into those rows' sums
-//    by a product of NaN and visibility indicators.
+//    value code that only some rows see is taken out of the tile and put into those rows' sums.
 #include <algorithm>
+#include <cfloat>
 #include <mutex>
 
 #include "td_f8.cuh"
@@ -88,11 +88,6 @@ __device__ __forceinline__ uint32_t hi_pair(uint32_t w) { return e4m3x2_f16x2((u
 // The bytes of w that are NaN codes (0x7f or 0xff), as 0x80 each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
-// Bytes 0, 2 (or 1, 3) of a word marked 0x80 as an fp16 pair of ones.
-__device__ __forceinline__ uint32_t ones_of(uint32_t n, int odd) {
-  return ((n >> (8 * odd)) & 0x80u ? 0x3c00u : 0u) | ((n >> (8 * odd + 16)) & 0x80u ? 0x3c000000u : 0u);
-}
-
 __device__ __forceinline__ void add_scaled(float (&o)[4], const float (&x)[4], float s) {
   const float2 a = ffma2(make_float2(x[0], x[1]), make_float2(s, s), make_float2(o[0], o[1]));
   const float2 b = ffma2(make_float2(x[2], x[3]), make_float2(s, s), make_float2(o[2], o[3]));
@@ -112,16 +107,17 @@ __device__ __forceinline__ void add_scaled(float (&o)[4], const float (&x)[4], f
 // Query fragments: qn in registers for one n tile; of more, q_mem in shared memory (8 bytes per tile,
 // k step and lane), which leaves the registers to fragments in flight.
 // ksc / vsc: the halves' scales; qs: the rows' score scale (base 2); lim: the rows' visible keys
-// (index 2 nt + e); kend: the sequence's end. MASK: some key lies past a row's limit or the end.
-template <int D, int NT, bool MASK>
+// (index 2 nt + e). masked: some key lies past a row's limit; the values that it must not see whatever
+// they are have gone by then (clear_tail, mark_nans).
+template <int D, int NT>
 __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2], const uint2 *q_mem,
                                                uint32_t kt, uint32_t vt, int kr,
-                                               int key0, int kend, const int (&lim)[2 * NT], const float (&qs)[2 * NT],
+                                               int key0, bool masked, const int (&lim)[2 * NT], const float (&qs)[2 * NT],
                                                const float (&ksc)[2], const float (&vsc)[2],
                                                float (&o)[NT][D / 16][4], float (&m_run)[2 * NT],
                                                float (&l_run)[2 * NT]) {
   constexpr int NX = D / 32;  // ldmatrix.x4 per 16 keys: 16 keys x 32 dims
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int lane = threadIdx.x & 31, gid = lane >> 2;
   const int lrow = kr + (lane & 7) + ((lane >> 3) & 1) * 8, lch = lane >> 4;
   float sc[NT][2][4];
 #pragma unroll
@@ -159,6 +155,20 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2
   // warp rises more than kMaxGap above its row's, which one vote finds; only then are the rows'
   // maxima reduced over their 8 lanes and the sums rescaled. The score scales are not negative.
   float kss[2 * NT][2], top[2 * NT];
+#pragma unroll
+  for (int ri = 0; ri < 2 * NT; ++ri) kss[ri][0] = ksc[0] * qs[ri], kss[ri][1] = ksc[1] * qs[ri];
+  if (masked) {
+#pragma unroll
+    for (int ri = 0; ri < 2 * NT; ++ri)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        // a normal number, so that -inf times it stays -inf; of a score it leaves nothing
+        if (kss[ri][hf] < FLT_MIN) kss[ri][hf] = FLT_MIN;
+#pragma unroll
+        for (int hk = 0; hk < 2; ++hk)
+          if (key0 + 16 * hf + 8 * hk + gid >= lim[ri]) sc[ri / 2][hf][2 * hk + (ri & 1)] = -INFINITY;
+      }
+  }
   bool over = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -167,19 +177,7 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2
       const int ri = 2 * nt + e;
       float half_top[2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        kss[ri][hf] = ksc[hf] * qs[ri];
-        if constexpr (MASK) {
-#pragma unroll
-          for (int hk = 0; hk < 2; ++hk) {
-            const int key = key0 + 16 * hf + 8 * hk + gid;
-            sc[nt][hf][2 * hk + e] = key < lim[ri] ? sc[nt][hf][2 * hk + e] * kss[ri][hf] : -INFINITY;
-          }
-          half_top[hf] = fmaxf(sc[nt][hf][e], sc[nt][hf][2 + e]);
-        } else {
-          half_top[hf] = fmaxf(sc[nt][hf][e], sc[nt][hf][2 + e]) * kss[ri][hf];
-        }
-      }
+      for (int hf = 0; hf < 2; ++hf) half_top[hf] = fmaxf(sc[nt][hf][e], sc[nt][hf][2 + e]) * kss[ri][hf];
       top[ri] = fmaxf(half_top[0], half_top[1]);
       over |= top[ri] > m_run[ri] + kMaxGap;
     }
@@ -218,7 +216,7 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2
 #pragma unroll
         for (int hk = 0; hk < 2; ++hk) {
           float &x = sc[nt][hf][2 * hk + e];
-          x = exp2_approx(MASK ? x - base : fmaf(x, kss[ri][hf], -base));
+          x = exp2_approx(fmaf(x, kss[ri][hf], -base));
         }
       // this thread's keys; lanes summed at the end
       l_run[ri] += (sc[nt][0][e] + sc[nt][0][2 + e]) + (sc[nt][1][e] + sc[nt][1][2 + e]);
@@ -232,55 +230,10 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2
       pb[nt][0] = movmatrix_trans(pack_f16x2(sc[nt][hf][0], sc[nt][hf][1]));
       pb[nt][1] = movmatrix_trans(pack_f16x2(sc[nt][hf][2], sc[nt][hf][3]));
     }
-    uint32_t live[2];  // bytes of keys 2c, 2c+1 (+8) before the sequence's end
-    if constexpr (MASK) {
-#pragma unroll
-      for (int hk = 0; hk < 2; ++hk) {
-        const int key = key0 + 16 * hf + 8 * hk + 2 * tig;
-        live[hk] = (key < kend ? 0xffffu : 0u) | (key + 1 < kend ? 0xffff0000u : 0u);
-      }
-    }
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
       uint32_t r[4];  // transposed: keys 0-7 / 8-15 of dims 32i .. 32i+15, then of 32i+16 ..
       ldmatrix_x4_trans(r, vt + code_swz<D>(lrow + 16 * hf, 2 * i + lch));
-      if constexpr (MASK) {
-        uint32_t n[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          r[x] &= live[x & 1];
-          n[x] = nan_bytes(r[x]);
-          r[x] &= ~((n[x] >> 7) * 0xffu);
-        }
-        if (__any_sync(0xffffffffu, (n[0] | n[1] | n[2] | n[3]) != 0u)) {
-          // rows that see a NaN value code: count them per output by indicators
-#pragma unroll 1
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t see[2] = {0u, 0u};
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-              if (x == nt)
-#pragma unroll
-                for (int hk = 0; hk < 2; ++hk) {
-                  const int key = key0 + 16 * hf + 8 * hk + gid;
-                  see[hk] = (key < lim[2 * x] ? 0x3c00u : 0u) | (key < lim[2 * x + 1] ? 0x3c000000u : 0u);
-                }
-            const uint32_t b0 = movmatrix_trans(see[0]), b1 = movmatrix_trans(see[1]);
-#pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-              const uint32_t a[4] = {ones_of(n[0], odd), ones_of(n[2], odd), ones_of(n[1], odd), ones_of(n[3], odd)};
-              float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16_16816(cnt, a, b0, b1);
-#pragma unroll
-              for (int x = 0; x < NT; ++x)
-                if (x == nt)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (cnt[y] > 0.f) o[x][2 * i + odd][y] = __uint_as_float(0x7fffffffu);
-            }
-          }
-        }
-      }
 #pragma unroll
       for (int x = 0; x < 4; ++x) r[x] = __byte_perm(r[x], 0u, 0x3120);  // the middle bytes swapped
       const uint32_t ae[4] = {lo_pair(r[0]), lo_pair(r[2]), lo_pair(r[1]), lo_pair(r[3])};
@@ -295,6 +248,65 @@ __device__ __forceinline__ void warp_keys32_f8(const uint32_t (&qn)[1][D / 16][2
       }
     }
   }
+}
+
+// One warp's values of a step that some row does not see whole (rows kr .. kr+31 of the tile vt, keys
+// key0 ..): zeros in place of the rows from key c1 on, whose bytes may be anything. True if a value
+// that some rows see and others do not, of keys [lim_all, c1), holds a NaN code, for mark_nans.
+// The step itself is one for whole and cut tiles: with one of its own for cut tiles the first CTA of
+// an SM that came to one waited for its instructions (one sequence, 8 kv heads, D = 128: 500 keys 7.6
+// -> 6.4 us, 4060 keys 8.7 -> 7.7; verify of six after 300, 14.4 -> 11.7).
+template <int D>
+__device__ __forceinline__ bool clear_tail(uint32_t vt, int kr, int key0, int lim_all, int c1) {
+  constexpr int CH = D / 16;  // 16-byte chunks of a row, in some order
+  const int lane = threadIdx.x & 31;
+  bool nan = false;
+#pragma unroll 1
+  for (int r = max(lim_all - key0, 0) + lane / CH; r < 32; r += 32 / CH) {
+    const uint32_t at = vt + (kr + r) * D + (lane % CH) * 16;
+    uint4 w;
+    if (key0 + r >= c1) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+    } else {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+      nan |= (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) != 0u;
+    }
+  }
+  nan = __any_sync(0xffffffffu, nan);
+  __syncwarp();
+  return nan;
+}
+
+// The NaN codes among the values of keys [lim_all, c1) of a step: NaN in the sums of the rows that see
+// them, and zeros in their place for the rows that do not.
+template <int D, int NT>
+__device__ __forceinline__ void mark_nans(uint32_t vt, int kr, int key0, int lim_all, int c1, const int (&lim)[2 * NT],
+                                          float (&o)[NT][D / 16][4]) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2;
+#pragma unroll 1
+  for (int r = max(lim_all - key0, 0); r < min(c1 - key0, 32); ++r) {
+    // this thread's dims 32 i + 16 h + 2 g, + 1: those of its o
+    uint16_t w[D / 16];
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x)
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(w[x]) : "r"(vt + code_swz<D>(kr + r, x) + 2 * gid) : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      const uint32_t n = nan_bytes(w[x]);
+      if ((n & 0x8080u) == 0u) continue;
+#pragma unroll
+      for (int ri = 0; ri < 2 * NT; ++ri)
+        if (key0 + r < lim[ri]) {
+          if (n & 0x80u) o[ri / 2][x & ~1][2 * (x & 1) + (ri & 1)] = __uint_as_float(0x7fffffffu);
+          if (n & 0x8000u) o[ri / 2][x | 1][2 * (x & 1) + (ri & 1)] = __uint_as_float(0x7fffffffu);
+        }
+      const uint16_t kept = (uint16_t)(w[x] & ~((n >> 7) * 0xffu));
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(vt + code_swz<D>(kr + r, x) + 2 * gid), "h"(kept) : "memory");
+    }
+  }
+  fence_proxy_async_smem();  // the stage may not be the last of its buffer
+  __syncwarp();
 }
 
 // Streams keys [c0, c1) of (b, kvh) for row block rb, as stream_chunk does for bf16 caches,
@@ -423,10 +435,10 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
       const uint32_t kt = sbase + buf * C::STAGE_BYTES, vt = kt + C::CODE_BYTES;
       const float ksc[2] = {__shfl_sync(0xffffffffu, s_mine, 0), __shfl_sync(0xffffffffu, s_mine, 1)};
       const float vsc[2] = {__shfl_sync(0xffffffffu, s_mine, 2), __shfl_sync(0xffffffffu, s_mine, 3)};
-      if (key0 + 32 <= lim_all)
-        warp_keys32_f8<D, NT, false>(qn, q_mem, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
-      else
-        warp_keys32_f8<D, NT, true>(qn, q_mem, kt, vt, kr, key0, L, lim, qs, ksc, vsc, o, m_run, l_run);
+      const bool masked = key0 + 32 > lim_all;
+      if (masked && clear_tail<D>(vt, kr, key0, lim_all, c1))
+        mark_nans<D, NT>(vt, kr, key0, lim_all, c1, lim, o);
+      warp_keys32_f8<D, NT>(qn, q_mem, kt, vt, kr, key0, masked, lim, qs, ksc, vsc, o, m_run, l_run);
     }
     consumed = st + 1;
   }
@@ -618,9 +630,8 @@ __device__ __forceinline__ int group_units(int L) {
 
 // Units of a run, or 0 for whole groups: W units in all, the longest group Kmax.
 __device__ __forceinline__ int run_units(const SplitParams &p, int W, int Kmax) {
-  const int G = gridDim.x, S = max((W + G - 1) / G, 1), rounds = (p.B * p.Hkv * p.RB + G - 1) / G;
-  const long long bound = (long long)S + kMergeStages + (rounds == 1 ? S / 4 : 0);
-  return !p.merge_apart && rounds <= 2 && (long long)rounds * Kmax <= bound ? 0 : S;
+  const unsigned S = max((W + (int)gridDim.x - 1) / (int)gridDim.x, 1), rounds = p.rounds;
+  return rounds != 0 && rounds * Kmax <= S + kMergeStages + (rounds == 1 ? S / 4 : 0) ? 0 : (int)S;
 }
 
 // Fills s_len (attended lengths) and s_prefix (units, or whole groups, before each sequence; their
@@ -836,6 +847,8 @@ cudaError_t launch(const SplitPlan &plan, const SplitParams &p, cudaStream_t str
   a.p = p;
   a.p.runs = plan.runs;
   a.p.merge_apart = plan.merge_apart;
+  const long long rounds = ((long long)p.B * p.Hkv * p.RB + plan.grid - 1) / plan.grid;
+  a.p.rounds = plan.merge_apart || rounds > 2 ? 0 : (int)rounds;
   {
     // every instantiation's shared-memory opt-in, once per device
     static std::mutex mu;
