@@ -9,7 +9,7 @@
 // Bound by the codes' bytes at few query rows, and by the warps' latency at many. Measured (GPU time
 // in a graph, inputs past L2): 3B-style layer, 32k keys, batch of 8, 80 us, 6.7 TB/s; ragged batch
 // of 32 (277 MB) 48 us; verify chunk of six over 16k keys, batch of 8 (24 rows), 63 us, 4.2 TB/s; one
-// sequence of 32k keys 14.7 us, of 4096 keys in the 360M-style layer 7.3 us (calls this short are a
+// sequence of 32k keys 15.2 us, of 4096 keys in the 360M-style layer 7.3 us (calls this short are a
 // chain of launch, lengths, first stage, ticket and merge).
 //
 // Design:
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) merge_f8_kernel(const Spl
 }
 
 // How work is cut. A split the caller chose: chunks of that size, an item per chunk (plan_items).
-// Else runs: the stages of 128 keys of every group (sequence, kv head, row block), one group after
+// Else whole groups (see kMergeStages) or runs: the stages of 128 keys of every group (sequence, kv head, row block), one group after
 // another, cut into equal runs, one per CTA, whatever the lengths. Starting and finishing a segment
 // of a group takes a CTA about as long as kSegmentStages stages, so each group counts that many
 // units more, ahead of its own. Measured, ragged batch of 32 (256 groups of 1 to 8192 keys,
