@@ -611,11 +611,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) merge_f8_kernel(const Spl
 // took 5 us after it). One sequence of 16384 keys and 8 kv heads: chunks 11.6 us, runs 11.1.
 constexpr int kSegmentStages = 3;
 
-// A run that ends inside a group costs the merge of its pieces, about kMergeStages stages; and once
-// memory is what bounds the call, CTAs that read for a quarter longer cost less than the CTAs that
-// have nothing to read seem to. So each CTA takes whole groups while the longest is no longer than
-// an equal run with that much more (over two rounds of CTAs: the merge alone; in more rounds, 1024
-// groups of 1024 keys, whole groups took 52.5 us and runs 49.2). Measured, runs / whole groups, D =
+// A run that ends inside a group costs the merge of its pieces, about kMergeStages stages; and of long
+// runs memory is the bound, which four fifths of the CTAs reach as well as all. So each CTA takes whole
+// groups while the longest is at most an equal run and kMergeStages, and in one round of CTAs a
+// quarter of a run more (in more than two rounds never: 1024 groups of 1024 keys took 52.5 us whole
+// and 49.2 in runs). Measured, runs / whole groups, D =
 // 128, 8 kv heads: one sequence of 256 keys 7.0 / 5.2 us, of 512 7.1 / 6.5, of 768 7.1 / 8.1; 32
 // sequences of 512 keys 15.9 / 11.6, of 2048 27.9 / 25.3, of 8192 83.2 / 79.9; 8 of 1024 11.0 / 12.2;
 // 20 of 4096 33.1 / 34.8. 5 kv heads, D = 64: 64 sequences (two rounds) of 256 12.5 / 10.8, of 512
