@@ -287,6 +287,57 @@ def test_rope_append_bad_positions(td, T):
     assert np.array_equal(codes_of(kc), rc) and np.array_equal(ks.cpu().numpy(), rs)
 
 
+LONG = [
+    # dtype, D, block, T, lengths, Hq, Hkv, axes: chunks whose CTAs take their heads in several rounds
+    ("bf16", 128, 32, 1531, [0, 5, 32, 100, 333, 640, 777], 32, 8, 3),   # 11 million keys; six rounds of four heads
+    ("f32", 64, 64, 2000, [0, 1, 63, 64], 24, 8, 0),                     # five of two heads
+    ("bf16", 64, 16, 3000, [7, 128], 24, 8, 0),                          # three of eight heads, a warp each
+]
+
+
+@pytest.mark.parametrize("dtype,D,block,T,lens,Hq,H,A", LONG)
+def test_rope_append_long(td, dtype, D, block, T, lens, Hq, H, A):
+    """Prompts: the keys' codes are the fp32 formula's bit for bit (an operation rounded otherwise moves
+    about one code in a million), the values' codes theirs, the queries td_rope_kv_append's."""
+    B, S = len(lens), 4096
+    rng, g = np.random.default_rng(T), torch.Generator(device="cuda").manual_seed(T)
+
+    def new(h):
+        x = torch.randn(B, h, T, D, generator=g, device="cuda") * torch.randn(B, h, T, 1, generator=g, device="cuda").exp()
+        return x.to(DT[dtype])
+
+    kn, vn, q = new(H), new(H), new(Hq)
+    kc, ks = filled(rng, B, H, S, D, block, lens)
+    cos, sin = (t.cuda() for t in rope_tables(S, D))
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    d = [f8(kc), torch.from_numpy(ks).cuda(), f8(kc), torch.from_numpy(ks).cuda(), ln]
+    at = ln.long()[:, None, None] + torch.arange(T, device="cuda")[None, :, None] + torch.zeros(D // 2, dtype=torch.long, device="cuda")
+    pos = axes = None
+    if A:
+        pos = torch.randint(0, S, (B, T, A), generator=g, device="cuda", dtype=torch.int32)
+        axes = (torch.arange(D // 2, device="cuda") * A // (D // 2)).to(torch.int32)
+        at = pos.long()[:, :, axes.long()]
+    c, s = torch.gather(cos[None].expand(B, -1, -1), 1, at)[:, None], torch.gather(sin[None].expand(B, -1, -1), 1, at)[:, None]
+    got = td.td_rope_kv_append_f8(kn, vn, *d, block, cos, sin, positions=pos, axes=axes, q=q, advance=False)
+    torch.cuda.synchronize()
+    y = f8_ref.rotate_keys(kn.double().cpu().numpy(), c.cpu().numpy(), s.cpu().numpy())
+    for x, codes, scales in ((vn.double().cpu().numpy(), d[2], d[3]), (y.astype(np.float64), d[0], d[1])):
+        wc, ws = kc.copy(), ks.copy()
+        f8_ref.append(wc, ws, x, lens, block)
+        assert np.array_equal(scales.cpu().numpy(), ws, equal_nan=True)
+        moved = int((codes_of(codes) != wc).sum())
+        assert moved == 0
+    # queries: two roundings of 2^-24 of the larger product, then one into dtype
+    lo, hi = q.double().split(D // 2, dim=-1)
+    want, pair = torch.cat([lo * c - hi * s, hi * c + lo * s], -1), torch.hypot(lo, hi)
+    u = torch.finfo(DT[dtype]).eps / 2
+    tol = u * want.abs() * (1 + 2.0 ** -10) + (1 + u) * 2.0 ** -22 * torch.cat([pair, pair], -1)
+    assert bool(((got.double() - want).abs() <= tol).all())
+    if not A:
+        cache = [torch.empty(B, H, S, D, dtype=DT[dtype], device="cuda") for _ in range(2)]
+        assert torch.equal(got, td.td_rope_kv_append(kn, vn, *cache, ln, cos, sin, q=q, advance=False))
+
+
 # ------------------------------------------------------------------------------ read-back
 
 READ = [
