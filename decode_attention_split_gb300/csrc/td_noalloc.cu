@@ -64,11 +64,9 @@ extern "C" td_status td_decode_attn_noalloc(td_dtype dtype, const void *q, const
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(seq_lens, 4) || (lse != nullptr && !aligned(lse, 4)) || (dev_status != nullptr && !aligned(dev_status, 4)))
     return TD_ERR_UNSUPPORTED;
-  // the shape needs more scratch than the array holds: the same test a caller can make with
-  // td_decode_workspace_bytes (the largest layout over the element types), so the documented
-  // limit and this check agree
-  if (plan.bytes > kScratchBytes || td_decode_workspace_bytes(B, Hq, Hkv, Smax, D, 1, split) > kScratchBytes)
-    return TD_ERR_WORKSPACE;
+  // the layout of this call's dtype alone: td_decode_workspace_bytes also covers the 8-bit caches'
+  // kernels, which this call never runs
+  if (plan.bytes > kScratchBytes) return TD_ERR_WORKSPACE;
   void *scratch = nullptr;
   const td_status sa = scratch_address(&scratch);
   if (sa != TD_OK) return sa;

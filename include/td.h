@@ -378,7 +378,8 @@ td_status td_selftest_wait_timeout(long long limit_cycles, uint32_t *dev_status,
  * running, or code working while another runtime owns the device heap.)
  * Its scratch is a fixed 4 MiB array compiled into the library, which every GPU that loads
  * the library holds until the process exits; the call allocates nothing. A shape whose
- * workspace (td_decode_workspace_bytes with q_len 1) exceeds 4 MiB returns TD_ERR_WORKSPACE.
+ * workspace exceeds 4 MiB in the layout of its dtype returns TD_ERR_WORKSPACE; none does whose
+ * td_decode_workspace_bytes (q_len 1; the largest of all dtypes and cache formats) is at most that.
  * The first call on a device looks up the array's address on that device (make that first
  * call before any stream capture). Every call zeroes the array's counter area on its stream
  * before launching. All calls on a device share the one array, so calls that may overlap on

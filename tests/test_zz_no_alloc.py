@@ -113,3 +113,32 @@ def test_noalloc_rejects_shapes_beyond_its_scratch():
     lse = torch.empty(16, 32, dtype=torch.float32, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     assert _noalloc(lib, q, kc, kc, sl, 0.1, 0, out, lse, status) == 3  # TD_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("B,Hq,Hkv", [(24, 32, 32), (24, 40, 40), (12, 64, 32), (16, 32, 8)])
+def test_noalloc_counts_only_the_layout_it_runs(B, Hq, Hkv):
+    """Shapes just under the array's size in their own layout are taken, whatever the other dtypes' and
+    cache formats' layouts need: 24 sequences of 32 heads hold 4,061,440 bytes of the 4,194,304. The
+    last, over it in every layout, is refused."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_attention_split_gb300 import _lib, build
+    build.build()
+    import decode_attention_split_gb300 as td
+    lib = _lib.lib()
+    S = 2048
+    g = torch.Generator(device="cuda").manual_seed(B)
+    q = torch.randn(B, Hq, 128, generator=g, device="cuda").to(torch.bfloat16)
+    kc, vc = (torch.randn(B, Hkv, S, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    sl = torch.tensor([S - 83 * i for i in range(B)], dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    lse = torch.empty(B, Hq, dtype=torch.float32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    st = _noalloc(lib, q, kc, vc, sl, 0.09, 0, out, lse, status)
+    torch.cuda.synchronize()
+    if Hkv == 8:
+        assert st == 3  # TD_ERR_WORKSPACE
+        return
+    assert st == 0 and int(status.item()) == 0
+    want, wl = td.td_decode_attn(q, kc, vc, sl, 0.09, 0, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
