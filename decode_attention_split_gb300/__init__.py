@@ -21,6 +21,7 @@ from .api import (  # noqa: F401
     td_decode_attn_f8,
     td_decode_attn_q8,
     td_decode_workspace_bytes,
+    td_f8_workspace_bytes,
     td_kv_append,
     td_kv_append_f8,
     td_kv_append_q8,

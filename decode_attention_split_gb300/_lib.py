@@ -17,6 +17,7 @@ SYMBOLS = (
     "td_version",
     "td_last_cuda_error",
     "td_decode_workspace_bytes",
+    "td_f8_workspace_bytes",
     "td_split_plan",
     "td_rope_kv_append",
     "td_rope_append_attn",
@@ -62,6 +63,8 @@ def _declare(lib):
     lib.td_last_cuda_error.restype = i
     lib.td_decode_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
     lib.td_decode_workspace_bytes.restype = sz
+    lib.td_f8_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+    lib.td_f8_workspace_bytes.restype = sz
     lib.td_split_plan.argtypes = [i, i, i, i, i, i, i, i, vp, vp, vp, vp]
     lib.td_split_plan.restype = i
     lib.td_rope_kv_append.argtypes = [i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp]

@@ -81,6 +81,12 @@ def td_decode_workspace_bytes(B: int, Hq: int, Hkv: int, Smax: int, D: int, q_le
     return int(lib().td_decode_workspace_bytes(B, Hq, Hkv, Smax, D, q_len, split))
 
 
+def td_f8_workspace_bytes(B: int, Hq: int, Hkv: int, Smax: int, D: int, q_len: int = 1, split: int = 0) -> int:
+    """Workspace bytes td_decode_attn_f8 / td_verify_attn_f8 need on the current device (0 = invalid);
+    those of td_decode_workspace_bytes cover them."""
+    return int(lib().td_f8_workspace_bytes(B, Hq, Hkv, Smax, D, q_len, split))
+
+
 KERNEL_NAMES = ("cuda_core", "tensor_core_persistent", "tensor_core_cluster")
 
 

@@ -66,6 +66,8 @@ td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void
   p->RB = plan->RB;
   p->split = split;
   p->ns_ws = plan->ns_ws;
+  p->n_part = (int)plan->n_part;
+  p->pieces = reinterpret_cast<int2 *>(ws + plan->off_pieces);
   p->p_target = plan->p_target;
   p->min_chunk = plan->min_chunk;
   p->warm_stages = plan->warm;
@@ -120,6 +122,12 @@ size_t td_decode_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_
       bytes = plan.bytes;
   }
   return bytes;
+}
+
+size_t td_f8_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int split) {
+  td::SplitPlan plan;
+  if (td::plan_split(TD_BF16, B, Hq, Hkv, q_len, Smax, D, split, &plan, td::KvFormat::kF8) != TD_OK) return 0;
+  return plan.bytes;
 }
 
 td_status td_split_plan(td_dtype dtype, int B, int Hq, int Hkv, int Smax, int D, int q_len, int split, int *kernel,

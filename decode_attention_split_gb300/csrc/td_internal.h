@@ -30,7 +30,8 @@ struct SplitPlan {
   bool f8;       // block-scaled e4m3 cache: its kernel
   bool runs;     // its work cut into equal runs of stages instead of chunks
   bool merge_apart;  // its partials merged by a second launch
-  size_t off_part, bytes;  // workspace layout: counters, then partial blocks
+  long long n_part;  // partial blocks in the workspace
+  size_t off_pieces, off_part, bytes;  // workspace layout: counters, pieces (merge_apart), partial blocks
 };
 
 // Records a failed CUDA call for td_last_cuda_error (and clears the runtime's last-error slot,

@@ -474,9 +474,11 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   // completion counters, one per (b, kv head, row block), then as many counts of finished
   // slice merges, then the fused step's read count
   plan->counters_n = (int)(2LL * B * U);
-  const size_t counters = align256(((size_t)plan->counters_n + 1) * sizeof(int));
-  plan->off_part = counters;
-  plan->bytes = plan->off_part + align256((size_t)B * U * ns * part_block_floats(R, D) * sizeof(float));
+  plan->off_pieces = align256(((size_t)plan->counters_n + 1) * sizeof(int));
+  plan->off_part = plan->off_pieces + (plan->merge_apart ? align256((size_t)B * U * sizeof(int2)) : 0);
+  // runs leave a block where a CTA's run ends inside a group, and one more per group cut (first_block)
+  plan->n_part = plan->runs ? plan->grid + std::min((long long)plan->grid, (long long)B * U) : items_max;
+  plan->bytes = plan->off_part + align256((size_t)plan->n_part * part_block_floats(R, D) * sizeof(float));
   return TD_OK;
 }
 

@@ -42,7 +42,8 @@ struct SplitParams {
   const int32_t *seq_lens;
   void *out;            // [B, Hq, T, D]
   float *lse;           // [B, Hq, T] or null
-  float *ws_part;       // [B, Hkv, RB][ns_ws] partial blocks of R rows (see part_row_floats)
+  float *ws_part;       // [B, Hkv, RB][ns_ws] partial blocks of R rows (see part_row_floats); of the
+                        // e4m3 kernel's runs, n_part (see first_block)
   int *counters;        // [B, Hkv, RB] completion tickets, then [B, Hkv, RB] finished slice merges
   uint32_t *status;
   int B, Hq, Hkv, G, T, Smax;
@@ -72,6 +73,8 @@ struct SplitParams {
   // e4m3 (td_split_f8.cu): work cut into equal runs of stages; a second launch merges; rounds of CTAs
   // that the groups make left whole, 0 where they never are
   int runs, merge_apart, rounds;
+  int n_part;           // partial blocks in the workspace
+  int2 *pieces;         // merge_apart: of every group, its first block and how many it has
 };
 
 // Attended length of a sequence whose stored length is `raw`, with the status bits its
@@ -298,17 +301,16 @@ __device__ __forceinline__ long long out_row_of(const SplitParams &p, int b, int
 // chunks at a time as the free shared memory holds, and are merged online: per row the
 // running maximum M, normaliser Lsum and weighted sum are rescaled when a block raises M.
 // `smem_f` spans `smem_floats` floats no one else uses now; `bar` is this CTA's merge
-// mbarrier and `phase` its current parity (uniform across the CTA).
+// mbarrier and `phase` its current parity (uniform across the CTA); `first` the group's first block.
 template <typename E, int D, int ROWS>
 __device__ void merge_group(const SplitParams &p, float *smem_f, int smem_floats, uint64_t *bar, uint32_t &phase,
-                            int b, int kvh, int rb, int NC, int nv) {
+                            int b, int kvh, int rb, long long first, int NC, int nv) {
   constexpr int kFB = 64;  // most chunks staged at a time
   constexpr int D4 = D / 4, RF = part_row_floats(D);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int R = p.R;
   const int BF = part_block_floats(R, D);
-  const long long g = ((long long)b * p.Hkv + kvh) * p.RB + rb;
-  const float *src = p.ws_part + g * p.ns_ws * (long long)BF;
+  const float *src = p.ws_part + first * BF;
   float *acc = smem_f;          // [ROWS][D] running weighted sums (between passes)
   float *st = acc + ROWS * D;   // M[ROWS], Lsum[ROWS], rescale[ROWS], 1 / Lsum[ROWS]
   float *fac = st + 4 * ROWS;   // [ROWS][kFB] factors 2^(m_c - M) of the staged chunks
@@ -559,11 +561,12 @@ __device__ void merge_rows_direct(const SplitParams &p, float *sm, int b, int kv
 //    chunks streamed in 7;
 //  * otherwise the CTA holding the last ticket merges every row (merge_group): with a few rows
 //    the helpers' waits cost more than they save (their slots are the next call's).
+// `first` is the group's first partial block, negative for the layout [B, Hkv, RB][ns_ws].
 // Ends with a __syncthreads (the shared areas may be reused afterwards).
 template <typename E, int D, int ROWS, int NSRC, int CAS = D>
 __device__ void finish_item(const SplitParams &p, float *smem_f, int smem_floats, uint64_t *merge_bar,
                             uint32_t &merge_phase, int b, int kvh, int rb, int c, int NC, int *s_last,
-                            bool one_wave) {
+                            bool one_wave, long long first = -1) {
   constexpr int D4 = D / 4, RF = part_row_floats(D);
   const int tid = threadIdx.x;
   const int GT = p.G * p.T;
@@ -599,7 +602,8 @@ __device__ void finish_item(const SplitParams &p, float *smem_f, int smem_floats
     }
     __syncthreads();
   }
-  float *blk = p.ws_part + (g * p.ns_ws + c) * (long long)part_block_floats(R, D);
+  if (first < 0) first = g * p.ns_ws;
+  float *blk = p.ws_part + (first + c) * (long long)part_block_floats(R, D);
 #pragma unroll 1
   for (int idx = tid; idx < nv * D4; idx += kThreads) {
     const int r = idx / D4, d = (idx % D4) * 4;
@@ -676,7 +680,7 @@ __device__ void finish_item(const SplitParams &p, float *smem_f, int smem_floats
         }
       }
     } else if (t == NC - 1) {
-      merge_group<E, D, ROWS>(p, smem_f, smem_floats, merge_bar, merge_phase, b, kvh, rb, NC, nv);
+      merge_group<E, D, ROWS>(p, smem_f, smem_floats, merge_bar, merge_phase, b, kvh, rb, first, NC, nv);
       if (tid == 0) *cnt = 0;  // leave the counter area zero for the next call
     }
   }

@@ -495,16 +495,17 @@ __device__ __forceinline__ void store_row_f8(const SplitParams &p, long long row
 }
 
 // Leaves a segment's result: the four warps' partials combined, to out and lse if it is its group's
-// only one, else as partial block c for merge_f8_kernel. Block 0's first row carries, in its padding,
-// the number of its group's blocks (also where that is one). Ends with a barrier.
+// only one, else as the group's partial block c (the first is `first`) for merge_f8_kernel. Segment 0
+// also leaves the group's entry of p.pieces, whatever their number. Ends with a barrier.
 template <int D, int ROWS>
-__device__ void publish_f8(const SplitParams &p, const float *combine, int b, int kvh, int rb, int c, int NC) {
+__device__ void publish_f8(const SplitParams &p, const float *combine, int b, int kvh, int rb, int c, int NC,
+                           long long first) {
   constexpr int D4 = D / 4, RF = part_row_floats(D), CAS = combine_stride<D>();
   const float *cm = combine, *cl = combine + kWarps * ROWS, *ca = combine + 2 * kWarps * ROWS;
   const int nv = min(p.R, p.G * p.T - rb * p.R);  // rows of this block that exist
   const long long g = ((long long)b * p.Hkv + kvh) * p.RB + rb;
-  float *blk = p.ws_part + (g * p.ns_ws + c) * (long long)part_block_floats(p.R, D);
-  if (c == 0 && threadIdx.x == 0) blk[D + 2] = __int_as_float(NC);
+  float *blk = p.ws_part + (first + c) * (long long)part_block_floats(p.R, D);
+  if (c == 0 && threadIdx.x == 0) p.pieces[g] = make_int2((int)first, NC);
 #pragma unroll 1
   for (int idx = threadIdx.x; idx < nv * D4; idx += kThreads) {
     const int r = idx / D4, d = (idx % D4) * 4;
@@ -547,12 +548,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) merge_f8_kernel(const Spl
   const int g = blockIdx.x, rb = g % p.RB, kvh = g / p.RB % p.Hkv, b = g / p.RB / p.Hkv;
   if (r >= min(p.R, p.G * p.T - rb * p.R)) return;
   const int BF = part_block_floats(p.R, D);
-  const float *blk = p.ws_part + (long long)g * p.ns_ws * BF, *row = blk + r * RF;
   uint32_t bits = 0;
   const int L = attended_len(p, p.seq_lens[b], bits);
   // this call's if the sequence has keys and no copy timed out, which leaves a group unpublished
-  const int NC = min(max(__float_as_int(__ldcg(blk + D + 2)), 0), p.ns_ws);
+  const int2 piece = __ldcg(p.pieces + g);
+  const int first = min(max(piece.x, 0), p.n_part), NC = min(max(piece.y, 0), p.n_part - first);
   if (L == 0 || NC == 1) return;
+  const float *row = p.ws_part + (long long)first * BF + r * RF;
   float M = -INFINITY, Ls = 0.f;
   float acc[PER];
 #pragma unroll
@@ -717,6 +719,16 @@ __device__ __forceinline__ int sequence_of(const int *s_prefix, int B, int at) {
   return lo;
 }
 
+// First partial block of group g, which has some. A caller's split: [B, Hkv, RB][ns_ws]. Runs: a group's
+// segment c lies in run f + c, f the run of its first stage, and starts at block f + min(f, g) + c. A group
+// that is cut has two segments or more, so for the next one cut f has grown by at least one less than
+// their number and min(f, g) by at least one: no block is shared, and grid + min(grid, groups) hold all
+// (64 sequences, 8 kv heads, 24 rows: 7.7 MB, where ns_ws for every group took 253).
+__device__ __forceinline__ long long first_block(const SplitParams &p, bool runs, int g, int c) {
+  const int f = (int)blockIdx.x - c;
+  return runs ? f + min(f, g) : (long long)g * p.ns_ws;
+}
+
 // Persistent kernel over a block-scaled cache: the items, chunks and fused merge of
 // split_attn_mma_kernel, or runs.
 template <int D, int NT>
@@ -809,11 +821,12 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_f8_kernel(const __grid
     }
     const int rb = unit % p.RB, kvh = unit / p.RB;
     const bool ok = stream_chunk_f8<D, NT>(a, smem, s_bars, seq, b, kvh, rb, L, c0, c1);
+    const long long first = NC > 1 ? first_block(p, runs, b * p.Hkv * p.RB + unit, c) : 0;
     if (p.merge_apart)
-      publish_f8<D, TR>(p, combine, b, kvh, rb, c, NC);
+      publish_f8<D, TR>(p, combine, b, kvh, rb, c, NC, first);
     else
       finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
-                                                         rb, c, NC, &s_last, false);
+                                                         rb, c, NC, &s_last, false, first);
     fence_proxy_async_smem();
     __syncthreads();
     if (!ok) break;

@@ -311,12 +311,14 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t) {
 }
 
 // Workspaces kept for calls that bring none: one per (device, stream, call shape), zero-filled when
-// made, most recently used first. Never destroyed: they may outlive the driver at exit.
+// made, most recently used first, kMost of them and kMostBytes in all at most (a caller's split can ask
+// for gigabytes; the one in use stays whatever its size). One that is dropped goes back to the
+// allocator of the stream whose calls alone used it. Never destroyed at exit, which they may outlive.
 using Key = std::array<long long, 9>;
 at::Tensor kept_workspace(const Key &key, const at::Tensor &like) {
   static std::mutex mu;
   static auto *kept = new std::list<std::pair<Key, at::Tensor>>();
-  constexpr size_t kMost = 32;
+  constexpr size_t kMost = 32, kMostBytes = size_t(256) << 20;
   want(c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None, PyExc_ValueError,
        "pass a workspace of its own to a call that is captured in a graph");
   {
@@ -327,12 +329,17 @@ at::Tensor kept_workspace(const Key &key, const at::Tensor &like) {
         return it->second;
       }
   }
-  const size_t need = td_decode_workspace_bytes((int)key[2], (int)key[3], (int)key[4], (int)key[5], (int)key[6],
-                                                (int)key[7], (int)key[8]);
+  const size_t need = td_f8_workspace_bytes((int)key[2], (int)key[3], (int)key[4], (int)key[5], (int)key[6],
+                                            (int)key[7], (int)key[8]);
   at::Tensor ws = at::zeros({(int64_t)(need < 256 ? 256 : need)}, like.options().dtype(at::kByte));
   std::lock_guard<std::mutex> lock(mu);
   kept->emplace_front(key, ws);
-  if (kept->size() > kMost) kept->pop_back();
+  size_t bytes = 0;
+  for (const auto &w : *kept) bytes += (size_t)w.second.numel();
+  while (kept->size() > 1 && (kept->size() > kMost || bytes > kMostBytes)) {
+    bytes -= (size_t)kept->back().second.numel();
+    kept->pop_back();
+  }
   return ws;
 }
 

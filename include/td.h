@@ -109,6 +109,12 @@ int td_last_cuda_error(void);
 size_t td_decode_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int split);
 
 /*
+ * Workspace for td_decode_attn_f8 / td_verify_attn_f8 alone, under the same rules: with split 0 at most
+ * 8 MB of partials whatever the batch, and 16 bytes for every sequence, kv head and row block.
+ */
+size_t td_f8_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int split);
+
+/*
  * The launch td_decode_attn (q_len = 1) or td_verify_attn (q_len = T) makes for these
  * arguments on the current CUDA device; nothing is launched. Outputs are host pointers,
  * each nullable:
@@ -335,7 +341,7 @@ td_status td_kv_read_f8(td_dtype dtype, const void *k_codes, const float *k_scal
 /* td_decode_attn / td_verify_attn over an f8 cache: the results over the cache the codes stand
  * for, q and out bf16. split is 0 or a multiple of 16. A row that sees a NaN key gives NaN and
  * lse = +inf, a NaN value NaN in that element; bytes past a sequence's length are never used.
- * The workspace is td_decode_workspace_bytes' (which covers it). */
+ * The workspace is td_f8_workspace_bytes' (td_decode_workspace_bytes' covers it). */
 td_status td_decode_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
                             const float *v_scales, const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D,
                             int block, float scale, int split, void *out, float *lse, void *workspace,

@@ -210,6 +210,12 @@ def test_binding_checks_the_rest(name, change):
     assert "CUDA" not in str(e.value)
 
 
+@pytest.mark.parametrize("args", [(0, 4, 2, 64, 128, 1, 0), (1, 5, 2, 64, 128, 1, 0), (1, 4, 2, 64, 96, 1, 0),
+                                  (1, 4, 2, 64, 128, 65, 0), (1, 4, 2, 64, 128, 1, -1), (1025, 4, 2, 64, 128, 1, 0)])
+def test_workspace_of_refused_shapes(lib, args):
+    assert lib.td_f8_workspace_bytes(*args) == 0
+
+
 def test_binding_names_stand_in_the_package():
     import decode_attention_split_gb300 as td
     for n in ("td_kv_append_f8", "td_rope_kv_append_f8", "td_kv_read_f8", "td_decode_attn_f8", "td_verify_attn_f8",

@@ -821,6 +821,50 @@ def test_one_workspace_for_calls_of_one_shape(td):
             assert torch.equal(a, first[0]) and torch.equal(b, first[1])
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,S,T,block,lens,split", ATTN)
+def test_attention_stays_inside_its_workspace(td, D, Hq, Hkv, S, T, block, lens, split):
+    """A workspace of exactly the bytes asked for gives the same bits, and nothing behind it is written."""
+    rng = np.random.default_rng(D + S + T)
+    B = len(lens)
+    kc, ks = filled(rng, B, Hkv, S, D, block, lens)
+    q = rows(rng, B, Hq, T, D, spread=0.3)
+    want = attend(td, q, (kc, ks, kc, ks), lens, block, 0.1, split)
+    n = td.td_f8_workspace_bytes(B, Hq, Hkv, S, D, T, split)
+    buf = torch.zeros(n + 65536, dtype=torch.uint8, device="cuda")
+    buf[n:] = 0xa5
+    for _ in range(2):
+        got = attend(td, q, (kc, ks, kc, ks), lens, block, 0.1, split, workspace=buf[:n])
+        assert all(np.array_equal(a, b) for a, b in zip(got, want))
+    assert bool((buf[n:] == 0xa5).all())
+    assert n <= td.td_decode_workspace_bytes(B, Hq, Hkv, S, D, T, split)
+
+
+def _memory_of_call(td, B, splits):
+    Hkv, S, D, block, T = 8, 4864, 128, 128, 6
+    cache = td.make_f8_cache(B, Hkv, S, D, block)
+    lens = torch.full((B,), 700, dtype=torch.int32, device="cuda")
+    q = torch.zeros(B, 4 * Hkv, T, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for split in splits:
+        td.td_verify_attn_f8(q, *cache, lens, block, split=split, out=out)
+    torch.cuda.synchronize()
+    return torch.cuda.memory_allocated() - before
+
+
+def test_workspaces_are_small(td):
+    """What a call keeps does not grow with the batch: 608 blocks of 24 rows (7.7 MB) and 16 bytes a group."""
+    assert td.td_f8_workspace_bytes(64, 32, 8, 32768, 128, 6) < 9 << 20
+    assert td.td_f8_workspace_bytes(1024, 8, 1, 32768, 128, 3) < 9 << 20
+    assert _memory_of_call(td, 64, [0]) < 9 << 20
+
+
+def test_kept_workspaces_are_bounded(td):
+    """Splits of the caller's that ask for 247, 123, 84 and 62 MB: 256 MB of them are kept at most."""
+    assert _memory_of_call(td, 8, [16, 32, 48, 64]) <= 256 << 20
+
+
 def test_largest_batch(td):
     rng = np.random.default_rng(19)
     B, Hkv, S, D, block = 1024, 1, 40, 64, 16
