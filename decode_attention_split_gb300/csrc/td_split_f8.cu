@@ -63,8 +63,10 @@ struct F8Cfg {
   static_assert(SMEM_BYTES + 8704 <= 227 * 1024, "shared memory of a CTA");
 };
 
-// Powers of two that the probabilities are kept above their usual place by.
-constexpr float kPShift = 7.f;
+// Powers of two that the probabilities are kept above their usual place by, for fp16's sake alone: the
+// value scales take them off again, so the fp32 sums of p V hold values as large as the bf16 kernel's do
+// (a value of 3e38 seen alone is the output), and the sums of p as they leave the CTA.
+constexpr float kPShift = 7.f, kPUnit = 1.f / 128;
 
 // Byte offset of 16-byte chunk `ch` of row `row` in a code tile of D-byte rows as the TMA unit
 // writes it (128- or 64-byte swizzle): the 8 rows one ldmatrix reads fall in 8 bank groups.
@@ -106,7 +108,7 @@ __device__ __forceinline__ void add_scaled(float (&o)[4], const float (&x)[4], f
 //    o[nt][2i+1] the dims after them.
 // Query fragments: qn in registers for one n tile; of more, q_mem in shared memory (8 bytes per tile,
 // k step and lane), which leaves the registers to fragments in flight.
-// ksc / vsc: the halves' scales; qs: the rows' score scale (base 2); lim: the rows' visible keys
+// ksc / vsc: the halves' scales (the values' times kPUnit); qs: the rows' score scale (base 2); lim: the rows' visible keys
 // (index 2 nt + e). masked: some key lies past a row's limit; the values that it must not see whatever
 // they are have gone by then (clear_tail, mark_nans).
 template <int D, int NT>
@@ -434,7 +436,7 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
     if (key0 < c1) {
       const uint32_t kt = sbase + buf * C::STAGE_BYTES, vt = kt + C::CODE_BYTES;
       const float ksc[2] = {__shfl_sync(0xffffffffu, s_mine, 0), __shfl_sync(0xffffffffu, s_mine, 1)};
-      const float vsc[2] = {__shfl_sync(0xffffffffu, s_mine, 2), __shfl_sync(0xffffffffu, s_mine, 3)};
+      const float vsc[2] = {kPUnit * __shfl_sync(0xffffffffu, s_mine, 2), kPUnit * __shfl_sync(0xffffffffu, s_mine, 3)};
       const bool masked = key0 + 32 > lim_all;
       if (masked && clear_tail<D>(vt, kr, key0, lim_all, c1))
         mark_nans<D, NT>(vt, kr, key0, lim_all, c1, lim, o);
@@ -470,8 +472,8 @@ __device__ bool stream_chunk_f8(const F8Args &a, unsigned char *smem, uint64_t *
         // a row that saw a NaN key: the merges drop partials whose sum is not positive, so it is
         // given a sum and a maximum that outweigh every other partial's
         const bool bad = isnan(l_run[ri]);
-        cm[warp * TR + r] = bad ? 3e38f : m_run[ri] - kPShift;
-        cl[warp * TR + r] = bad ? INFINITY : l_run[ri];
+        cm[warp * TR + r] = bad ? 3e38f : m_run[ri];
+        cl[warp * TR + r] = bad ? INFINITY : l_run[ri] * kPUnit;
       }
       float *row = &ca[(warp * TR + r) * combine_stride<D>()];
 #pragma unroll

@@ -553,6 +553,21 @@ def test_attention_magnitudes(td, T, what):
     check(td, q, (kc, ks, vc, vs), lens, block, scale)
 
 
+@pytest.mark.parametrize("T", [1, 5])
+def test_attention_largest_values(td, T):
+    """Values up to 2^116, whose sums over 500 keys are inside fp32 (2^125), and one key of the largest
+    value a cache holds of finite rows, 448 * 2^119: the output itself."""
+    rng = np.random.default_rng(T)
+    B, Hq, Hkv, S, D, block, lens = 2, 8, 2, 500, 128, 32, [500, 130]
+    kc, ks = filled(rng, B, Hkv, S, D, block, lens)
+    vc, vs = filled(rng, B, Hkv, S, D, block, lens)
+    vs *= np.float32(2.0 ** 116 / np.nanmax(448 * vs))
+    check(td, rows(rng, B, Hq, T, D, spread=0.3), (kc, ks, vc, vs), lens, block, 1 / math.sqrt(D))
+    vc[:], vs[:] = 0x7e, 2.0 ** 119
+    out, _, _ = attend(td, rows(rng, B, Hq, T, D), (kc, ks, vc, vs), [T, 1], block, 0.1)
+    assert np.all(out[0, :, 0] == 448 * 2.0 ** 119) and np.all(out[1, :, T - 1] == 448 * 2.0 ** 119)
+
+
 @pytest.mark.parametrize("T,Hq,split", [(1, 8, 0), (1, 8, 64), (6, 8, 0), (6, 8, 64), (3, 2, 0)])
 def test_attention_nan_values_reach_only_the_rows_that_see_them(td, T, Hq, split):
     """A NaN value code gives NaN in its element for the rows that see it, and nothing else."""
