@@ -87,7 +87,10 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile every .cu under csrc/ and link libtd.so, then the native binding; returns libtd.so's path."""
+    """Compile every .cu under csrc/ and link libtd.so, then the native binding; returns libtd.so's path.
+
+    Where the binding does not build (no Python or torch headers) libtd.so is in place when this
+    raises: every call but the f8 ones from Python works with it."""
     if not force and not extra_flags and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -107,13 +110,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             if os.path.exists(tmp_lib):
                 os.unlink(tmp_lib)
             raise RuntimeError(f"link failed:\n{r.stderr}")
-        binding.result()
         os.replace(tmp_lib, LIB)
-        _link_binding(binding_obj)
         with open(PTXAS_LOG, "w") as f:
             f.write("\n".join(logs))
         if verbose:
             print("\n".join(logs))
+        try:
+            binding.result()
+            _link_binding(binding_obj)
+        except BaseException:
+            if os.path.exists(BINDING):
+                os.unlink(BINDING)  # an earlier library's
+            raise
     finally:
         shutil.rmtree(tmpdir, ignore_errors=True)
     return LIB

@@ -1,5 +1,6 @@
 """The block-scaled 8-bit cache without a GPU: what the C calls and the binding refuse before any
 launch, and the plain reference against itself."""
+import ctypes
 import inspect
 import re
 
@@ -229,6 +230,24 @@ def test_make_f8_cache_shapes():
     assert ks.shape == vs.shape == (2, 3, 4) and ks.dtype == torch.float32
     with pytest.raises(ValueError):
         api.make_f8_cache(2, 3, 100, 64, 20, device="cpu")
+
+
+def test_library_is_installed_though_the_binding_fails(monkeypatch, tmp_path):
+    """libtd.so needs neither Python's nor torch's headers: a binding that does not compile raises with
+    the library in place, and no earlier library's binding is left beside it."""
+    (tmp_path / "td_one.cu").write_text('extern "C" int td_one(void) { return 41; }\n')
+    (tmp_path / "binding.cpp").write_text("#include <no_such_header.h>\n")
+    out = tmp_path / "_build"
+    out.mkdir()
+    (out / "_td_torch.so").write_bytes(b"an earlier one")
+    for name, at in dict(CSRC=tmp_path, BUILD=out, LIB=out / "libtd.so", BINDING=out / "_td_torch.so",
+                         BINDING_SRC=tmp_path / "binding.cpp", PTXAS_LOG=out / "ptxas.log").items():
+        monkeypatch.setattr(td_build, name, str(at))
+    with pytest.raises(RuntimeError, match="no_such_header"):
+        td_build.build(force=True)
+    assert ctypes.CDLL(str(out / "libtd.so")).td_one() == 41
+    assert sorted(p.name for p in out.iterdir()) == ["libtd.so", "ptxas.log"]
+    assert not td_build.up_to_date()
 
 
 def test_f8_kernels_have_no_spills(lib):
