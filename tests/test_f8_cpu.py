@@ -260,6 +260,16 @@ def test_f8_kernels_have_no_spills(lib):
         assert sum(k in x for x in seen) == n, k
 
 
+def test_f8_row_kernels_have_no_spills(lib):
+    """The same gate for the token append, whose CTAs of 1024 threads leave it 64 registers, and the
+    launch that advances the lengths."""
+    log = open(td_build.PTXAS_LOG).read()
+    entries = re.findall(r"Compiling entry function '(\w+)'.*?\n(?:.*?\n)*?\s+(\d+) bytes stack frame, (\d+) bytes "
+                         r"spill stores, (\d+) bytes spill loads", log)
+    for k, n in (("append_f8_rows_kernel", 8), ("advance_f8_kernel", 1)):
+        assert [(int(st), int(ld)) for name, _, st, ld in entries if k in name] == [(0, 0)] * n, k
+
+
 def test_reference_codes_agree_with_torch():
     """encode and VALUE against torch's e4m3 conversions, ties and the least values included."""
     x = np.concatenate([f8_ref.VALUE[:127], f8_ref._MID, -f8_ref._MID, np.linspace(-460, 460, 4001),
