@@ -478,7 +478,10 @@ __global__ void advance_f8_kernel(int32_t *seq_lens, int B, int T, int Smax) {
 // block's rows at once, in more rounds the more heads there are. Measured in us, rows / tiles, 48
 // heads a sequence rotated: 1 sequence T = 1 3.2 / 3.4, T = 4 5.2 / 3.8; 24 sequences T = 4 5.3 / 7.0,
 // T = 8 8.1 / 7.3; 64 sequences T = 12 11.2 / 12, T = 16 16.5 / 12.8. 16 heads, plain: 1 sequence T = 4
-// 3.1 / 3.5, T = 8 3.6 / 3.3; 64 sequences T = 8 3.9 / 5.3, T = 16 4.8 / 5.6.
+// 3.1 / 3.5, T = 8 3.6 / 3.3; 64 sequences T = 8 3.9 / 5.3, T = 16 4.8 / 5.6. The rows kernel's launch counts on
+// one block a chunk; where a plain one crosses into another, some warps take a second unit (16 heads of 24
+// sequences, T = 4 2.0 against 3.0, T = 8 2.5 against 3.8; rotated ones, whose units get shorter, lose 3 % at
+// most and gain up to a fifth).
 bool takes_rows(bool rope, int T, long long heads) {
   return T <= kF8RowsT && T <= (rope ? 1 + heads / 240 : 4 + heads / 50);
 }

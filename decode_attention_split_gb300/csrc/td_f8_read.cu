@@ -1,7 +1,7 @@
 // Read-back of the block-scaled 8-bit cache: rows start[b] .. start[b]+N-1 of every head as
 // code * scale in bf16 or fp32, K and V in one launch; rows at or past the sequence's length (and
 // before row 0) leave the output as it was. Bound by memory: one byte read and 2 or 4 written per
-// element. A thread converts 16 bytes of output at a time, kRows rows' worth in flight.
+// element. A thread converts 16 bytes of output at a time, with kReadVecs such loads in flight.
 #include "td_f8.cuh"
 #include "td_internal.h"
 

@@ -7,9 +7,9 @@
 // kernel, the partial blocks and the fused merge of that kernel and a plan of its own.
 //
 // Bound by the codes' bytes at few query rows, and by the warps' latency at many. Measured (GPU time
-// in a graph, inputs past L2): 3B-style layer, 32k keys, batch of 8, 80 us, 6.7 TB/s; ragged batch
-// of 32 (277 MB) 48 us; verify chunk of six over 16k keys, batch of 8 (24 rows), 63 us, 4.2 TB/s; one
-// sequence of 32k keys 15.2 us, of 4096 keys in the 360M-style layer 7.3 us (calls this short are a
+// in a graph, inputs past L2): 3B-style layer, 32k keys, batch of 8, 79 us, 6.8 TB/s; ragged batch
+// of 32 (277 MB) 48 us; verify chunk of six over 16k keys, batch of 8 (24 rows), 62 us, 4.3 TB/s; one
+// sequence of 32k keys 15.1 us, of 4096 keys in the 360M-style layer 7.6 us (calls this short are a
 // chain of launch, lengths, first stage, ticket and merge).
 //
 // Design:
@@ -30,8 +30,11 @@
 //    several streams cannot block one another.
 //  * fp16 has 11 significant bits but a short range: a query row is first brought to a largest
 //    element in [2^14, 2^15) by a power of two (undone with the scores' scale), and probabilities
-//    are kept 2^7 above their usual place (at most 2^15), which puts the least normal fp16 at
-//    2^-21 of a row's reference.
+//    are kept 2^7 above their usual place (at most 2^15). So fewer bits than fp32 are left to query
+//    elements below 2^-28 of their row's largest, and to probabilities: 11 significant bits down to
+//    2^-21 of the row's reference, an absolute 2^-32 of it below. The sum of a row's probabilities
+//    is taken before that rounding. Outputs are as far from the exact ones as a formula in fp32's,
+//    whose last rounding into bf16 is the coarser.
 //  * A code may be NaN (a stored NaN or infinity; any byte behind a sequence's end). A step that
 //    reaches a row's limit or the sequence's end zeroes the value codes past the end, and a NaN
 //    value code that only some rows see is taken out of the tile and put into those rows' sums.
@@ -624,6 +627,10 @@ constexpr int kSegmentStages = 3;
 // sequences of 512 keys 15.9 / 11.6, of 2048 27.9 / 25.3, of 8192 83.2 / 79.9; 8 of 1024 11.0 / 12.2;
 // 20 of 4096 33.1 / 34.8. 5 kv heads, D = 64: 64 sequences (two rounds) of 256 12.5 / 10.8, of 512
 // 15.1 / 14.3; 56 of 32768 190.5 / 183.2.
+// Blocks of more than 8 rows are always cut: their stages take longer, their merge is spread over the GPU
+// by its own launch, and the same rule would lose more than it gains (runs / whole groups, verify of six,
+// 32 query and 8 kv heads, D = 128: one sequence of 256 keys 11.4 / 13.0 us, of 500 12.2 / 15.1; 8 of 512
+// 16.1 / 18.2; 32 of 512 25.3 / 21.2, of 2048 41.1 / 38.8, of 8192 101 / 109).
 constexpr int kMergeStages = 7;
 
 // Units of a group of L keys.

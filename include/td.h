@@ -71,7 +71,7 @@ typedef enum td_status {
   TD_OK = 0,
   TD_ERR_INVALID_ARG = 1, /* null pointer, bad shape, bad scale */
   TD_ERR_UNSUPPORTED = 2, /* valid but not built: head dim, dtype, alignment, batch size */
-  TD_ERR_WORKSPACE = 3,   /* workspace missing or smaller than td_decode_workspace_bytes() */
+  TD_ERR_WORKSPACE = 3,   /* workspace missing or smaller than td_*_workspace_bytes() gives */
   TD_ERR_CUDA = 4         /* a CUDA call failed (see td_last_cuda_error) */
 } td_status;
 
@@ -339,7 +339,9 @@ td_status td_kv_read_f8(td_dtype dtype, const void *k_codes, const float *k_scal
                         int Smax, int D, int block, void *k_out, void *v_out, uint32_t *dev_status, void *stream);
 
 /* td_decode_attn / td_verify_attn over an f8 cache: the results over the cache the codes stand
- * for, q and out bf16. split is 0 or a multiple of 16. A row that sees a NaN key gives NaN and
+ * for, q and out bf16. split is 0 or a multiple of 16. Operands are fp16, sums fp32: a query element
+ * below 2^-28 of its row's largest loses bits, a softmax weight has 11 significant ones down to 2^-21 of
+ * the row's largest and an absolute error of 2^-32 of it below. A row that sees a NaN key gives NaN and
  * lse = +inf, a NaN value NaN in that element; bytes past a sequence's length are never used.
  * The workspace is td_f8_workspace_bytes' (td_decode_workspace_bytes' covers it). */
 td_status td_decode_attn_f8(const void *q, const void *k_codes, const float *k_scales, const void *v_codes,
