@@ -415,9 +415,6 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
     const long long by_grid = (p_target + U - 1) / U;
     ns = by_size < by_grid ? by_size : by_grid;
     if (ns < 1) ns = 1;
-    // the block-scaled kernel cuts the keys into equal runs of 128-key stages, one per CTA, that cross
-    // from group to group: a group then meets one CTA more
-    if (f8) ns = std::max(ns, std::min(((long long)Smax + 127) / 128, by_grid + 1));
   }
   const long long items_max = (long long)B * U * ns;
   if (items_max >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
