@@ -27,6 +27,7 @@ from .api import (  # noqa: F401
     td_kv_append_q8,
     td_kv_read_f8,
     td_lse_merge,
+    td_norm_rope_kv_append,
     td_prefill_attn,
     td_rope_append_attn,
     td_rope_kv_append,

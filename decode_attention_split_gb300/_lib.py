@@ -20,6 +20,7 @@ SYMBOLS = (
     "td_f8_workspace_bytes",
     "td_split_plan",
     "td_rope_kv_append",
+    "td_norm_rope_kv_append",
     "td_rope_append_attn",
     "td_spec_accept",
     "td_spec_workspace_bytes",
@@ -69,6 +70,9 @@ def _declare(lib):
     lib.td_split_plan.restype = i
     lib.td_rope_kv_append.argtypes = [i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp]
     lib.td_rope_kv_append.restype = i
+    lib.td_norm_rope_kv_append.argtypes = [i, vp, vp, i, vp, vp, vp, vp, f, vp, vp, i, vp, vp, i, vp, vp, vp, i, i, i, i, i,
+                                           i, vp, vp]
+    lib.td_norm_rope_kv_append.restype = i
     lib.td_rope_append_attn.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp, vp, vp,
                                         sz, vp, vp]
     lib.td_rope_append_attn.restype = i

@@ -32,6 +32,15 @@ DEV_WORKSPACE_DIRTY = 32
 DEV_BAD_TOKEN = 64
 DEV_BAD_POSITION = 128
 
+_native = None  # the native binding of some of the calls (csrc/td_torch.cpp)
+
+
+def _load_native():
+    global _native
+    _native = torch_binding()
+    return _native
+
+
 _ws_lock = threading.Lock()
 _ws_cache: dict[tuple[int, int], torch.Tensor] = {}
 
@@ -279,6 +288,18 @@ def td_rope_kv_append(k_new, v_new, k_cache, v_cache, seq_lens, cos_t, sin_t, q=
     return q_out
 
 
+def td_norm_rope_kv_append(k_new, v_new, k_cache, v_cache, seq_lens, k_weight, cos_t, sin_t, eps: float = 1e-6,
+                           positions=None, axes=None, q=None, q_weight=None, q_out=None, advance: bool = True,
+                           dev_status=None, stream=None):
+    """td_rope_kv_append with each head's row divided by its root mean square (over D, plus eps) and multiplied
+    by k_weight float32 [D] before the rotation; with q [B,Hq,T,D] and q_weight float32 [D], also return q
+    normed and rotated the same way (into q_out, which may be q). Pair i of token t turns by table row
+    seq_lens[b]+t, or with positions int32 [B,T,A] by row positions[b,t,axes[i]] (axes int32 [D/2], None for
+    axis 0): tokens behind a shared prefix, or time, height and width of image and video tokens."""
+    return (_native or _load_native()).norm_append(k_new, v_new, k_cache, v_cache, seq_lens, k_weight, cos_t, sin_t, eps,
+                                                   positions, axes, q, q_weight, q_out, advance, dev_status, stream)
+
+
 def td_rope_append_attn(q, k_new, v_new, k_cache, v_cache, seq_lens, scale: float | None = None, split: int = 0,
                         cos_t=None, sin_t=None, advance: bool = True, out=None, lse=None, workspace=None,
                         dev_status=None, stream=None, return_lse: bool = False):
@@ -432,13 +453,6 @@ def td_decode_attn_q8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, scale: 
 # ------------------------------------------------------------------ 8-bit cache in blocks (f8)
 
 F8_BLOCKS = (16, 32, 64, 128)
-_f8 = None  # the native binding of these calls (csrc/td_torch.cpp)
-
-
-def _load_f8():
-    global _f8
-    _f8 = torch_binding()
-    return _f8
 
 
 def make_f8_cache(B: int, Hkv: int, Smax: int, D: int, block: int, device=None):
@@ -456,7 +470,7 @@ def td_kv_append_f8(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens
     """Quantise k_new/v_new [B,Hkv,T,D] (float32 or bfloat16) into a block-scaled cache at rows
     seq_lens[b].. (td.h; td_kv_append's rules): codes float8_e4m3fn [B,Hkv,Smax,D], scales float32
     [B,Hkv,ceil(Smax/block)], block 16, 32, 64 or 128."""
-    (_f8 or _load_f8()).append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, advance, dev_status,
+    (_native or _load_native()).append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, advance, dev_status,
                                stream)
 
 
@@ -467,7 +481,7 @@ def td_rope_kv_append_f8(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq
     way (into q_out, which may be q). Tables float32 [positions, D/2]. Pair i of token t turns by
     table row seq_lens[b]+t, or with positions int32 [B,T,A] by row positions[b,t,axes[i]] (axes int32
     [D/2], None for axis 0): time, height and width of image or video tokens."""
-    return (_f8 or _load_f8()).rope_append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, cos_t,
+    return (_native or _load_native()).rope_append(k_new, v_new, k_codes, k_scales, v_codes, v_scales, seq_lens, block, cos_t,
                                            sin_t, positions, axes, q, q_out, advance, dev_status, stream)
 
 
@@ -477,7 +491,7 @@ def td_kv_read_f8(k_codes, k_scales, v_codes, v_scales, seq_lens, block: int, ro
     code * scale: (k_out, v_out) [B,Hkv,rows,D] in dtype (or that of the outputs passed, whose third
     size is then the number of rows). Rows outside the sequence are left as they were, zero in
     outputs made here. Read whole, the outputs are the bfloat16 caches td_prefill_attn takes."""
-    return (_f8 or _load_f8()).read(k_codes, k_scales, v_codes, v_scales, seq_lens, block, rows, start, dtype, k_out,
+    return (_native or _load_native()).read(k_codes, k_scales, v_codes, v_scales, seq_lens, block, rows, start, dtype, k_out,
                                     v_out, dev_status, stream)
 
 
@@ -487,7 +501,7 @@ def td_decode_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: 
     """Single-token decode over a block-scaled cache: q [B,Hq,D] bf16 -> out [B,Hq,D] (+ lse [B,Hq])."""
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
-    return (_f8 or _load_f8()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
+    return (_native or _load_native()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
                                     workspace, dev_status, stream, return_lse)
 
 
@@ -498,7 +512,7 @@ def td_verify_attn_f8(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block: 
     tokens) -> out [B,Hq,T,D] (+ lse [B,Hq,T])."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, T, D]")
-    return (_f8 or _load_f8()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
+    return (_native or _load_native()).attn(q, k_codes, k_scales, v_codes, v_scales, seq_lens, block, scale, split, out, lse,
                                     workspace, dev_status, stream, return_lse)
 
 

@@ -214,6 +214,57 @@ td_status td_rope_kv_append(td_dtype dtype, const void *q, void *q_out, int Hq, 
   return e == cudaSuccess ? TD_OK : cuda_fail(e);
 }
 
+td_status td_norm_rope_kv_append(td_dtype dtype, const void *q, void *q_out, int Hq, const float *q_weight,
+                                 const void *k_new, const void *v_new, const float *k_weight, float eps,
+                                 const float *cos_t, const float *sin_t, int table_rows, const int32_t *positions,
+                                 const int32_t *axes, int n_axes, void *k_cache, void *v_cache, int32_t *seq_lens, int B,
+                                 int Hkv, int T, int Smax, int D, int advance, uint32_t *dev_status, void *stream) {
+  if (dtype != TD_F32 && dtype != TD_BF16) return TD_ERR_UNSUPPORTED;
+  if (k_new == nullptr || v_new == nullptr || k_weight == nullptr || k_cache == nullptr || v_cache == nullptr ||
+      seq_lens == nullptr || cos_t == nullptr || sin_t == nullptr || (q == nullptr) != (q_out == nullptr) ||
+      (q == nullptr) != (q_weight == nullptr))
+    return TD_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || T < 1 || Smax < 1 || (q != nullptr && Hq < 1) || !(eps > 0.f) || !isfinite(eps))
+    return TD_ERR_INVALID_ARG;
+  if (positions == nullptr ? (axes != nullptr || table_rows < Smax) : (n_axes < 1 || table_rows < 1))
+    return TD_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || B > 65535 || T > (1 << 20) || Smax > (1 << 30) || Hkv > 4096 ||
+      (q != nullptr && Hq > 4096) || (positions != nullptr && n_axes > 16))
+    return TD_ERR_UNSUPPORTED;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_weight) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(cos_t) || !aligned16(sin_t) || !aligned4(seq_lens) ||
+      (q != nullptr && (!aligned16(q) || !aligned16(q_out) || !aligned16(q_weight))) ||
+      (positions != nullptr && !aligned4(positions)) || (axes != nullptr && !aligned4(axes)) ||
+      (dev_status != nullptr && !aligned4(dev_status)))
+    return TD_ERR_UNSUPPORTED;
+  td::NormAppend p = {};
+  p.q = q;
+  p.q_out = q_out;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.cos_t = cos_t;
+  p.sin_t = sin_t;
+  p.positions = positions;
+  p.axes = axes;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.seq_lens = seq_lens;
+  p.status = dev_status;
+  p.eps = eps;
+  p.B = B;
+  p.Hq = q == nullptr ? 0 : Hq;
+  p.Hkv = Hkv;
+  p.T = T;
+  p.Smax = Smax;
+  p.A = n_axes;
+  p.table_rows = table_rows;
+  p.advance = advance != 0;
+  const cudaError_t e = td::launch_norm_append(elem_size(dtype), D, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
 td_status td_rope_append_attn(td_dtype dtype, const void *q, const void *k_new, const void *v_new, const float *cos_t,
                               const float *sin_t, void *k_cache, void *v_cache, int32_t *seq_lens, int B, int Hq,
                               int Hkv, int T, int Smax, int D, float scale, int split, int advance, void *out,

@@ -486,10 +486,6 @@ bool takes_rows(bool rope, int T, long long heads) {
   return T <= kF8RowsT && T <= (rope ? 1 + heads / 240 : 4 + heads / 50);
 }
 
-cudaError_t launch_advance(const AppendF8 &p, cudaStream_t stream) {
-  return launch_pdl(advance_f8_kernel, dim3((p.B + 255) / 256), dim3(256), 0, stream, p.seq_lens, p.B, p.T, p.Smax);
-}
-
 template <typename E, int D, bool ROPE>
 cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
   AppendF8 p = args;
@@ -505,7 +501,7 @@ cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
     if (apart) p.advance = 0;
     cudaError_t e = launch_pdl(append_f8_rows_kernel<E, D, ROPE>, dim3(p.B, (unsigned)(spread > 1024 ? 1024 : spread)),
                                dim3(32 * warps), 0, stream, p);
-    if (e == cudaSuccess && apart) e = launch_advance(p, stream);
+    if (e == cudaSuccess && apart) e = launch_advance(p.seq_lens, p.B, p.T, p.Smax, stream);
     return e;
   }
   const int block = 1 << p.block_log2;
@@ -528,7 +524,7 @@ cudaError_t launch(const AppendF8 &args, cudaStream_t stream) {
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess)
     e = launch_pdl(append_f8_tiles_kernel<E, D, ROPE>, dim3(nblk, groups, p.B), dim3(threads), smem, stream, p);
-  if (e == cudaSuccess && p.advance) e = launch_advance(p, stream);
+  if (e == cudaSuccess && p.advance) e = launch_advance(p.seq_lens, p.B, p.T, p.Smax, stream);
   return e;
 }
 
@@ -538,6 +534,10 @@ cudaError_t launch_d(const AppendF8 &p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_advance(int32_t *seq_lens, int B, int T, int Smax, cudaStream_t stream) {
+  return launch_pdl(advance_f8_kernel, dim3((B + 255) / 256), dim3(256), 0, stream, seq_lens, B, T, Smax);
+}
 
 cudaError_t launch_append_f8(size_t elem_bytes, int D, const AppendF8 &p, cudaStream_t stream) {
   cudaError_t e;

@@ -71,6 +71,27 @@ constexpr int kF8RowsT = 12;
 constexpr int kF8RowsThreads = 1024;
 cudaError_t launch_append_f8(size_t elem_bytes, int D, const AppendF8 &p, cudaStream_t stream);
 
+// seq_lens[b] += T for the sequences whose T rows fit, as a launch of its own after their append's.
+cudaError_t launch_advance(int32_t *seq_lens, int B, int T, int Smax, cudaStream_t stream);
+
+// Append to a cache of rows with the queries and keys normed and rotated first.
+struct NormAppend {
+  const void *q;   // [B, Hq, T, D] or null (Hq 0)
+  void *q_out;
+  const void *k_new, *v_new;  // [B, Hkv, T, D]
+  const float *q_weight, *k_weight;  // [D]
+  const float *cos_t, *sin_t;        // [table_rows, D / 2]
+  const int32_t *positions;   // [B, T, A] or null: row L + t
+  const int32_t *axes;        // [D / 2] or null: axis 0
+  void *k_cache, *v_cache;    // [B, Hkv, Smax, D]
+  int32_t *seq_lens;
+  uint32_t *status;
+  float eps;
+  int B, Hq, Hkv, T, Smax, A, table_rows, advance;
+  int tok, per_cta, head_groups;  // launch: tokens of a CTA, its heads, CTAs that share a token tile's heads
+};
+cudaError_t launch_norm_append(size_t elem_bytes, int D, const NormAppend &p, cudaStream_t stream);
+
 // Read-back of rows start[b] .. start[b] + N - 1 (start null: 0).
 struct ReadF8 {
   const uint8_t *k_codes, *v_codes;

@@ -68,6 +68,11 @@ int extent(const at::Tensor &t, int64_t d) {
   want(v <= 2147483647LL, PyExc_ValueError, "size out of range");
   return (int)v;
 }
+double real(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
 bool truth(PyObject *o) {
   const int v = PyObject_IsTrue(o);
   if (v < 0) throw Raised{};
@@ -199,6 +204,24 @@ int new_rows(const at::Tensor &k, const at::Tensor &v, const Cache &c) {
   return T;
 }
 
+// Rotation tables [rows, D/2] with positions [B, T, axes] and axes [D/2] or neither, checked; the axes' count.
+int turns(const at::Tensor &cos, const at::Tensor &sin, const at::Tensor *pos, const at::Tensor *axes, int B, int T,
+          int Smax, int D) {
+  want(cos.scalar_type() == at::kFloat && sin.scalar_type() == at::kFloat && cos.dim() == 2 && cos.size(1) == D / 2 &&
+           same_shape(sin, cos),
+       PyExc_TypeError, "rope tables must be float32 [rows, D/2], alike");
+  if (pos == nullptr) {
+    want(axes == nullptr, PyExc_ValueError, "axes need positions");
+    want(cos.size(0) >= Smax, PyExc_TypeError, "rope tables must have a row for every cache row");
+    return 0;
+  }
+  want(pos->scalar_type() == at::kInt && pos->dim() == 3 && pos->size(0) == B && pos->size(1) == T, PyExc_TypeError,
+       "positions must be int32 [B, T, axes]");
+  want(axes == nullptr || (axes->scalar_type() == at::kInt && shaped(*axes, {D / 2})), PyExc_TypeError,
+       "axes must be int32 [D/2]");
+  return extent(*pos, 2);
+}
+
 // append(k_new, v_new, <cache>, advance, dev_status, stream)
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t) {
   return guarded([&]() -> PyObject * {
@@ -228,21 +251,8 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     const at::Tensor *q_out = tensor_or_null(a[5]);
     const bool advance = truth(a[6]);
     const at::Tensor *st = status_word(a[7]);
-    want(cos.scalar_type() == at::kFloat && sin.scalar_type() == at::kFloat && cos.dim() == 2 &&
-             cos.size(1) == c.D / 2 && same_shape(sin, cos),
-         PyExc_TypeError, "rope tables must be float32 [rows, D/2], alike");
     const int rows = extent(cos, 0);
-    int A = 0;
-    if (pos != nullptr) {
-      want(pos->scalar_type() == at::kInt && pos->dim() == 3 && pos->size(0) == c.B && pos->size(1) == T, PyExc_TypeError,
-           "positions must be int32 [B, T, axes]");
-      A = extent(*pos, 2);
-      want(axes == nullptr || (axes->scalar_type() == at::kInt && shaped(*axes, {c.D / 2})), PyExc_TypeError,
-           "axes must be int32 [D/2]");
-    } else {
-      want(axes == nullptr, PyExc_ValueError, "axes need positions");
-      want(rows >= c.Smax, PyExc_TypeError, "rope tables must have a row for every cache row");
-    }
+    const int A = turns(cos, sin, pos, axes, c.B, T, c.Smax, c.D);
     int Hq = 0;
     if (q != nullptr) {
       want(q->dim() == 4 && q->size(0) == c.B && q->size(2) == T && q->size(3) == c.D &&
@@ -269,6 +279,57 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                                  place.stream()));
     if (q_out == nullptr) Py_RETURN_NONE;
     if (!made.defined()) return Py_NewRef(a[5]);
+    return wrap(made);
+  });
+}
+
+// norm_append(k_new, v_new, k_cache, v_cache, seq_lens, k_weight, cos_t, sin_t, eps, positions, axes, q, q_weight,
+// q_out, advance, dev_status, stream)
+PyObject *norm_append(PyObject *, PyObject *const *a, Py_ssize_t) {
+  return guarded([&]() -> PyObject * {
+    const at::Tensor &k = tensor(a[0]), &v = tensor(a[1]), &kc = tensor(a[2]), &vc = tensor(a[3]), &lens = tensor(a[4]);
+    const at::Tensor &kw = tensor(a[5]), &cos = tensor(a[6]), &sin = tensor(a[7]);
+    const double eps = real(a[8]);
+    const at::Tensor *pos = tensor_or_null(a[9]), *axes = tensor_or_null(a[10]), *q = tensor_or_null(a[11]);
+    const at::Tensor *qw = tensor_or_null(a[12]), *q_out = tensor_or_null(a[13]);
+    const bool advance = truth(a[14]);
+    const at::Tensor *st = status_word(a[15]);
+    want(k.dim() == 4 && same_shape(v, k) && kc.dim() == 4 && same_shape(vc, kc), PyExc_ValueError,
+         "new rows must be [B, Hkv, T, D] and caches [B, Hkv, Smax, D], K and V alike");
+    const int B = extent(k, 0), Hkv = extent(k, 1), T = extent(k, 2), D = extent(k, 3), Smax = extent(kc, 2);
+    want(shaped(kc, {B, Hkv, Smax, D}), PyExc_ValueError, "shape mismatch between new rows and caches");
+    const at::ScalarType type = k.scalar_type();
+    want(v.scalar_type() == type && kc.scalar_type() == type && vc.scalar_type() == type, PyExc_TypeError,
+         "new rows and caches must share a dtype");
+    const td_dtype dt = code(type);
+    want(lens.scalar_type() == at::kInt && shaped(lens, {B}), PyExc_TypeError, "seq_lens must be int32 [B]");
+    want(kw.scalar_type() == at::kFloat && shaped(kw, {D}), PyExc_TypeError, "k_weight must be float32 [D]");
+    const int A = turns(cos, sin, pos, axes, B, T, Smax, D);
+    int Hq = 0;
+    if (q != nullptr) {
+      want(q->dim() == 4 && q->size(0) == B && q->size(2) == T && q->size(3) == D && q->scalar_type() == type,
+           PyExc_ValueError, "q must be [B, Hq, T, D] in the new rows' dtype");
+      Hq = extent(*q, 1);
+      want(qw != nullptr && qw->scalar_type() == at::kFloat && shaped(*qw, {D}), PyExc_TypeError,
+           "q_weight must be float32 [D]");
+      want(q_out == nullptr || (same_shape(*q_out, *q) && q_out->scalar_type() == type), PyExc_TypeError,
+           "q_out must match q");
+    } else {
+      want(q_out == nullptr && qw == nullptr, PyExc_ValueError, "q_weight and q_out need q");
+    }
+    const Place place(device_of({&k, &v, &kc, &vc, &lens, &kw, &cos, &sin, pos, axes, q, qw, q_out, st}), a[16]);
+    at::Tensor made;
+    if (q != nullptr && q_out == nullptr) {
+      made = at::empty_like(*q);
+      q_out = &made;
+    }
+    checked("td_norm_rope_kv_append",
+            td_norm_rope_kv_append(dt, ptr<void>(q), ptr<void>(q_out), Hq, ptr<float>(qw), ptr<void>(k), ptr<void>(v),
+                                   ptr<float>(kw), (float)eps, ptr<float>(cos), ptr<float>(sin), extent(cos, 0),
+                                   ptr<int32_t>(pos), ptr<int32_t>(axes), A, ptr<void>(kc), ptr<void>(vc),
+                                   ptr<int32_t>(lens), B, Hkv, T, Smax, D, advance, ptr<uint32_t>(st), place.stream()));
+    if (q_out == nullptr) Py_RETURN_NONE;
+    if (!made.defined()) return Py_NewRef(a[13]);
     return wrap(made);
   });
 }
@@ -353,10 +414,7 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t) {
     const bool decode = q.dim() == 3;
     const char *name = decode ? "td_decode_attn_f8" : "td_verify_attn_f8";
     double scale = 1.0 / std::sqrt((double)c.D);
-    if (a[0] != Py_None) {
-      scale = PyFloat_AsDouble(a[0]);
-      if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
-    }
+    if (a[0] != Py_None) scale = real(a[0]);
     const int split = small(a[1]);
     const at::Tensor *out = tensor_or_null(a[2]), *lse = tensor_or_null(a[3]), *ws = tensor_or_null(a[4]);
     const at::Tensor *st = status_word(a[5]);
@@ -405,7 +463,7 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define TD_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&counted<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {TD_METHOD(append, 2 + kCache + 3), TD_METHOD(rope_append, 2 + kCache + 9),
+PyMethodDef methods[] = {TD_METHOD(append, 2 + kCache + 3), TD_METHOD(rope_append, 2 + kCache + 9), TD_METHOD(norm_append, 17),
                          TD_METHOD(read, kCache + 7), TD_METHOD(attn, 1 + kCache + 8), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_td_torch", "Native binding of the f8 calls.", -1, methods,

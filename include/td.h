@@ -207,6 +207,29 @@ td_status td_rope_kv_append(td_dtype dtype, const void *q, void *q_out, int Hq, 
                             int B, int Hkv, int T, int Smax, int D, int advance, uint32_t *dev_status, void *stream);
 
 /*
+ * td_rope_kv_append with every head's query and key row normed before the rotation (layers that norm
+ * queries and keys):
+ *   y = x * w / sqrt(mean_i x_i^2 + eps),  w = q_weight or k_weight, fp32 [D]
+ * (a weight kept as an offset from one is passed as 1 + offset), then the pairs turn as above; values
+ * are copied. All in fp32, rounded once into the element type. A NaN makes its row NaN; an infinity, or a
+ * sum of squares past fp32's range, is an infinite mean: finite elements become 0, infinite ones NaN.
+ * Pair i of token t turns by row P of the tables, fp32 [table_rows, D/2]:
+ *   positions NULL: P = L + t, the token's cache row (table_rows >= Smax);
+ *   else            P = positions[b, t, axes[i]], positions int32 [B, T, n_axes], axes int32 [D/2]
+ *                   (NULL: axis 0), n_axes 1 .. 16: a token behind a shared prefix, or the time, height
+ *                   and width of image and video tokens.
+ * A position outside [0, table_rows) or an axis outside [0, n_axes) leaves its pair normed but unrotated
+ * and sets TD_DEV_BAD_POSITION. eps > 0; D 64 or 128; q, q_out and q_weight all given or all NULL.
+ * q_out may be q. Overflow rule, advance and status bit as td_rope_kv_append. One launch, or with advance two
+ * (the second moves the lengths, unless one CTA holds a sequence's rows).
+ */
+td_status td_norm_rope_kv_append(td_dtype dtype, const void *q, void *q_out, int Hq, const float *q_weight,
+                                 const void *k_new, const void *v_new, const float *k_weight, float eps,
+                                 const float *cos_t, const float *sin_t, int table_rows, const int32_t *positions,
+                                 const int32_t *axes, int n_axes, void *k_cache, void *v_cache, int32_t *seq_lens, int B,
+                                 int Hkv, int T, int Smax, int D, int advance, uint32_t *dev_status, void *stream);
+
+/*
  * One layer's decode (T = 1) or verify (T > 1) step in one launch: for every b whose new rows
  * fit (0 <= L = seq_lens[b], L + T <= Smax), the result of
  *   td_rope_kv_append(q -> rotated q, k_new, v_new at L .. L+T-1)   (no rotation if cos_t is NULL)

@@ -1,0 +1,111 @@
+"""The normed append, windowed attention and shared-prefix attention without a GPU: what the C calls and
+the binding refuse before any launch."""
+import pytest
+import torch
+
+from decode_attention_split_gb300 import api
+from decode_attention_split_gb300 import build as td_build
+
+FAKE = 0x10000  # a 16-byte aligned address the host never dereferences
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    td_build.build()
+    from decode_attention_split_gb300 import _lib
+    return _lib.lib()
+
+
+def _call(fn, order, defaults, kw):
+    a = {**defaults, **kw}
+    return fn(*[a[k] for k in order])
+
+
+NORM = ("dtype", "q", "qo", "Hq", "qw", "kn", "vn", "kw", "eps", "cos", "sin", "rows", "pos", "axes", "A", "kc", "vc",
+        "sl", "B", "Hkv", "T", "Smax", "D", "adv", "st", "stream")
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(dtype=2), UNSUPPORTED),
+    (dict(kn=None), INVALID),
+    (dict(vc=None), INVALID),
+    (dict(kw=None), INVALID),
+    (dict(sl=None), INVALID),
+    (dict(sin=None), INVALID),
+    (dict(q=None), INVALID),                          # q_out without q
+    (dict(qo=None), INVALID),
+    (dict(qw=None), INVALID),
+    (dict(Hq=0), INVALID),
+    (dict(T=0), INVALID),
+    (dict(B=0), INVALID),
+    (dict(eps=0.0), INVALID),
+    (dict(eps=-1.0), INVALID),
+    (dict(eps=NAN), INVALID),
+    (dict(eps=float("inf")), INVALID),
+    (dict(rows=63), INVALID),                         # fewer table rows than cache rows
+    (dict(axes=FAKE), INVALID),                       # axes without positions
+    (dict(pos=FAKE, A=0, rows=1), INVALID),
+    (dict(pos=FAKE, A=2, rows=0), INVALID),
+    (dict(pos=FAKE, A=17, rows=8), UNSUPPORTED),
+    (dict(pos=FAKE + 2, A=2, rows=8), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED),
+    (dict(D=256), UNSUPPORTED),
+    (dict(B=65536), UNSUPPORTED),
+    (dict(T=(1 << 20) + 1), UNSUPPORTED),
+    (dict(Smax=(1 << 30) + 1, rows=(1 << 30) + 1), UNSUPPORTED),
+    (dict(Hkv=4097), UNSUPPORTED),
+    (dict(kn=FAKE + 8), UNSUPPORTED),
+    (dict(kw=FAKE + 4), UNSUPPORTED),
+    (dict(qw=FAKE + 4), UNSUPPORTED),
+    (dict(cos=FAKE + 4), UNSUPPORTED),
+    (dict(st=FAKE + 1), UNSUPPORTED),
+])
+def test_norm_append_refuses(lib, kw, expect):
+    d = dict(dtype=1, q=FAKE, qo=FAKE, Hq=4, qw=FAKE, kn=FAKE, vn=FAKE, kw=FAKE, eps=1e-6, cos=FAKE, sin=FAKE, rows=64,
+             pos=None, axes=None, A=0, kc=FAKE, vc=FAKE, sl=FAKE, B=2, Hkv=2, T=1, Smax=64, D=128, adv=1, st=None,
+             stream=None)
+    assert _call(lib.td_norm_rope_kv_append, NORM, d, kw) == expect
+
+
+def rows(*s, dtype=torch.bfloat16):
+    return torch.zeros(*s, dtype=dtype)
+
+
+def norm_args(**kw):
+    a = dict(k_new=rows(2, 2, 3, 128), v_new=rows(2, 2, 3, 128), k_cache=rows(2, 2, 64, 128),
+             v_cache=rows(2, 2, 64, 128), seq_lens=torch.zeros(2, dtype=torch.int32), k_weight=torch.ones(128),
+             cos_t=torch.zeros(64, 64), sin_t=torch.zeros(64, 64), q=rows(2, 4, 3, 128), q_weight=torch.ones(128))
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("kw,error", [
+    (dict(v_new=rows(2, 2, 4, 128)), ValueError),
+    (dict(k_cache=rows(2, 3, 64, 128), v_cache=rows(2, 3, 64, 128)), ValueError),
+    (dict(k_cache=torch.zeros(2, 2, 64, 128)), TypeError),
+    (dict(k_new=rows(2, 2, 3, 128, dtype=torch.float16), v_new=rows(2, 2, 3, 128, dtype=torch.float16),
+          k_cache=rows(2, 2, 64, 128, dtype=torch.float16), v_cache=rows(2, 2, 64, 128, dtype=torch.float16)), TypeError),
+    (dict(seq_lens=torch.zeros(2)), TypeError),
+    (dict(seq_lens=torch.zeros(3, dtype=torch.int32)), TypeError),
+    (dict(k_weight=rows(128)), TypeError),
+    (dict(k_weight=torch.ones(64)), TypeError),
+    (dict(q_weight=None), TypeError),
+    (dict(q=None), ValueError),
+    (dict(q=rows(2, 4, 2, 128)), ValueError),
+    (dict(q_out=rows(2, 4, 2, 128)), TypeError),
+    (dict(cos_t=torch.zeros(63, 64), sin_t=torch.zeros(63, 64)), TypeError),
+    (dict(cos_t=torch.zeros(64, 32), sin_t=torch.zeros(64, 32)), TypeError),
+    (dict(axes=torch.zeros(64, dtype=torch.int32)), ValueError),
+    (dict(positions=torch.zeros(2, 3, dtype=torch.int32)), TypeError),
+    (dict(positions=torch.zeros(2, 3, 2, dtype=torch.int64)), TypeError),
+    (dict(positions=torch.zeros(2, 3, 2, dtype=torch.int32), axes=torch.zeros(63, dtype=torch.int32)), TypeError),
+    (dict(eps="x"), TypeError),
+    (dict(dev_status=torch.zeros(1)), TypeError),
+    (dict(k_new=None), TypeError),
+    (dict(), ValueError),                             # all in order, but not on a GPU
+])
+def test_norm_append_binding_refuses(lib, kw, error):
+    with pytest.raises(error):
+        api.td_norm_rope_kv_append(**norm_args(**kw))
