@@ -88,7 +88,7 @@ struct NormAppend {
   uint32_t *status;
   float eps;
   int B, Hq, Hkv, T, Smax, A, table_rows, advance;
-  int tok, per_cta, head_groups;  // launch: tokens of a CTA, its heads, CTAs that share a token tile's heads
+  int per_cta, head_groups;  // a chunk's launch: heads of a CTA, CTAs that share a token tile
 };
 cudaError_t launch_norm_append(size_t elem_bytes, int D, const NormAppend &p, cudaStream_t stream);
 

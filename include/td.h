@@ -218,8 +218,8 @@ td_status td_rope_kv_append(td_dtype dtype, const void *q, void *q_out, int Hq, 
  *   else            P = positions[b, t, axes[i]], positions int32 [B, T, n_axes], axes int32 [D/2]
  *                   (NULL: axis 0), n_axes 1 .. 16: a token behind a shared prefix, or the time, height
  *                   and width of image and video tokens.
- * A position outside [0, table_rows) or an axis outside [0, n_axes) leaves its pair normed but unrotated
- * and sets TD_DEV_BAD_POSITION. eps > 0; D 64 or 128; q, q_out and q_weight all given or all NULL.
+ * A position outside [0, table_rows) or an axis outside [0, n_axes) turns its pair by no angle and sets
+ * TD_DEV_BAD_POSITION. eps > 0; D 64 or 128; q, q_out and q_weight all given or all NULL.
  * q_out may be q. Overflow rule, advance and status bit as td_rope_kv_append. One launch, or with advance two
  * (the second moves the lengths, unless one CTA holds a sequence's rows).
  */

@@ -157,7 +157,16 @@ def test_queries_of_a_sequence_that_does_not_fit_stay(td):
     p.check()
 
 
-@pytest.mark.parametrize("T", [1, 21])
+@pytest.mark.parametrize("T", [9, 100])
+def test_a_chunk_longer_than_the_cache_is_left_out(td, T):
+    """Its tokens have neither cache rows nor table rows."""
+    p = Problem("bf16", 128, T, 8, [0, 3])
+    g = p.call(td, inplace=True)
+    assert torch.equal(g["q"].cpu(), p.q)
+    p.check()
+
+
+@pytest.mark.parametrize("T", [1, 21, 50])
 def test_bad_positions_leave_their_pairs(td, T):
     p = Problem("bf16", 128, T, 64, [2, 30], A=3, rows=40)
     p.pos[0, T // 2, 1] = 40
@@ -165,7 +174,8 @@ def test_bad_positions_leave_their_pairs(td, T):
     p.axes[5] = 3
     p.axes[9] = -2
     g = p.call(td)
-    assert int(g["st"]) == td.DEV_BAD_POSITION
+    # the second sequence's 50 tokens do not fit behind its 30 rows
+    assert int(g["st"]) == td.DEV_BAD_POSITION | (td.DEV_APPEND_OVERFLOW if 30 + T > 64 else 0)
     p.check()
 
 

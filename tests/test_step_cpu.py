@@ -1,5 +1,7 @@
 """The normed append, windowed attention and shared-prefix attention without a GPU: what the C calls and
 the binding refuse before any launch."""
+import re
+
 import pytest
 import torch
 
@@ -109,3 +111,12 @@ def norm_args(**kw):
 def test_norm_append_binding_refuses(lib, kw, error):
     with pytest.raises(error):
         api.td_norm_rope_kv_append(**norm_args(**kw))
+
+
+def test_kernels_have_no_spills(lib):
+    """Register gate (ptxas), as for the other kernels."""
+    log = open(td_build.PTXAS_LOG).read()
+    entries = re.findall(r"Compiling entry function '(\w+)'.*?\n(?:.*?\n)*?\s+(\d+) bytes stack frame, (\d+) bytes "
+                         r"spill stores, (\d+) bytes spill loads", log)
+    for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4)):
+        assert [(int(st), int(ld)) for name, _, st, ld in entries if k in name] == [(0, 0)] * n, k
