@@ -20,6 +20,7 @@ from .api import (  # noqa: F401
     td_decode_attn,
     td_decode_attn_f8,
     td_decode_attn_q8,
+    td_decode_attn_window,
     td_decode_workspace_bytes,
     td_f8_workspace_bytes,
     td_kv_append,
@@ -29,6 +30,7 @@ from .api import (  # noqa: F401
     td_lse_merge,
     td_norm_rope_kv_append,
     td_prefill_attn,
+    td_prefill_attn_window,
     td_rope_append_attn,
     td_rope_kv_append,
     td_rope_kv_append_f8,
@@ -38,4 +40,6 @@ from .api import (  # noqa: F401
     td_verify_attn,
     td_verify_attn_f8,
     td_verify_attn_q8,
+    td_verify_attn_window,
+    td_window_workspace_bytes,
 )

@@ -34,6 +34,10 @@ SYMBOLS = (
     "td_decode_attn_f8",
     "td_verify_attn_f8",
     "td_prefill_attn",
+    "td_window_workspace_bytes",
+    "td_decode_attn_window",
+    "td_verify_attn_window",
+    "td_prefill_attn_window",
     "td_kv_append",
     "td_decode_attn",
     "td_verify_attn",
@@ -101,6 +105,14 @@ def _declare(lib):
     lib.td_verify_attn_f8.restype = i
     lib.td_prefill_attn.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, vp, vp, vp, vp]
     lib.td_prefill_attn.restype = i
+    lib.td_window_workspace_bytes.argtypes = [i] * 9
+    lib.td_window_workspace_bytes.restype = sz
+    lib.td_decode_attn_window.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, vp, vp, sz, vp, vp]
+    lib.td_decode_attn_window.restype = i
+    lib.td_verify_attn_window.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp, vp, vp, sz, vp, vp]
+    lib.td_verify_attn_window.restype = i
+    lib.td_prefill_attn_window.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp, vp, vp, vp]
+    lib.td_prefill_attn_window.restype = i
     lib.td_spec_accept.restype = i
     lib.td_kv_append.argtypes = [i, vp, vp, vp, vp, vp, i, i, i, i, i, i, vp, vp]
     lib.td_kv_append.restype = i

@@ -542,3 +542,41 @@ def td_prefill_attn(q, k_cache, v_cache, seq_lens, scale: float | None = None, o
                                    float(scale), _ptr(out), _ptr(lse), _ptr(dev_status), _stream(stream, dev))
     check("td_prefill_attn", st)
     return (out, lse) if (return_lse or lse is not None) else out
+
+
+# ------------------------------------------------------------------ sliding window with sinks
+
+def td_window_workspace_bytes(B: int, Hq: int, Hkv: int, Smax: int, D: int, window: int, sinks: int = 0, q_len: int = 1,
+                              split: int = 0) -> int:
+    """Workspace bytes td_decode_attn_window / td_verify_attn_window need on the current device (0 = invalid)."""
+    return int(lib().td_window_workspace_bytes(B, Hq, Hkv, Smax, D, q_len, window, sinks, split))
+
+
+def td_decode_attn_window(q, k_cache, v_cache, seq_lens, window: int, sinks: int = 0, scale: float | None = None,
+                          split: int = 0, out=None, lse=None, workspace=None, dev_status=None, stream=None,
+                          return_lse: bool = False):
+    """td_decode_attn over the last `window` keys and the first `sinks`: q [B,Hq,D] -> out [B,Hq,D] (+ lse [B,Hq])."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    return (_native or _load_native()).window_attn(q, k_cache, v_cache, seq_lens, window, sinks, scale, split, out, lse,
+                                                   workspace, dev_status, stream, return_lse)
+
+
+def td_verify_attn_window(q, k_cache, v_cache, seq_lens, window: int, sinks: int = 0, scale: float | None = None,
+                          split: int = 0, out=None, lse=None, workspace=None, dev_status=None, stream=None,
+                          return_lse: bool = False):
+    """td_verify_attn where the token at position P attends keys j <= P with j > P - window or j < sinks:
+    q [B,Hq,T,D] (seq_lens count the T new tokens) -> out [B,Hq,T,D] (+ lse [B,Hq,T])."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, T, D]")
+    return (_native or _load_native()).window_attn(q, k_cache, v_cache, seq_lens, window, sinks, scale, split, out, lse,
+                                                   workspace, dev_status, stream, return_lse)
+
+
+def td_prefill_attn_window(q, k_cache, v_cache, seq_lens, window: int, sinks: int = 0, scale: float | None = None,
+                           out=None, lse=None, dev_status=None, stream=None, return_lse: bool = False):
+    """td_prefill_attn over the same window: q [B,Hq,T,D] bf16 -> out [B,Hq,T,D] (+ lse [B,Hq,T])."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, T, D]")
+    return (_native or _load_native()).window_prefill(q, k_cache, v_cache, seq_lens, window, sinks, scale, out, lse,
+                                                      dev_status, stream, return_lse)

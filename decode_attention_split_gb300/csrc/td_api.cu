@@ -33,11 +33,11 @@ size_t elem_size(td_dtype d) { return d == TD_F32 ? 4 : 2; }
 td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens,
                   int B, int Hq, int Hkv, int T, int Smax, int D, float scale, int split, void *out, float *lse,
                   void *workspace, size_t workspace_bytes, uint32_t *dev_status, td::SplitPlan *plan,
-                  td::SplitParams *p, td::KvFormat format = td::KvFormat::kRows) {
+                  td::SplitParams *p, td::KvFormat format = td::KvFormat::kRows, int window = 0, int sinks = 0) {
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr || out == nullptr)
     return TD_ERR_INVALID_ARG;
   if (!isfinite(scale)) return TD_ERR_INVALID_ARG;
-  const td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, format);
+  const td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, format, window, sinks);
   if (st == TD_ERR_CUDA) return cuda_fail(cudaGetLastError());
   if (st != TD_OK) return st;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(seq_lens) ||
@@ -73,6 +73,17 @@ td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void
   p->warm_stages = plan->warm;
   p->qscale = scale * td::kLog2e;
   p->done = p->counters + plan->counters_n;
+  p->window = window;
+  p->sinks = sinks;
+  return TD_OK;
+}
+
+// A window's arguments: sizes past the cache's mean the whole cache. TD_OK or an error.
+td_status window_args(int Smax, int split, int *window, int *sinks) {
+  if (*window < 1 || *sinks < 0 || Smax < 1) return TD_ERR_INVALID_ARG;
+  if (split % 16 != 0) return TD_ERR_UNSUPPORTED;  // chunks start at multiples of 16 keys
+  if (*window > Smax) *window = Smax;
+  if (*sinks > Smax) *sinks = Smax;
   return TD_OK;
 }
 
@@ -173,6 +184,40 @@ td_status td_verify_attn(td_dtype dtype, const void *q, const void *k_cache, con
                          uint32_t *dev_status, void *stream) {
   return attn(dtype, q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, split, out, lse, workspace,
               workspace_bytes, dev_status, stream);
+}
+
+size_t td_window_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int window, int sinks, int split) {
+  if (window_args(Smax, split, &window, &sinks) != TD_OK) return 0;
+  size_t bytes = 0;
+  for (td_dtype dt : {TD_F32, TD_BF16}) {
+    td::SplitPlan plan;
+    if (td::plan_split(dt, B, Hq, Hkv, q_len, Smax, D, split, &plan, td::KvFormat::kRows, window, sinks) != TD_OK) return 0;
+    if (plan.bytes > bytes) bytes = plan.bytes;
+  }
+  return bytes;
+}
+
+td_status td_verify_attn_window(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax, int D, float scale,
+                                int window, int sinks, int split, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+  td_status st = window_args(Smax, split, &window, &sinks);
+  if (st != TD_OK) return st;
+  td::SplitPlan plan;
+  td::SplitParams p;
+  st = prepare(dtype, q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, split, out, lse, workspace,
+               workspace_bytes, dev_status, &plan, &p, td::KvFormat::kRows, window, sinks);
+  if (st != TD_OK) return st;
+  const cudaError_t e = td::launch_split(dtype, D, plan, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+td_status td_decode_attn_window(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D, float scale, int window,
+                                int sinks, int split, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                uint32_t *dev_status, void *stream) {
+  return td_verify_attn_window(dtype, q, k_cache, v_cache, seq_lens, B, Hq, Hkv, 1, Smax, D, scale, window, sinks, split,
+                               out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 td_status td_lse_merge(const float *m, const float *l, const float *acc, const int32_t *seq_lens, int B, int rows,
@@ -527,9 +572,11 @@ td_status td_decode_attn_f8(const void *q, const void *k_codes, const float *k_s
 
 }  // extern "C"
 
-extern "C" td_status td_prefill_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens,
-                                     int B, int Hq, int Hkv, int T, int Smax, int D, float scale, void *out, float *lse,
-                                     uint32_t *dev_status, void *stream) {
+namespace {
+
+td_status prefill(const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq,
+                  int Hkv, int T, int Smax, int D, float scale, int window, int sinks, void *out, float *lse,
+                  uint32_t *dev_status, void *stream) {
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr || out == nullptr)
     return TD_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Smax < 1 || Hq % Hkv != 0 || !isfinite(scale)) return TD_ERR_INVALID_ARG;
@@ -539,7 +586,25 @@ extern "C" td_status td_prefill_attn(const void *q, const void *k_cache, const v
       (lse != nullptr && !aligned4(lse)) || (dev_status != nullptr && !aligned4(dev_status)))
     return TD_ERR_UNSUPPORTED;
   const cudaError_t e = td::launch_prefill(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, out, lse,
-                                           dev_status, static_cast<cudaStream_t>(stream));
+                                           dev_status, static_cast<cudaStream_t>(stream), window, sinks);
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+}  // namespace
+
+extern "C" td_status td_prefill_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens,
+                                     int B, int Hq, int Hkv, int T, int Smax, int D, float scale, void *out, float *lse,
+                                     uint32_t *dev_status, void *stream) {
+  return prefill(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, 0, 0, out, lse, dev_status, stream);
+}
+
+extern "C" td_status td_prefill_attn_window(const void *q, const void *k_cache, const void *v_cache,
+                                            const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax, int D,
+                                            float scale, int window, int sinks, void *out, float *lse,
+                                            uint32_t *dev_status, void *stream) {
+  const td_status st = window_args(Smax, 0, &window, &sinks);
+  if (st != TD_OK) return st;
+  if (Smax > (1 << 30)) return TD_ERR_UNSUPPORTED;
+  return prefill(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, window, sinks, out, lse, dev_status, stream);
 }

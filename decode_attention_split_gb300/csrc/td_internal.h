@@ -29,6 +29,7 @@ struct SplitPlan {
   bool q8;       // int8 cache (codes + per-row scales): the quantised-cache kernel
   bool f8;       // block-scaled e4m3 cache: its kernel
   bool runs;     // its work cut into equal runs of stages instead of chunks
+  bool window;   // windowed attention: the kernels' WIN instantiations
   bool merge_apart;  // its partials merged by a second launch
   long long n_part;  // partial blocks in the workspace
   size_t off_pieces, off_part, bytes;  // workspace layout: counters, pieces (merge_apart), partial blocks
@@ -42,9 +43,13 @@ td_status cuda_fail(cudaError_t e);
 // scales, or e4m3 codes with per-block scales (q and out are bf16 for both, dtype TD_BF16).
 enum class KvFormat { kRows, kQ8, kF8 };
 
-// Fills *plan for the current device; TD_OK, or an error for unsupported shapes.
+// Fills *plan for the current device; TD_OK, or an error for unsupported shapes. window > 0: windowed attention
+// with so many sinks (both at most Smax).
 td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, int D, int split, SplitPlan *plan,
-                     KvFormat format = KvFormat::kRows);
+                     KvFormat format = KvFormat::kRows, int window = 0, int sinks = 0);
+
+// The windowed kernels' launch (td_split_window.cu).
+cudaError_t launch_split_window(td_dtype dtype, int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream);
 
 // The block-scaled kernel for row blocks of R rows: its function (for the occupancy query) and
 // dynamic shared memory, and its launch.
@@ -134,10 +139,11 @@ cudaError_t launch_spec_accept(const float *target, const float *draft, const in
                                int B, int G, int V, float temperature, int32_t *n_out, int32_t *tok_out,
                                uint32_t *status, void *workspace, cudaStream_t stream);
 
-// Tiled causal prefill attention on the tensor cores (tcgen05); bf16, D 64 or 128.
+// Tiled causal prefill attention on the tensor cores (tcgen05); bf16, D 64 or 128. window > 0: over a window with
+// so many sinks.
 cudaError_t launch_prefill(const void *q, const void *k, const void *v, const int32_t *seq_lens, int B, int Hq, int Hkv,
                            int T, int Smax, int D, float scale, void *out, float *lse, uint32_t *status,
-                           cudaStream_t stream);
+                           cudaStream_t stream, int window = 0, int sinks = 0);
 
 // SM count of the current device (cached per device).
 int device_sm_count(int device);

@@ -73,6 +73,7 @@ struct PfArgs {
   uint32_t *status;
   int B, Hq, Hkv, T, Smax;
   float qscale;      // scale * log2(e)
+  int window, sinks; // the WIN instantiation: keys j <= P with j > P - window or j < sinks
 };
 
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
@@ -167,11 +168,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
   tmem_st32(taddr, w);
 }
 
+// Which of a tile's 64 keys a row sees: the first `vis`, or with a window those whose bit is set.
+struct SeenFirst {
+  int vis;
+  __device__ __forceinline__ bool operator()(int i) const { return i < vis; }
+  __device__ __forceinline__ bool any() const { return vis > 0; }
+};
+struct SeenBits {
+  uint32_t lo, hi;
+  __device__ __forceinline__ bool operator()(int i) const { return ((i < 32 ? lo : hi) >> (i & 31)) & 1u; }
+  __device__ __forceinline__ bool any() const { return (lo | hi) != 0; }
+};
+// The low n of 32 bits (n any integer).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 // One row's probabilities 2^(s * qscale + nbase) for the 64 scores sv, packed in bf16 pairs
-// into pk; MASK: keys from `vis` on get 0. Returns their fp32 sum (in packed pairs, two
+// into pk; MASK: keys that the row does not see get 0. Returns their fp32 sum (in packed pairs, two
 // partial sums, so the additions do not form one chain).
-template <bool MASK>
-__device__ __forceinline__ float p_row(const float (&sv)[kPfKeys], float qscale, float nbase, int vis,
+template <bool MASK, typename Seen>
+__device__ __forceinline__ float p_row(const float (&sv)[kPfKeys], float qscale, float nbase, const Seen &seen,
                                        uint32_t (&pk)[kPfKeys / 2]) {
   float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 sc2 = make_float2(qscale, qscale), nb2 = make_float2(nbase, nbase);
@@ -180,8 +195,8 @@ __device__ __forceinline__ float p_row(const float (&sv)[kPfKeys], float qscale,
     const float2 x = ffma2(make_float2(sv[i], sv[i + 1]), sc2, nb2);
     float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
     if (MASK) {
-      pr.x = i < vis ? pr.x : 0.f;
-      pr.y = i + 1 < vis ? pr.y : 0.f;
+      pr.x = seen(i) ? pr.x : 0.f;
+      pr.y = seen(i + 1) ? pr.y : 0.f;
     }
     l2[(i >> 1) & 1] = fadd2(l2[(i >> 1) & 1], pr);
     pk[i / 2] = pack_bf16x2(pr.x, pr.y);
@@ -210,7 +225,23 @@ __device__ __forceinline__ uint32_t tile_chunk(int rows, int r, int c) {
   return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-template <int D>
+// What a row that sees keys below `lim` sees of the tile of keys from j0 on.
+template <bool WIN>
+__device__ __forceinline__ auto seen_of(const PfArgs &a, int j0, int lim) {
+  if constexpr (WIN) {
+    const int end = lim - j0, start = end - a.window, first = min(a.sinks, lim) - j0;
+    SeenBits s;
+    s.lo = (low_bits(end) & ~low_bits(start)) | low_bits(first);
+    s.hi = (low_bits(end - 32) & ~low_bits(start - 32)) | low_bits(first - 32);
+    return s;
+  } else {
+    return SeenFirst{min(kPfKeys, max(0, lim - j0))};
+  }
+}
+
+// WIN: attention over a sliding window with sinks. The key tiles are then those of the sinks and those from the first
+// row's window on; tiles that every row sees whole need no mask, as without a window.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_constant__ PfArgs a) {
   using C = PfCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -267,7 +298,13 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
   const int last_t = min(t0 + kPfRows, a.T) - 1;
   const int kend = max(0, min(L, L - a.T + last_t + 1));  // keys any row of the tile sees
   const int kall = max(0, min(L, L - a.T + t0 + 1));      // keys every row of the tile sees
-  const int nkt = (kend + kPfKeys - 1) / kPfKeys;
+  // tile i holds the keys from tile_key(i) on
+  const int ends = (kend + kPfKeys - 1) / kPfKeys;
+  const int head = WIN ? min((min(a.sinks, kend) + kPfKeys - 1) / kPfKeys, ends) : 0;  // tiles with sinks
+  const int win0 = WIN ? max(0, L - a.T + t0 - a.window + 1) : 0;  // first key in the first row's window
+  const int skip = WIN ? max(0, min(win0 / kPfKeys, ends) - head) : 0;  // tiles between the sinks and the window
+  const int nkt = ends - skip;
+  auto tile_key = [&](int i) { return (WIN && i >= head ? i + skip : i) * kPfKeys; };
   if (tid == 0 && qt == 0 && hq == 0) {
     uint32_t bits = 0;
     if (raw < 0) bits |= TD_DEV_NEGATIVE_SEQLEN;
@@ -350,7 +387,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
         const uint32_t dst = sb + (v ? C::V_OFF : C::K_OFF) + buf * C::KV_TILE;
         mbar_arrive_expect_tx(bar, C::KV_TILE);
 #pragma unroll
-        for (int h = 0; h < C::HALVES; ++h) tma3(dst + h * kKRegion, v ? &a.vmap : &a.kmap, 64 * h, kt * kPfKeys, zk, bar);
+        for (int h = 0; h < C::HALVES; ++h) tma3(dst + h * kKRegion, v ? &a.vmap : &a.kmap, 64 * h, tile_key(kt), zk, bar);
       };
       {
         const uint32_t bar = smem_u32(&bar_q);
@@ -394,11 +431,12 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
         break;
       }
       tc_fence_after();
-      const int j0 = kt * kPfKeys;
-      const int vrows = min(kPfKeys, L - j0);
-      if (vrows < kPfKeys) {
-        // V rows at or past the sequence's length, once landed: zeroed (a masked p of 0 must
-        // not meet a stale value)
+      const int j0 = tile_key(kt);
+      // V rows at or past the sequence's length (with a window: rows that none of the tile's
+      // queries sees), once landed: zeroed (a masked p of 0 must not meet a stale value)
+      const int vrows = min(kPfKeys, (WIN ? kend : L) - j0);
+      const int g0 = WIN ? max(a.sinks - j0, 0) : 0, g1 = WIN ? min(win0 - j0, kPfKeys) : 0;  // and [g0, g1)
+      if (vrows < kPfKeys || g0 < g1) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[b0]), ph))) {
           ok = false;
           break;
@@ -406,6 +444,10 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
         unsigned char *vt = smem + C::V_OFF + b0 * C::KV_TILE;
         for (int idx = tid; idx < (kPfKeys - vrows) * (D / 8); idx += 32 * kPfSoftmaxWarps) {
           const int r = vrows + idx / (D / 8), c = idx % (D / 8);
+          *reinterpret_cast<uint4 *>(vt + tile_chunk(kPfKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        for (int idx = tid; WIN && idx < (g1 - g0) * (D / 8); idx += 32 * kPfSoftmaxWarps) {
+          const int r = g0 + idx / (D / 8), c = idx % (D / 8);
           *reinterpret_cast<uint4 *>(vt + tile_chunk(kPfKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();  // read next by the tensor core (asynchronous proxy)
@@ -418,17 +460,17 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       if (lane == 0) mbar_arrive(smem_u32(&bar_sfree));
       // tiles short of every row's diagonal and of the sequence's end need no mask; in the
       // others, keys from `vis` on are masked (this row's visible keys of the tile)
-      const bool full = j0 + kPfKeys <= kall;
-      const int vis = full ? kPfKeys : min(kPfKeys, max(0, lim - j0));
+      const bool full = j0 + kPfKeys <= kall && (!WIN || j0 + kPfKeys <= a.sinks || j0 >= kend - a.window);
+      const auto seen = seen_of<WIN>(a, j0, lim);
       if (!full) {
 #pragma unroll
         for (int i = 0; i < kPfKeys; ++i)
-          if (i >= vis) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
+          if (!seen(i)) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
       }
       // the row maximum, scaled to base 2 (the scale's sign decides which extreme): eight
       // independent chains of three-input steps
       const float ext = qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv);
-      const float mx = vis > 0 ? ext * qscale : -INFINITY;
+      const float mx = full || seen.any() ? ext * qscale : -INFINITY;
       const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
       const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
       if (move) {
@@ -456,9 +498,9 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
       uint32_t pk[kPfKeys / 2];
       if (full)
-        l += p_row<false>(sv, qscale, nbase, vis, pk);
+        l += p_row<false>(sv, qscale, nbase, seen, pk);
       else
-        l += p_row<true>(sv, qscale, nbase, vis, pk);
+        l += p_row<true>(sv, qscale, nbase, seen, pk);
       if (kt >= 2) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_vfree[b0]), (uint32_t)((kt - 2) >> 1) & 1u))) {
           ok = false;
@@ -556,7 +598,7 @@ bool pf_map(CUtensorMap *m, const void *base, long long planes, int rows, int D,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_prefill_d(PfArgs &a, const void *q, const void *k, const void *v, cudaStream_t stream) {
   if (!pf_map(&a.qmap, q, (long long)a.B * a.Hq, a.T, D, kPfRows) ||
       !pf_map(&a.kmap, k, (long long)a.B * a.Hkv, a.Smax, D, kPfKeys) ||
@@ -565,19 +607,19 @@ cudaError_t launch_prefill_d(PfArgs &a, const void *q, const void *k, const void
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(reinterpret_cast<const void *>(&prefill_kernel<D>),
+    attr = cudaFuncSetAttribute(reinterpret_cast<const void *>(&prefill_kernel<D, WIN>),
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
   });
   if (attr != cudaSuccess) return attr;
   const dim3 grid((unsigned)(a.B * a.Hq), (unsigned)((a.T + kPfRows - 1) / kPfRows));
-  return launch_pdl(prefill_kernel<D>, grid, dim3(kPfThreads), PfCfg<D>::SMEM, stream, a);
+  return launch_pdl(prefill_kernel<D, WIN>, grid, dim3(kPfThreads), PfCfg<D>::SMEM, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_prefill(const void *q, const void *k, const void *v, const int32_t *seq_lens, int B, int Hq, int Hkv,
                            int T, int Smax, int D, float scale, void *out, float *lse, uint32_t *status,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, int window, int sinks) {
   PfArgs a;
   a.seq_lens = seq_lens;
   a.out = out;
@@ -589,7 +631,11 @@ cudaError_t launch_prefill(const void *q, const void *k, const void *v, const in
   a.T = T;
   a.Smax = Smax;
   a.qscale = scale * kLog2e;
-  return D == 64 ? launch_prefill_d<64>(a, q, k, v, stream) : launch_prefill_d<128>(a, q, k, v, stream);
+  a.window = window;
+  a.sinks = sinks;
+  if (window > 0)
+    return D == 64 ? launch_prefill_d<64, true>(a, q, k, v, stream) : launch_prefill_d<128, true>(a, q, k, v, stream);
+  return D == 64 ? launch_prefill_d<64, false>(a, q, k, v, stream) : launch_prefill_d<128, false>(a, q, k, v, stream);
 }
 
 }  // namespace td

@@ -76,21 +76,19 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
-namespace {
-
-// 3-D map over a bf16 cache [B*Hkv][Smax][D]: boxes of 64 columns (128 bytes) x 64 rows,
-// 128-byte swizzle, zero fill outside the tensor.
-bool encode_cache_map(CUtensorMap *map, const void *base, int B, int Hkv, int Smax, int D) {
+bool encode_cache_map(CUtensorMap *map, const void *base, int B, int Hkv, int Smax, int D, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Smax, (cuuint64_t)B * Hkv};
   const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Smax * D * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // The persistent kernel's instantiation for this launch: the tile by the rows; the plan made
 // before the wait for the previous kernel when one row block of at most 16 rows covers a kv
@@ -217,13 +215,6 @@ KernelRef q8_ref_of() {
   return KernelRef{reinterpret_cast<const void *>(&split_attn_q8_kernel<D, false, false>), smem, nullptr};
 }
 
-template <int D>
-constexpr int cluster_smem() {
-  return MmaCfg<D, kClusterStages<D>>::RING_BYTES + 1024;  // the ring plus alignment slack
-}
-static_assert(cluster_smem<128>() + 1024 <= 227 * 1024 && cluster_smem<64>() + 1024 <= 227 * 1024,
-              "cluster kernel shared memory");
-
 const void *cluster_fn(int D, int tile) {
   if (D == 64) {
     if (tile == kTileN8) return reinterpret_cast<const void *>(&split_attn_cluster_kernel<64, kTileN8>);
@@ -234,6 +225,8 @@ const void *cluster_fn(int D, int tile) {
   if (tile == kTileM16) return reinterpret_cast<const void *>(&split_attn_cluster_kernel<128, kTileM16>);
   return reinterpret_cast<const void *>(&split_attn_cluster_kernel<128, kTileN24>);
 }
+
+}  // namespace
 
 cudaLaunchConfig_t cluster_config(int D, int grid, int cs, cudaStream_t stream, cudaLaunchAttribute *attr) {
   cudaLaunchConfig_t cfg = {};
@@ -251,6 +244,8 @@ cudaLaunchConfig_t cluster_config(int D, int grid, int cs, cudaStream_t stream, 
   cfg.numAttrs = 2;
   return cfg;
 }
+
+namespace {
 
 template <int D>
 cudaError_t launch_cluster(const SplitParams &p, int grid, int cs, cudaStream_t stream) {
@@ -352,12 +347,18 @@ static int device_l2_bytes(int device) {
 }
 
 td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, int D, int split, SplitPlan *plan,
-                     KvFormat format) {
+                     KvFormat format, int window, int sinks) {
   const bool q8 = format == KvFormat::kQ8, f8 = format == KvFormat::kF8;
   if (dtype != TD_F32 && dtype != TD_BF16) return TD_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return TD_ERR_UNSUPPORTED;
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Smax < 1 || split < 0 || Hq % Hkv != 0) return TD_ERR_INVALID_ARG;
   if (B > TD_MAX_BATCH || Smax > (1 << 30) || T > Smax) return TD_ERR_UNSUPPORTED;
+  // keys that a sequence's chunks are cut from, at most (window_span)
+  const int most_keys = window == 0 ? Smax
+                        : Smax - T - window + 1 > sinks
+                            ? (dtype == TD_BF16 ? window_span<kWindowPad>(window, sinks, T, Smax).n
+                                                : window_span<1>(window, sinks, T, Smax).n)
+                            : Smax;
   const long long GT = (long long)(Hq / Hkv) * T;
   // bf16 caches: tensor-core kernels, the group's rows split evenly over row blocks of at most
   // 24 rows (tile_of_rows: up to 8 on the narrow n8 tile, 9 to 16 on one m16 tile, 17 to 24 on
@@ -409,9 +410,9 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   const long long p_target = slots - (spare ? (long long)B * U : 0);
   long long ns;
   if (split > 0) {
-    ns = ((long long)Smax + split - 1) / split;
+    ns = ((long long)most_keys + split - 1) / split;
   } else {
-    const long long by_size = ((long long)Smax + 15) / 16;
+    const long long by_size = ((long long)most_keys + 15) / 16;
     const long long by_grid = (p_target + U - 1) / U;
     ns = by_size < by_grid ? by_size : by_grid;
     if (ns < 1) ns = 1;
@@ -420,6 +421,7 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
   if (items_max >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
   // the block-scaled kernel counts stages, with a few units more a group, in 32 bits
   if (f8 && (long long)B * U * ((Smax + 127) / 128 + 8) >= (1LL << 31)) return TD_ERR_UNSUPPORTED;
+  plan->window = window > 0;
   plan->mma = mma;
   plan->q8 = q8;
   plan->f8 = f8;
@@ -481,7 +483,9 @@ td_status plan_split(td_dtype dtype, int B, int Hq, int Hkv, int T, int Smax, in
 
 cudaError_t launch_split(td_dtype dtype, int D, const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
   cudaError_t e;
-  if (plan.f8) {
+  if (plan.window) {
+    e = launch_split_window(dtype, D, plan, p, stream);
+  } else if (plan.f8) {
     e = launch_split_f8(D, plan, p, stream);
   } else if (plan.q8) {
     e = D == 64 ? launch_q8<64>(p, plan.grid, plan.smem, plan.spare, stream)

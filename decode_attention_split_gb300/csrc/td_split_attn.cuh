@@ -75,6 +75,7 @@ struct SplitParams {
   int runs, merge_apart, rounds;
   int n_part;           // partial blocks in the workspace
   int2 *pieces;         // merge_apart: of every group, its first block and how many it has
+  int window, sinks;    // windowed attention (the WIN instantiations): see WindowSpan
 };
 
 // Attended length of a sequence whose stored length is `raw`, with the status bits its
@@ -91,6 +92,36 @@ __device__ __forceinline__ int attended_len(const SplitParams &p, int32_t raw, u
   if (raw > p.Smax) bits |= TD_DEV_SEQLEN_CLAMPED;
   if (p.T > 1 && L < p.T) bits |= TD_DEV_VERIFY_SHORT;
   return L;
+}
+
+// Windowed attention: the query of token t, at position P = L - T + t, sees keys j <= P with j > P - window or
+// j < sinks. The T rows of a sequence see between them the sinks and the rows from the first row's window on. Where
+// there is a gap between the two, the kernels number the keys without it: sinks first, padded to `head` rows (a
+// multiple of PAD, so that the copies' boxes of PAD rows lie on one side of the gap), then cache rows head + shift,
+// head + shift + 1, ... Without a gap the numbers are the cache rows (head = shift = 0).
+struct WindowSpan {
+  int head, shift, n;  // n keys in all
+};
+template <int PAD>
+__host__ __device__ __forceinline__ WindowSpan window_span(int window, int sinks, int T, int L) {
+  const int first = L - T - window + 1;  // first key in the window of the first row (all are at most 2^30)
+  WindowSpan s;
+  s.head = first > sinks ? (sinks + PAD - 1) / PAD * PAD : 0;
+  s.shift = first > sinks ? first - s.head : 0;
+  s.n = L - s.shift;
+  return s;
+}
+// Keys that a sequence's chunks are cut from: WIN is 0 (no window: its L attended rows) or the PAD of a window.
+template <int WIN>
+__device__ __forceinline__ int keys_of(const SplitParams &p, int L) {
+  if constexpr (WIN == 0) return L;
+  else return window_span<WIN>(p.window, p.sinks, p.T, L).n;
+}
+// Whether a row whose keys end at number `hi` sees key number `key`.
+template <int WIN>
+__device__ __forceinline__ bool sees(int key, int hi, int window, int sinks) {
+  if constexpr (WIN == 0) return key < hi;
+  else return key < hi && (key >= hi - window || key < sinks);
 }
 
 // A chunk's partial result for its row block is R rows of part_row_floats(D) floats: acc[D]
@@ -131,6 +162,7 @@ struct SplitCfg {
 // Chunk size before the overshoot check of plan_items: the caller's split, or keys per item
 // so the items fill the grid once; then every sequence has at most ceil(p_target / U) chunks,
 // which is what the workspace holds (the guard on `longest` only restates that bound).
+template <int WIN = 0>
 __device__ __forceinline__ int first_chunk_size(const SplitParams &p, long long all, int longest) {
   if (p.split > 0) return p.split;
   const int U = p.Hkv * p.RB;
@@ -139,6 +171,7 @@ __device__ __forceinline__ int first_chunk_size(const SplitParams &p, long long 
   if (want < p.min_chunk) want = p.min_chunk;
   const long long fits = ((long long)longest + p.ns_ws - 1) / p.ns_ws;
   if (want < fits) want = fits;
+  if constexpr (WIN != 0) return (int)((want + 15) / 16 * 16);  // chunks start at multiples of 16 keys
   int S = (int)(want > p.Smax ? p.Smax : want);
   return S < 1 ? 1 : S;
 }
@@ -146,6 +179,7 @@ __device__ __forceinline__ int first_chunk_size(const SplitParams &p, long long 
 // Exclusive prefix over the per-sequence item counts, computed by the whole CTA.
 // s_len[b] receives the clamped length; returns the chunk size through *s_chunk and the
 // item total in s_prefix[B]. s_red holds 2 * kWarps values.
+template <int WIN = 0>
 static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red,
                                   bool report_bits = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -163,8 +197,8 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
       // them where that kernel's writes land, not through L1
       const int L = attended_len(p, report_bits ? p.seq_lens[b] : ld_relaxed(p.seq_lens + b), bits);
       s_len[b] = L;
-      tot += L;
-      lmax = max(lmax, L);
+      tot += keys_of<WIN>(p, L);
+      lmax = max(lmax, keys_of<WIN>(p, L));
     }
   }
   if (report_bits && blockIdx.x == 0) report(p.status, bits);
@@ -185,7 +219,7 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
     all += s_red[w];
     longest = max(longest, (int)s_red[kWarps + w]);
   }
-  int S = first_chunk_size(p, all, longest);  // the same value in every thread
+  int S = first_chunk_size<WIN>(p, all, longest);  // the same value in every thread
   // Per-thread segment sums of items, then a CTA-wide exclusive scan. With an automatic
   // chunk size, rounding each sequence's chunk count up can push the items past the grid,
   // leaving a second, mostly idle wave: then S grows, by the overshoot and by at least enough
@@ -196,7 +230,7 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
 #pragma unroll
     for (int i = 0; i < kSeg; ++i) {
       const int b = b0 + i;
-      if (b < p.B) seg += ((s_len[b] + S - 1) / S) * U;
+      if (b < p.B) seg += ((keys_of<WIN>(p, s_len[b]) + S - 1) / S) * U;
     }
     int incl = seg;
 #pragma unroll
@@ -215,7 +249,7 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
       const long long drop = ((long long)longest + n_long - 2) / (n_long - 1);
       if (grow < drop) grow = drop;
       grow = (grow + 15) / 16 * 16;
-      S = (int)(grow > p.Smax ? p.Smax : grow);
+      S = (int)(grow > p.Smax && WIN == 0 ? p.Smax : grow);
       continue;  // the same decision in every thread
     }
     int before = incl - seg;
@@ -225,7 +259,7 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
       const int b = b0 + i;
       if (b < p.B) {
         s_prefix[b] = before;
-        before += ((s_len[b] + S - 1) / S) * U;
+        before += ((keys_of<WIN>(p, s_len[b]) + S - 1) / S) * U;
       }
     }
     if (tid == 0) {
@@ -259,8 +293,9 @@ static __device__ bool lengths_unchanged(const SplitParams &p, const int *s_len)
 // length reads the same now: the plan is a function of those lengths alone. Otherwise it is made
 // again. Either way the status bits come from the lengths as read after the wait. Ends with a
 // __syncthreads.
+template <int WIN = 0>
 static __device__ void confirm_plan(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red) {
-  if (!lengths_unchanged(p, s_len)) plan_items(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
+  if (!lengths_unchanged(p, s_len)) plan_items<WIN>(p, s_len, s_prefix, s_chunk, s_red);  // ends with __syncthreads
 }
 
 // Fused step with advance: the last CTA of the grid to have read the lengths moves every
@@ -687,7 +722,8 @@ __device__ void finish_item(const SplitParams &p, float *smem_f, int smem_floats
   __syncthreads();
 }
 
-template <typename E, int D, int RP>
+// WIN: 1 for windowed attention (bulk copies of any rows: no padding), else 0.
+template <typename E, int D, int RP, int WIN = 0>
 __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitParams p) {
   using C = SplitCfg<E, D, RP>;
   extern __shared__ __align__(128) unsigned char smem[];
@@ -717,10 +753,10 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitPara
   }
   uint32_t merge_phase = 0;
   // a plan on the lengths as they read now, kept after the wait if they read the same then
-  plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
+  plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red, false);
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
-  confirm_plan(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+  confirm_plan<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
 
   const int S = s_chunk;
   const int W = s_prefix[p.B];
@@ -748,14 +784,17 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitPara
     }
     const int b = lo;
     const int L = s_len[b];
-    const int NC = (L + S - 1) / S;
+    const int keys = keys_of<WIN>(p, L);
+    const int NC = (keys + S - 1) / S;
     const int local = item - s_prefix[b];
     const int c = local % NC;
     const int rest = local / NC;
     const int rb = rest % p.RB;
     const int kvh = rest / p.RB;
     const int c0 = c * S;
-    const int c1 = min(c0 + S, L);
+    const int c1 = min(c0 + S, keys);
+    WindowSpan span = {};
+    if constexpr (WIN != 0) span = window_span<WIN>(p.window, p.sinks, p.T, L);
 
     // ---- this warp's slice of the chunk, in whole stages
     const int n = c1 - c0;
@@ -775,8 +814,22 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitPara
       unsigned char *dst = ring + st * C::STAGE_BYTES;
       fence_proxy_async_smem();
       mbar_arrive_expect_tx(bar, 2 * bytes);
-      bulk_g2s(smem_u32(dst), kg + (size_t)j0 * C::ROW_BYTES, bytes, bar, policy);
-      bulk_g2s(smem_u32(dst + C::TILE_BYTES), vg + (size_t)j0 * C::ROW_BYTES, bytes, bar, policy);
+      if constexpr (WIN != 0) {
+        // keys below the head are the sinks' rows; the others' rows are shifted
+        const uint32_t low = (uint32_t)min(max(span.head - j0, 0), min(C::TKW, w1 - j0)) * C::ROW_BYTES;
+        if (low > 0) {
+          bulk_g2s(smem_u32(dst), kg + (size_t)j0 * C::ROW_BYTES, low, bar, policy);
+          bulk_g2s(smem_u32(dst + C::TILE_BYTES), vg + (size_t)j0 * C::ROW_BYTES, low, bar, policy);
+        }
+        if (low < bytes) {
+          const size_t from = (size_t)(j0 + span.shift) * C::ROW_BYTES + low;
+          bulk_g2s(smem_u32(dst) + low, kg + from, bytes - low, bar, policy);
+          bulk_g2s(smem_u32(dst + C::TILE_BYTES) + low, vg + from, bytes - low, bar, policy);
+        }
+      } else {
+        bulk_g2s(smem_u32(dst), kg + (size_t)j0 * C::ROW_BYTES, bytes, bar, policy);
+        bulk_g2s(smem_u32(dst + C::TILE_BYTES), vg + (size_t)j0 * C::ROW_BYTES, bytes, bar, policy);
+      }
     };
     if (lane == 0) {
       for (int i = 0; i < min(kStages, ntiles); ++i) issue(i);
@@ -791,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitPara
       const bool valid = r < p.R && gr < GT;
       const int hq = kvh * p.G + gr / p.T;
       const int t = gr % p.T;
-      nvis[r] = valid ? max(L - p.T + t + 1, 0) : 0;
+      nvis[r] = valid ? max(L - p.T + t + 1 - span.shift, 0) : 0;
       const unsigned char *qrow =
           static_cast<const unsigned char *>(p.q) + (((size_t)b * p.Hq + hq) * p.T + t) * C::ROW_BYTES;
 #pragma unroll
@@ -866,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_kernel(const SplitPara
         }
         const int kk = kb0 + (sub / RP) * 4 + g8;  // key (within the stage) of this lane's score
         const int j = j0 + kk;
-        const bool valid = kk < nk && j < my_nvis;
+        const bool valid = kk < nk && sees<WIN>(j, my_nvis, p.window, p.sinks);
         const float sc = valid ? part[0] : -INFINITY;
         float bm = sc;
 #pragma unroll

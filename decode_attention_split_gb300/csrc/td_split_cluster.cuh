@@ -18,9 +18,10 @@
 
 namespace td {
 
-// TILE: the warps' step for the group's rows (tile_of_rows).
-template <int D, int TILE = kTileM16>
-__global__ void __launch_bounds__(kThreads, 1) split_attn_cluster_kernel(const __grid_constant__ MmaArgs a) {
+// TILE: the warps' step for the group's rows (tile_of_rows). WIN: kWindowPad for windowed attention, else 0.
+template <int D, int TILE = kTileM16, int WIN = 0>
+__global__ void __launch_bounds__(kThreads, 1)
+    split_attn_cluster_kernel(const __grid_constant__ typename MmaArgsOf<WIN>::type a) {
   constexpr int NST = kClusterStages<D>;
   constexpr int D4 = D / 4;
   constexpr int TR = tile_rows<TILE>();
@@ -54,9 +55,13 @@ __global__ void __launch_bounds__(kThreads, 1) split_attn_cluster_kernel(const _
     // prefetch_first_item): warm L2 with its first stages
     uint32_t guess_bits = 0;
     const int Lg = attended_len(p, ld_relaxed(p.seq_lens + b), guess_bits);
-    const int Sg = ((Lg + CS - 1) / CS + C::TK - 1) / C::TK * C::TK;
-    const int g0 = min((int)rank * Sg, Lg);
-    prefetch_chunk_l2<D>(p, b, kvh, g0, min(g0 + Sg, Lg), prefetch_stages(p));
+    const int keys = keys_of<WIN>(p, Lg);
+    const int Sg = ((keys + CS - 1) / CS + C::TK - 1) / C::TK * C::TK;
+    const int g0 = min((int)rank * Sg, keys);
+    if constexpr (WIN != 0)
+      prefetch_window_l2<D>(p, b, kvh, Lg, g0, min(g0 + Sg, keys), prefetch_stages(p));
+    else
+      prefetch_chunk_l2<D>(p, b, kvh, g0, min(g0 + Sg, keys), prefetch_stages(p));
   }
   griddep_wait();  // seq_lens and the cache may come from the previous kernel in the stream
   griddep_launch_dependents();
@@ -66,11 +71,12 @@ __global__ void __launch_bounds__(kThreads, 1) split_attn_cluster_kernel(const _
   __syncthreads();  // barrier initialisation is visible before any wait
   advance_after_reads(p, &s_flag);  // fused step: the lengths move on once every CTA has read them
   // chunk of this CTA: whole 64-key stages, the group's keys spread over the cluster
-  const int S = ((L + CS - 1) / CS + C::TK - 1) / C::TK * C::TK;
-  const int c0 = min((int)rank * S, L);
-  const int c1 = min(c0 + S, L);
+  const int keys = keys_of<WIN>(p, L);
+  const int S = ((keys + CS - 1) / CS + C::TK - 1) / C::TK * C::TK;
+  const int c0 = min((int)rank * S, keys);
+  const int c1 = min(c0 + S, keys);
   uint32_t seq = 0;
-  stream_chunk<D, NST, TILE>(a, smem, s_bars, seq, b, kvh, rb, L, c0, c1);
+  stream_chunk<D, NST, TILE, WIN>(a, smem, s_bars, seq, b, kvh, rb, L, c0, c1);
   const float *combine = reinterpret_cast<const float *>(smem);
   float *blk = reinterpret_cast<float *>(smem) + combine_floats<D, TILE>();  // acc[R][D], m[R], l[R]
   combine_block<D, TR>(combine, blk, R, nv);
@@ -125,5 +131,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_attn_cluster_kernel(const _
   }
   cluster_sync_all();  // no CTA leaves while CTA 0 may still read its shared memory
 }
+
+template <int D>
+constexpr int cluster_smem() {
+  return MmaCfg<D, kClusterStages<D>>::RING_BYTES + 1024;  // the ring plus alignment slack
+}
+static_assert(cluster_smem<128>() + 1024 <= 227 * 1024 && cluster_smem<64>() + 1024 <= 227 * 1024,
+              "cluster kernel shared memory");
+// Launch of `grid` CTAs in clusters of `cs`; attr holds two attributes.
+cudaLaunchConfig_t cluster_config(int D, int grid, int cs, cudaStream_t stream, cudaLaunchAttribute *attr);
 
 }  // namespace td

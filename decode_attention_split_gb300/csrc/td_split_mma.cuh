@@ -42,6 +42,9 @@ constexpr int kMmaRows = 16;  // query rows per CTA: one m16 tile
 
 // The driver's tensor-map encoder; null without a driver.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+// 3-D map over a bf16 cache [B*Hkv][Smax][D]: boxes of 64 columns (128 bytes) x box_rows rows,
+// 128-byte swizzle, zero fill outside the tensor.
+bool encode_cache_map(CUtensorMap *map, const void *base, int B, int Hkv, int Smax, int D, int box_rows = 64);
 
 // Tile of a warp's 16-key step, by the query rows of a row block:
 //   kTileN8   at most 8 rows: keys on the m side, the rows on one 8-wide n tile (warp_keys16_n8);
@@ -104,6 +107,20 @@ struct MmaArgs {
   CUtensorMap kmap;
   CUtensorMap vmap;
   SplitParams p;
+};
+// Windowed attention: also maps with boxes of 16 rows, for the stages that hold sinks.
+struct MmaWindowArgs : MmaArgs {
+  CUtensorMap kmap16;
+  CUtensorMap vmap16;
+};
+constexpr int kWindowPad = 16;  // the tensor-core kernels' WIN
+template <int WIN>
+struct MmaArgsOf {
+  using type = MmaArgs;
+};
+template <>
+struct MmaArgsOf<kWindowPad> {
+  using type = MmaWindowArgs;
 };
 
 // Byte offset of 16-byte chunk `ch` of row `row` in the query tile (row-major, chunks XOR-ed
@@ -192,10 +209,10 @@ constexpr float kMaxGap = 8.f;
 // the stage's tiles): S = Q K^T over two 8-key n tiles, masking by the rows' visible-key
 // limits `lim`, the online softmax in base 2, then O += P V. kt / vt address bf16 K / V
 // tiles in the TMA-swizzled layout.
-template <int D>
+template <int D, int WIN = 0>
 __device__ __forceinline__ void warp_keys16(const uint32_t (&qa)[D / 16][4], uint32_t kt, uint32_t vt, int kr,
                                             int key0, const int (&lim)[2], float qscale, float (&o)[D / 8][4],
-                                            float (&m_run)[2], float (&l_run)[2]) {
+                                            float (&m_run)[2], float (&l_run)[2], int window = 0, int sinks = 0) {
   constexpr int TK = 64, KSD = D / 16, NTD = D / 8;
   const int lane = threadIdx.x & 31, tig = lane & 3;
   float sc[2][4];
@@ -220,7 +237,7 @@ __device__ __forceinline__ void warp_keys16(const uint32_t (&qa)[D / 16][4], uin
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = key0 + nt * 8 + 2 * tig + e;
-        const float v = key < lim[h] ? sc[nt][2 * h + e] * qscale : -INFINITY;
+        const float v = sees<WIN>(key, lim[h], window, sinks) ? sc[nt][2 * h + e] * qscale : -INFINITY;
         sc[nt][2 * h + e] = v;
         mx = fmaxf(mx, v);
       }
@@ -276,10 +293,10 @@ __device__ __forceinline__ void warp_keys16(const uint32_t (&qa)[D / 16][4], uin
 // run over the 8 lanes of one tig. Half the tensor-core tiles, exponentials and output
 // registers of warp_keys16 when a kv head has 8 query rows or fewer (decode with grouped
 // heads). o[dt] holds O^T of dims 16*dt + gid (+8) and rows 2*tig (+1).
-template <int D>
+template <int D, int WIN = 0>
 __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], uint32_t kt, uint32_t vt, int kr,
                                                int key0, const int (&lim)[2], float qscale, float (&o)[D / 16][4],
-                                               float (&m_run)[2], float (&l_run)[2]) {
+                                               float (&m_run)[2], float (&l_run)[2], int window = 0, int sinks = 0) {
   constexpr int TK = 64, KSD = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
   // two accumulators (even and odd k steps) halve the dependent chain of tensor-core tiles
@@ -301,7 +318,7 @@ __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], 
 #pragma unroll
     for (int hk = 0; hk < 2; ++hk) {
       const int key = key0 + gid + 8 * hk;
-      sc[2 * hk + e] = key < lim[e] ? sc[2 * hk + e] * qscale : -INFINITY;
+      sc[2 * hk + e] = sees<WIN>(key, lim[e], window, sinks) ? sc[2 * hk + e] * qscale : -INFINITY;
     }
     float mx = fmaxf(sc[e], sc[2 + e]);
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -343,10 +360,10 @@ __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], 
 // 24 rows. A thread holds keys gid and gid + 8 of rows 8 nt + 2 tig (+1) of each tile, i.e. six
 // rows, reduced over the 8 lanes that share a tig. o[nt][dt] holds O^T of dims 16 dt + gid (+8)
 // and rows 8 nt + 2 tig (+1); the row limits, maxima and sums are indexed 2 nt + e.
-template <int D>
+template <int D, int WIN = 0>
 __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][2], uint32_t kt, uint32_t vt, int kr,
                                                 int key0, const int (&lim)[6], float qscale, float (&o)[3][D / 16][4],
-                                                float (&m_run)[6], float (&l_run)[6]) {
+                                                float (&m_run)[6], float (&l_run)[6], int window = 0, int sinks = 0) {
   constexpr int TK = 64, KSD = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
   // three independent accumulators, one per n tile
@@ -372,7 +389,7 @@ __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][
 #pragma unroll
       for (int hk = 0; hk < 2; ++hk) {
         const int key = key0 + gid + 8 * hk;
-        sc[nt][2 * hk + e] = key < lim[ri] ? sc[nt][2 * hk + e] * qscale : -INFINITY;
+        sc[nt][2 * hk + e] = sees<WIN>(key, lim[ri], window, sinks) ? sc[nt][2 * hk + e] * qscale : -INFINITY;
       }
       float mx = fmaxf(sc[nt][e], sc[nt][2 + e]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -430,9 +447,10 @@ __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][
 // Returns false, CTA-uniformly, if a copy never completed: the status bit is set, the other
 // copies in flight have been waited for, and the combine area holds empty partials.
 // Ends with a __syncthreads.
-template <int D, int NST, int TILE = kTileM16>
-__device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_bars, uint32_t &seq, int b, int kvh,
-                             int rb, int L, int c0, int c1) {
+// WIN (kWindowPad): windowed attention, keys [c0, c1) in the numbers of window_span, c0 a multiple of 16.
+template <int D, int NST, int TILE = kTileM16, int WIN = 0>
+__device__ bool stream_chunk(const typename MmaArgsOf<WIN>::type &a, unsigned char *smem, uint64_t *s_bars, uint32_t &seq,
+                             int b, int kvh, int rb, int L, int c0, int c1) {
   using C = MmaCfg<D, NST>;
   constexpr int TR = tile_rows<TILE>();
   constexpr bool KEYS_ON_M = TILE != kTileM16;       // the narrow layouts
@@ -446,6 +464,8 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
   const int nstages = (c1 - c0 + C::TK - 1) / C::TK;
   const int zc = b * p.Hkv + kvh;  // tensor-map coordinate of this (sequence, kv head)
   const uint64_t policy = l2_evict_first_policy();
+  WindowSpan span = {};
+  if constexpr (WIN != 0) span = window_span<WIN>(p.window, p.sinks, p.T, L);
 
   // stage sidx goes to ring buffer (seq + sidx) % NST
   auto issue = [&](int sidx) {
@@ -453,9 +473,25 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
     const uint32_t bar = smem_u32(&s_bars[buf]);
     const uint32_t kdst = sbase + buf * C::STAGE_BYTES;
     const uint32_t vdst = kdst + C::TILE_BYTES;
-    const int y = c0 + sidx * C::TK;
+    int y = c0 + sidx * C::TK;
     fence_proxy_async_smem();
     mbar_arrive_expect_tx(bar, 2 * C::TILE_BYTES);
+    if constexpr (WIN != 0) {
+      if (y < span.head) {
+        // 16 rows at a time, the sinks' or the window's
+        for (int i = 0; i < C::TK / 16; ++i) {
+          const int at = y + 16 * i, row = at < span.head ? at : at + span.shift;
+#pragma unroll
+          for (int h = 0; h < C::HALVES; ++h) {
+            const uint32_t off = h * C::BOX_BYTES + i * 16 * 128;
+            tma_load_3d(kdst + off, &a.kmap16, 64 * h, row, zc, bar, policy);
+            tma_load_3d(vdst + off, &a.vmap16, 64 * h, row, zc, bar, policy);
+          }
+        }
+        return;
+      }
+      y += span.shift;
+    }
 #pragma unroll
     for (int h = 0; h < C::HALVES; ++h) {
       tma_load_3d(kdst + h * C::BOX_BYTES, &a.kmap, 64 * h, y, zc, bar, policy);
@@ -510,7 +546,10 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
     const int r = KEYS_ON_M ? 8 * (h >> 1) + 2 * tig + (h & 1) : gid + 8 * h;
     const int gr = rb * p.R + r;
     const bool valid = r < p.R && gr < GT;
-    lim[h] = valid ? min(max(L - p.T + gr % p.T + 1, 0), c1) : 0;
+    if constexpr (WIN != 0)
+      lim[h] = valid ? max(L - p.T + gr % p.T + 1 - span.shift, 0) : 0;  // the window's start follows from it
+    else
+      lim[h] = valid ? min(max(L - p.T + gr % p.T + 1, 0), c1) : 0;
   }
   // query rows as mma A fragments (narrow: B fragments of each n tile), read once the first
   // stage lands
@@ -544,7 +583,19 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
       }
       fence_proxy_async_smem();  // these writes precede the buffer's next refill by the TMA unit
     }
-    if (landed && p.k_new != nullptr) place_new_rows<D, NST>(p, smem + buf * C::STAGE_BYTES, b, kvh, rb, L, j0, valid);
+    if constexpr (WIN != 0) {
+      // the V rows of the head's padding, which no row sees, likewise
+      const int r0 = max(p.sinks - j0, 0), r1 = min(span.head - j0, C::TK);
+      if (landed && r0 < r1) {
+        unsigned char *vrow = smem + buf * C::STAGE_BYTES + C::TILE_BYTES;
+        for (int idx = tid; idx < (r1 - r0) * C::NCH; idx += kThreads) {
+          const int r = r0 + idx / C::NCH, ch = idx % C::NCH;
+          *reinterpret_cast<uint4 *>(vrow + tma_swz<C::TK>(r, ch)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+    }
+    if (WIN == 0 && landed && p.k_new != nullptr) place_new_rows<D, NST>(p, smem + buf * C::STAGE_BYTES, b, kvh, rb, L, j0, valid);
     if (st == 0) cp_async_wait<0>();  // this thread's part of the query tile
     // one decision for the whole CTA: a thread whose wait gave up stops every thread
     if (!__syncthreads_and(landed)) {
@@ -578,11 +629,11 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
     const int key0 = j0 + kr;
     if (key0 < c1) {
       if constexpr (TILE == kTileN24)
-        warp_keys16_n24<D>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run);
+        warp_keys16_n24<D, WIN>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
       else if constexpr (TILE == kTileN8)
-        warp_keys16_n8<D>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run);
+        warp_keys16_n8<D, WIN>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
       else
-        warp_keys16<D>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run);
+        warp_keys16<D, WIN>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
     }
     consumed = st + 1;
   }
@@ -656,7 +707,8 @@ __device__ bool stream_chunk(const MmaArgs &a, unsigned char *smem, uint64_t *s_
 // (their block scales are a few lines).
 enum : int { kWarmRows = 0, kWarmQ8 = 1, kWarmF8 = 2 };
 
-// Warms L2 with the first `n` stages (of 64 rows) of K and V of keys [c0, c1) of (b, kvh).
+// Warms L2 with the first `n` stages (of 64 rows) of K and V of keys [c0, c1) of (b, kvh) (rows; of a window's keys, those
+// behind the sinks).
 template <int D, int WARM = kWarmRows>
 __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, int c1, int n) {
   constexpr int ROWB = WARM != kWarmRows ? D : D * 2, TK = 64;
@@ -683,6 +735,14 @@ __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, 
   }
 }
 
+// The same for keys [c0, c1) in the numbers of window_span: the rows of those behind the sinks (a few).
+template <int D>
+__device__ void prefetch_window_l2(const SplitParams &p, int b, int kvh, int L, int c0, int c1, int n) {
+  const WindowSpan span = window_span<kWindowPad>(p.window, p.sinks, p.T, L);
+  const int from = max(c0, span.head);
+  if (from < c1) prefetch_chunk_l2<D>(p, b, kvh, from + span.shift, c1 + span.shift, n);
+}
+
 // Run by one thread before the wait for the previous kernel in the stream, whose writes
 // (seq_lens among them) may not be visible yet: a guess of this CTA's first work item from
 // the lengths as they read now, the same arithmetic as plan_items without its overshoot
@@ -691,7 +751,7 @@ __device__ void prefetch_chunk_l2(const SplitParams &p, int b, int kvh, int c0, 
 // prefetch, and the real plan is made after the wait. Batches of up to 8 sequences.
 // `item` is the CTA's first work item; a cluster of `parts` CTAs shares each item, this CTA
 // taking run `part` of its whole 64-key stages (as split_attn_cc_kernel cuts it).
-template <int D, int WARM = kWarmRows>
+template <int D, int WARM = kWarmRows, int WIN = 0>
 __device__ void prefetch_first_item(const SplitParams &p, int n, int item, int part = 0, int parts = 1) {
   if (p.B > 8) return;
   long long all = 0;
@@ -700,18 +760,23 @@ __device__ void prefetch_first_item(const SplitParams &p, int n, int item, int p
   for (int b = 0; b < p.B; ++b) {
     const int L = attended_len(p, ld_relaxed(p.seq_lens + b), bits);
     if (b == 0) first = L;
-    all += L;
-    longest = max(longest, L);
+    all += keys_of<WIN>(p, L);
+    longest = max(longest, keys_of<WIN>(p, L));
   }
-  const int S = first_chunk_size(p, all, longest);
+  const int S = first_chunk_size<WIN>(p, all, longest);
   const int U = p.Hkv * p.RB;
   for (int b = 0; b < p.B; ++b) {
     // (a second read of the later lengths: still a guess)
     const int L = b == 0 ? first : attended_len(p, ld_relaxed(p.seq_lens + b), bits);
-    const int NC = (L + S - 1) / S;
+    const int keys = keys_of<WIN>(p, L);
+    const int NC = (keys + S - 1) / S;
     if (item < NC * U) {
       const int c = item % NC, kvh = item / NC / p.RB;
-      const int c0 = c * S, c1 = min(c0 + S, L);
+      const int c0 = c * S, c1 = min(c0 + S, keys);
+      if constexpr (WIN != 0) {
+        prefetch_window_l2<D>(p, b, kvh, L, c0, c1, n);
+        return;
+      }
       const int per = ((c1 - c0 + parts - 1) / parts + 63) / 64 * 64;
       const int r0 = min(c0 + part * per, c1);
       prefetch_chunk_l2<D, WARM>(p, b, kvh, r0, min(r0 + per, c1), n);
@@ -734,8 +799,10 @@ __device__ __forceinline__ unsigned char *align1024(unsigned char *p) {
 // they read the same then (measured on the 3B-style layer: 4k 11.4 -> 10.5 us, 32k 25.7 ->
 // 25.5 us). The other instantiation plans after the wait. TILE: the warps' step for the row
 // block's rows (tile_of_rows).
-template <int D, bool EARLY_PLAN, int TILE = kTileM16>
-__global__ void __launch_bounds__(kThreads, 2) split_attn_mma_kernel(const __grid_constant__ MmaArgs a) {
+// WIN: kWindowPad for windowed attention, else 0.
+template <int D, bool EARLY_PLAN, int TILE = kTileM16, int WIN = 0>
+__global__ void __launch_bounds__(kThreads, 2)
+    split_attn_mma_kernel(const __grid_constant__ typename MmaArgsOf<WIN>::type a) {
   constexpr int NST = kPersistentStages<D>;
   using C = MmaCfg<D, NST>;
   using E = __nv_bfloat16;
@@ -762,14 +829,14 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_mma_kernel(const __gri
   }
   uint32_t merge_phase = 0;
   uint32_t seq = 0;
-  if (tid == 0) prefetch_first_item<D>(p, prefetch_stages(p), blockIdx.x);
-  if constexpr (EARLY_PLAN) plan_items(p, s_len, s_prefix, &s_chunk, s_red, false);
+  if (tid == 0) prefetch_first_item<D, kWarmRows, WIN>(p, prefetch_stages(p), blockIdx.x);
+  if constexpr (EARLY_PLAN) plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red, false);
   griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   if constexpr (EARLY_PLAN)
-    confirm_plan(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+    confirm_plan<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   else
-    plan_items(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+    plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   advance_after_reads(p, &s_last);  // fused step: the lengths move on once every CTA has read them
   const int S = s_chunk;
   const int W = s_prefix[p.B];
@@ -792,14 +859,15 @@ __global__ void __launch_bounds__(kThreads, 2) split_attn_mma_kernel(const __gri
     }
     const int b = lo;
     const int L = s_len[b];
-    const int NC = (L + S - 1) / S;
+    const int keys = keys_of<WIN>(p, L);
+    const int NC = (keys + S - 1) / S;
     const int local = item - s_prefix[b];
     const int c = local % NC;
     const int rest = local / NC;
     const int rb = rest % p.RB;
     const int kvh = rest / p.RB;
     const int c0 = c * S;
-    const bool ok = stream_chunk<D, NST, TILE>(a, smem, s_bars, seq, b, kvh, rb, L, c0, min(c0 + S, L));
+    const bool ok = stream_chunk<D, NST, TILE, WIN>(a, smem, s_bars, seq, b, kvh, rb, L, c0, min(c0 + S, keys));
     finish_item<E, D, TR, kWarps, combine_stride<D>()>(p, combine, C::RING_BYTES / 4, &s_merge_bar, merge_phase, b, kvh,
                                                        rb, c, NC, &s_last, W <= (int)gridDim.x);
     // the combine and merge wrote the ring through the generic proxy; the next item's first

@@ -1,5 +1,6 @@
-// Python binding of the f8 calls (include/td.h) as a CPython extension on torch tensors: argument
-// checks, outputs and workspaces made when the caller passes none, then the C call.
+// Python binding of the calls on an f8 cache, the normed append, the windowed and the shared-prefix attention
+// (include/td.h) as a CPython extension on torch tensors: argument checks, outputs and workspaces made
+// when the caller passes none, then the C call.
 //
 // The other calls are bound through ctypes (api.py). These are bound natively because a token's
 // append or a short decode takes the GPU 2 to 7 us, and marshalling twenty arguments and checking
@@ -15,6 +16,7 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/FunctionRef.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -375,8 +377,9 @@ PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t) {
 // made, most recently used first, kMost of them and kMostBytes in all at most (a caller's split can ask
 // for gigabytes; the one in use stays whatever its size). One that is dropped goes back to the
 // allocator of the stream whose calls alone used it. Never destroyed at exit, which they may outlive.
-using Key = std::array<long long, 9>;
-at::Tensor kept_workspace(const Key &key, const at::Tensor &like) {
+using Key = std::array<long long, 13>;  // which call, device, stream, its shape arguments
+enum : long long { kWsF8, kWsWindow, kWsPrefix };
+at::Tensor kept_workspace(const Key &key, const at::Tensor &like, c10::function_ref<size_t()> bytes_of) {
   static std::mutex mu;
   static auto *kept = new std::list<std::pair<Key, at::Tensor>>();
   constexpr size_t kMost = 32, kMostBytes = size_t(256) << 20;
@@ -390,8 +393,7 @@ at::Tensor kept_workspace(const Key &key, const at::Tensor &like) {
         return it->second;
       }
   }
-  const size_t need = td_f8_workspace_bytes((int)key[2], (int)key[3], (int)key[4], (int)key[5], (int)key[6],
-                                            (int)key[7], (int)key[8]);
+  const size_t need = bytes_of();
   at::Tensor ws = at::zeros({(int64_t)(need < 256 ? 256 : need)}, like.options().dtype(at::kByte));
   std::lock_guard<std::mutex> lock(mu);
   kept->emplace_front(key, ws);
@@ -404,6 +406,43 @@ at::Tensor kept_workspace(const Key &key, const at::Tensor &like) {
   return ws;
 }
 
+long long stream_key(const Place &place) { return (long long)reinterpret_cast<intptr_t>(place.stream()); }
+
+// The results of an attention call: what the caller passed, or tensors made here.
+struct Results {
+  const at::Tensor *out, *lse;
+  at::Tensor made_out, made_lse;
+  PyObject *given_out, *given_lse;
+  bool want_lse;
+
+  Results(PyObject *o, PyObject *l, PyObject *return_lse, const at::Tensor &q)
+      : out(tensor_or_null(o)), lse(tensor_or_null(l)), given_out(o), given_lse(l) {
+    want(out == nullptr || (same_shape(*out, q) && out->scalar_type() == q.scalar_type()), PyExc_TypeError,
+         "out must match q");
+    want(lse == nullptr || (lse->scalar_type() == at::kFloat && lse->sizes() == rows(q)), PyExc_TypeError,
+         "lse must be float32 in q's shape without D");
+    want_lse = lse != nullptr || truth(return_lse);
+  }
+  static c10::IntArrayRef rows(const at::Tensor &q) { return q.sizes().slice(0, q.dim() - 1); }
+  void make(const at::Tensor &q) {
+    if (out == nullptr) {
+      made_out = at::empty_like(q);
+      out = &made_out;
+    }
+    if (want_lse && lse == nullptr) {
+      made_lse = at::empty(rows(q), q.options().dtype(at::kFloat));
+      lse = &made_lse;
+    }
+  }
+  PyObject *give() const {
+    PyObject *o = made_out.defined() ? wrap(made_out) : Py_NewRef(given_out);
+    if (!want_lse) return o;
+    return Py_BuildValue("(NN)", o, made_lse.defined() ? wrap(made_lse) : Py_NewRef(given_lse));
+  }
+};
+
+double scale_of(PyObject *o, int D) { return o == Py_None ? 1.0 / std::sqrt((double)D) : real(o); }
+
 // attn(q, <cache>, scale, split, out, lse, workspace, dev_status, stream, return_lse): decode for a
 // 3-D q, else verify
 PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t) {
@@ -413,43 +452,98 @@ PyObject *attn(PyObject *, PyObject *const *a, Py_ssize_t) {
     a += 1 + kCache;
     const bool decode = q.dim() == 3;
     const char *name = decode ? "td_decode_attn_f8" : "td_verify_attn_f8";
-    double scale = 1.0 / std::sqrt((double)c.D);
-    if (a[0] != Py_None) scale = real(a[0]);
+    const double scale = scale_of(a[0], c.D);
     const int split = small(a[1]);
-    const at::Tensor *out = tensor_or_null(a[2]), *lse = tensor_or_null(a[3]), *ws = tensor_or_null(a[4]);
-    const at::Tensor *st = status_word(a[5]);
     want(q.scalar_type() == at::kBFloat16, PyExc_TypeError, "q must be bfloat16");
     want(q.size(0) == c.B && q.size(-1) == c.D, PyExc_ValueError, "q and cache shapes disagree");
-    want(out == nullptr || (same_shape(*out, q) && out->scalar_type() == at::kBFloat16), PyExc_TypeError,
-         "out must match q");
-    const c10::IntArrayRef row_shape = q.sizes().slice(0, q.dim() - 1);
-    want(lse == nullptr || (lse->scalar_type() == at::kFloat && lse->sizes() == row_shape), PyExc_TypeError,
-         "lse must be float32 in q's shape without D");
+    Results r(a[2], a[3], a[7], q);
+    const at::Tensor *ws = tensor_or_null(a[4]);
+    const at::Tensor *st = status_word(a[5]);
     want(ws == nullptr || ws->scalar_type() == at::kByte, PyExc_TypeError, "workspace must be a uint8 tensor");
     const int Hq = extent(q, 1), T = decode ? 1 : extent(q, 2);
-    const bool want_lse = lse != nullptr || truth(a[7]);
-    const int dev = device_of({&q, &c.kc, &c.ks, &c.vc, &c.vs, &c.lens, out, lse, ws, st});
+    const int dev = device_of({&q, &c.kc, &c.ks, &c.vc, &c.vs, &c.lens, r.out, r.lse, ws, st});
     const Place place(dev, a[6]);
-    at::Tensor made_out, made_lse, kept;
-    if (out == nullptr) {
-      made_out = at::empty_like(q);
-      out = &made_out;
-    }
-    if (want_lse && lse == nullptr) {
-      made_lse = at::empty(row_shape, q.options().dtype(at::kFloat));
-      lse = &made_lse;
-    }
+    r.make(q);
+    at::Tensor kept;
     if (ws == nullptr) {
-      kept = kept_workspace({dev, (long long)reinterpret_cast<intptr_t>(place.stream()), c.B, Hq, c.Hkv, c.Smax, c.D, T, split}, q);
+      kept = kept_workspace({kWsF8, dev, stream_key(place), c.B, Hq, c.Hkv, c.Smax, c.D, T, split}, q,
+                            [&] { return td_f8_workspace_bytes(c.B, Hq, c.Hkv, c.Smax, c.D, T, split); });
       ws = &kept;
     }
     checked(name, td_verify_attn_f8(ptr<void>(q), ptr<void>(c.kc), ptr<float>(c.ks), ptr<void>(c.vc), ptr<float>(c.vs),
                                     ptr<int32_t>(c.lens), c.B, Hq, c.Hkv, T, c.Smax, c.D, c.block, (float)scale, split,
-                                    ptr<void>(out), ptr<float>(lse), ptr<void>(ws), (size_t)ws->numel(),
+                                    ptr<void>(r.out), ptr<float>(r.lse), ptr<void>(ws), (size_t)ws->numel(),
                                     ptr<uint32_t>(st), place.stream()));
-    PyObject *o = made_out.defined() ? wrap(made_out) : Py_NewRef(a[2]);
-    if (!want_lse) return o;
-    return Py_BuildValue("(NN)", o, made_lse.defined() ? wrap(made_lse) : Py_NewRef(a[3]));
+    return r.give();
+  });
+}
+
+// A cache of rows, its lengths and the queries over it, checked against one another (T is 1 for a 3-D q).
+struct Rows {
+  const at::Tensor &q, &k, &v, &lens;
+  bool decode;
+  int B, Hq, Hkv, T, Smax, D;
+  td_dtype dt;
+
+  explicit Rows(PyObject *const *a) : q(tensor(a[0])), k(tensor(a[1])), v(tensor(a[2])), lens(tensor(a[3])) {
+    want((q.dim() == 3 || q.dim() == 4) && k.dim() == 4 && same_shape(v, k) && q.size(0) == k.size(0) &&
+             q.size(-1) == k.size(3),
+         PyExc_ValueError, "q and cache shapes disagree");
+    want(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(), PyExc_TypeError,
+         "q and caches must share a dtype");
+    dt = code(q.scalar_type());
+    decode = q.dim() == 3;
+    B = extent(q, 0), Hq = extent(q, 1), T = decode ? 1 : extent(q, 2), D = extent(q, -1);
+    Hkv = extent(k, 1), Smax = extent(k, 2);
+    want(lens.scalar_type() == at::kInt && shaped(lens, {B}), PyExc_TypeError, "seq_lens must be int32 [B]");
+  }
+};
+
+// window_attn(q, k_cache, v_cache, seq_lens, window, sinks, scale, split, out, lse, workspace, dev_status, stream,
+// return_lse): decode for a 3-D q, else verify
+PyObject *window_attn(PyObject *, PyObject *const *a, Py_ssize_t) {
+  return guarded([&]() -> PyObject * {
+    const Rows c(a);
+    const int window = small(a[4]), sinks = small(a[5]), split = small(a[7]);
+    const double scale = scale_of(a[6], c.D);
+    Results r(a[8], a[9], a[13], c.q);
+    const at::Tensor *ws = tensor_or_null(a[10]), *st = status_word(a[11]);
+    want(ws == nullptr || ws->scalar_type() == at::kByte, PyExc_TypeError, "workspace must be a uint8 tensor");
+    const int dev = device_of({&c.q, &c.k, &c.v, &c.lens, r.out, r.lse, ws, st});
+    const Place place(dev, a[12]);
+    r.make(c.q);
+    at::Tensor kept;
+    if (ws == nullptr) {
+      kept = kept_workspace(
+          {kWsWindow, dev, stream_key(place), c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, split, window, sinks}, c.q,
+          [&] { return td_window_workspace_bytes(c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, window, sinks, split); });
+      ws = &kept;
+    }
+    checked(c.decode ? "td_decode_attn_window" : "td_verify_attn_window",
+            td_verify_attn_window(c.dt, ptr<void>(c.q), ptr<void>(c.k), ptr<void>(c.v), ptr<int32_t>(c.lens), c.B, c.Hq,
+                                  c.Hkv, c.T, c.Smax, c.D, (float)scale, window, sinks, split, ptr<void>(r.out),
+                                  ptr<float>(r.lse), ptr<void>(ws), (size_t)ws->numel(), ptr<uint32_t>(st),
+                                  place.stream()));
+    return r.give();
+  });
+}
+
+// window_prefill(q, k_cache, v_cache, seq_lens, window, sinks, scale, out, lse, dev_status, stream, return_lse)
+PyObject *window_prefill(PyObject *, PyObject *const *a, Py_ssize_t) {
+  return guarded([&]() -> PyObject * {
+    const Rows c(a);
+    want(c.dt == TD_BF16, PyExc_TypeError, "prefill takes bfloat16 q and caches");
+    const int window = small(a[4]), sinks = small(a[5]);
+    const double scale = scale_of(a[6], c.D);
+    Results r(a[7], a[8], a[11], c.q);
+    const at::Tensor *st = status_word(a[9]);
+    const Place place(device_of({&c.q, &c.k, &c.v, &c.lens, r.out, r.lse, st}), a[10]);
+    r.make(c.q);
+    checked("td_prefill_attn_window",
+            td_prefill_attn_window(ptr<void>(c.q), ptr<void>(c.k), ptr<void>(c.v), ptr<int32_t>(c.lens), c.B, c.Hq, c.Hkv,
+                                   c.T, c.Smax, c.D, (float)scale, window, sinks, ptr<void>(r.out), ptr<float>(r.lse),
+                                   ptr<uint32_t>(st), place.stream()));
+    return r.give();
   });
 }
 
@@ -464,9 +558,10 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 
 #define TD_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&counted<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TD_METHOD(append, 2 + kCache + 3), TD_METHOD(rope_append, 2 + kCache + 9), TD_METHOD(norm_append, 17),
-                         TD_METHOD(read, kCache + 7), TD_METHOD(attn, 1 + kCache + 8), {nullptr, nullptr, 0, nullptr}};
+                         TD_METHOD(read, kCache + 7), TD_METHOD(attn, 1 + kCache + 8),
+                         TD_METHOD(window_attn, 14), TD_METHOD(window_prefill, 12), {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_td_torch", "Native binding of the f8 calls.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_td_torch", "Native binding of some of the calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

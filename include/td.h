@@ -389,6 +389,32 @@ td_status td_prefill_attn(const void *q, const void *k_cache, const void *v_cach
                           uint32_t *dev_status, void *stream);
 
 /*
+ * Attention over a sliding window whose first tokens stay visible (layers of a fixed reach, and long generations that
+ * keep a few first tokens as sinks). The query of token t sits at position P = L_b - T + t and attends keys j <= P with
+ *   j > P - window   or   j < sinks;
+ * everything else is as td_decode_attn (T = 1), td_verify_attn and td_prefill_attn define it, rows that see no key and
+ * status bits included. window >= 1 and sinks >= 0, past Smax like Smax (the plain calls' keys). Keys and values that
+ * no token of a call sees are never used, whatever they hold; a value that one token of a verify chunk or of a prompt's
+ * tile of 128 sees and another does not must be finite for both (a weight of 0 times NaN is NaN), as in the plain calls.
+ * td_decode_attn_window and td_verify_attn_window: TD_F32 and TD_BF16; split is 0 or a multiple of 16; a workspace of
+ * td_window_workspace_bytes, used as td_decode_workspace_bytes says, for one (B, Hq, Hkv, Smax, D, q_len, window,
+ * sinks, split). Their cost follows the window, not the context: per sequence and kv head they read
+ * min(L, sinks + window + T - 1) rows. td_prefill_attn_window: bf16, whole tiles of 64 keys.
+ */
+size_t td_window_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int window, int sinks, int split);
+td_status td_decode_attn_window(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D, float scale, int window,
+                                int sinks, int split, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                uint32_t *dev_status, void *stream);
+td_status td_verify_attn_window(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *seq_lens, int B, int Hq, int Hkv, int T, int Smax, int D, float scale,
+                                int window, int sinks, int split, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream);
+td_status td_prefill_attn_window(const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B,
+                                 int Hq, int Hkv, int T, int Smax, int D, float scale, int window, int sinks, void *out,
+                                 float *lse, uint32_t *dev_status, void *stream);
+
+/*
  * Diagnostic of the bounded wait (the pages describe no such call; it exists so that the
  * failure path every kernel relies on can be exercised without a fault). One CTA waits for
  * the first phase of an mbarrier that nothing arrives on and no copy completes, with the

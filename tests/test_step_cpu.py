@@ -113,10 +113,107 @@ def test_norm_append_binding_refuses(lib, kw, error):
         api.td_norm_rope_kv_append(**norm_args(**kw))
 
 
+WINDOW = ("dtype", "q", "k", "v", "sl", "B", "Hq", "Hkv", "T", "Smax", "D", "scale", "window", "sinks", "split", "out",
+          "lse", "ws", "wsb", "st", "stream")
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(window=0), INVALID),
+    (dict(window=-5), INVALID),
+    (dict(sinks=-1), INVALID),
+    (dict(q=None), INVALID),
+    (dict(sl=None), INVALID),
+    (dict(out=None), INVALID),
+    (dict(Hq=5), INVALID),
+    (dict(T=0), INVALID),
+    (dict(split=-16), INVALID),
+    (dict(scale=NAN), INVALID),
+    (dict(Smax=0), INVALID),
+    (dict(split=40), UNSUPPORTED),
+    (dict(dtype=2), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED),
+    (dict(T=65), UNSUPPORTED),
+    (dict(B=1025), UNSUPPORTED),
+])
+def test_window_attention_refuses(lib, kw, expect):
+    d = dict(dtype=1, q=FAKE, k=FAKE, v=FAKE, sl=FAKE, B=2, Hq=4, Hkv=2, T=3, Smax=64, D=128, scale=1.0, window=8, sinks=2,
+             split=0, out=FAKE, lse=None, ws=FAKE, wsb=1 << 24, st=None, stream=None)
+    assert _call(lib.td_verify_attn_window, WINDOW, d, kw) == expect
+    if "T" not in kw:
+        order = tuple(k for k in WINDOW if k != "T")
+        assert _call(lib.td_decode_attn_window, order, d, kw) == expect
+
+
+PROMPT = ("q", "k", "v", "sl", "B", "Hq", "Hkv", "T", "Smax", "D", "scale", "window", "sinks", "out", "lse", "st", "stream")
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(window=0), INVALID),
+    (dict(sinks=-1), INVALID),
+    (dict(k=None), INVALID),
+    (dict(Hq=5), INVALID),
+    (dict(scale=NAN), INVALID),
+    (dict(T=65), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED),
+    (dict(q=FAKE + 8), UNSUPPORTED),
+    (dict(Smax=(1 << 30) + 1), UNSUPPORTED),
+])
+def test_window_prefill_refuses(lib, kw, expect):
+    d = dict(q=FAKE, k=FAKE, v=FAKE, sl=FAKE, B=2, Hq=4, Hkv=2, T=3, Smax=64, D=128, scale=1.0, window=8, sinks=2, out=FAKE,
+             lse=None, st=None, stream=None)
+    assert _call(lib.td_prefill_attn_window, PROMPT, d, kw) == expect
+
+
+def attn_args(decode=False, **kw):
+    a = dict(q=rows(2, 4, 128) if decode else rows(2, 4, 3, 128), k_cache=rows(2, 2, 64, 128), v_cache=rows(2, 2, 64, 128),
+             seq_lens=torch.zeros(2, dtype=torch.int32), window=8, sinks=2)
+    a.update(kw)
+    return a
+
+
+BAD_ATTN = [
+    (dict(q=rows(2, 4, 3, 64)), ValueError),
+    (dict(q=rows(3, 4, 3, 128)), ValueError),
+    (dict(q=rows(2, 4)), ValueError),
+    (dict(v_cache=rows(2, 2, 65, 128)), ValueError),
+    (dict(k_cache=torch.zeros(2, 2, 64, 128)), TypeError),
+    (dict(seq_lens=torch.zeros(2, dtype=torch.int64)), TypeError),
+    (dict(out=rows(2, 4, 2, 128)), TypeError),
+    (dict(out=torch.zeros(2, 4, 3, 128)), TypeError),
+    (dict(lse=torch.zeros(2, 4)), TypeError),
+    (dict(lse=rows(2, 4, 3)), TypeError),
+    (dict(window="8"), TypeError),
+    (dict(sinks=2.5), TypeError),
+    (dict(window=1 << 40), ValueError),
+    (dict(), ValueError),                             # all in order, but not on a GPU
+]
+
+
+@pytest.mark.parametrize("kw,error", BAD_ATTN + [(dict(workspace=torch.zeros(8)), TypeError)])
+def test_window_binding_refuses(lib, kw, error):
+    with pytest.raises(error):
+        api.td_verify_attn_window(**attn_args(**kw))
+
+
+@pytest.mark.parametrize("kw,error", BAD_ATTN + [
+    (dict(q=torch.zeros(2, 4, 3, 128), k_cache=torch.zeros(2, 2, 64, 128), v_cache=torch.zeros(2, 2, 64, 128)), TypeError)])
+def test_window_prefill_binding_refuses(lib, kw, error):
+    with pytest.raises(error):
+        api.td_prefill_attn_window(**attn_args(**kw))
+
+
+def test_decode_and_verify_take_their_own_queries(lib):
+    with pytest.raises(ValueError):
+        api.td_decode_attn_window(**attn_args())
+    with pytest.raises(ValueError):
+        api.td_verify_attn_window(**attn_args(decode=True))
+
+
 def test_kernels_have_no_spills(lib):
     """Register gate (ptxas), as for the other kernels."""
     log = open(td_build.PTXAS_LOG).read()
     entries = re.findall(r"Compiling entry function '(\w+)'.*?\n(?:.*?\n)*?\s+(\d+) bytes stack frame, (\d+) bytes "
                          r"spill stores, (\d+) bytes spill loads", log)
-    for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4)):
+    for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4), ("mma_kernelILi64", 10), ("mma_kernelILi128", 10),
+                 ("cluster_kernelILi64", 6), ("cluster_kernelILi128", 6), ("Li1EEEvNS_11SplitParams", 6), ("14prefill_kernel", 4)):
         assert [(int(st), int(ld)) for name, _, st, ld in entries if k in name] == [(0, 0)] * n, k
