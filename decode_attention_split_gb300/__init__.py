@@ -19,6 +19,7 @@ from .api import (  # noqa: F401
     make_workspace,
     td_decode_attn,
     td_decode_attn_f8,
+    td_decode_attn_prefix,
     td_decode_attn_q8,
     td_decode_attn_window,
     td_decode_workspace_bytes,
@@ -31,6 +32,7 @@ from .api import (  # noqa: F401
     td_norm_rope_kv_append,
     td_prefill_attn,
     td_prefill_attn_window,
+    td_prefix_workspace_bytes,
     td_rope_append_attn,
     td_rope_kv_append,
     td_rope_kv_append_f8,
@@ -39,6 +41,7 @@ from .api import (  # noqa: F401
     td_split_plan,
     td_verify_attn,
     td_verify_attn_f8,
+    td_verify_attn_prefix,
     td_verify_attn_q8,
     td_verify_attn_window,
     td_window_workspace_bytes,

@@ -34,6 +34,9 @@ SYMBOLS = (
     "td_decode_attn_f8",
     "td_verify_attn_f8",
     "td_prefill_attn",
+    "td_prefix_workspace_bytes",
+    "td_decode_attn_prefix",
+    "td_verify_attn_prefix",
     "td_window_workspace_bytes",
     "td_decode_attn_window",
     "td_verify_attn_window",
@@ -105,6 +108,12 @@ def _declare(lib):
     lib.td_verify_attn_f8.restype = i
     lib.td_prefill_attn.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, vp, vp, vp, vp]
     lib.td_prefill_attn.restype = i
+    lib.td_prefix_workspace_bytes.argtypes = [i] * 7
+    lib.td_prefix_workspace_bytes.restype = sz
+    lib.td_decode_attn_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp, vp, vp, sz, vp, vp]
+    lib.td_decode_attn_prefix.restype = i
+    lib.td_verify_attn_prefix.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp, vp, sz, vp, vp]
+    lib.td_verify_attn_prefix.restype = i
     lib.td_window_workspace_bytes.argtypes = [i] * 9
     lib.td_window_workspace_bytes.restype = sz
     lib.td_decode_attn_window.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, vp, vp, sz, vp, vp]

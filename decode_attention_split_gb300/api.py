@@ -580,3 +580,30 @@ def td_prefill_attn_window(q, k_cache, v_cache, seq_lens, window: int, sinks: in
         raise ValueError("q must be [B, Hq, T, D]")
     return (_native or _load_native()).window_prefill(q, k_cache, v_cache, seq_lens, window, sinks, scale, out, lse,
                                                       dev_status, stream, return_lse)
+
+
+# ------------------------------------------------------------------ a prefix shared by the batch
+
+def td_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Pmax: int, Smax: int, D: int, q_len: int = 1) -> int:
+    """Workspace bytes td_decode_attn_prefix / td_verify_attn_prefix need on the current device (0 = invalid)."""
+    return int(lib().td_prefix_workspace_bytes(B, Hq, Hkv, Pmax, Smax, D, q_len))
+
+
+def td_decode_attn_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, scale: float | None = None,
+                          out=None, lse=None, workspace=None, dev_status=None, stream=None, return_lse: bool = False):
+    """Single-token attention of a batch over one shared prefix [Hkv,Pmax,D] (its first prefix_len rows, int32 [1] on
+    the device), read once for all sequences, and each sequence's own keys: q [B,Hq,D] bf16 -> out [B,Hq,D] (+ lse)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    return (_native or _load_native()).prefix_attn(q, k_cache, v_cache, seq_lens, k_prefix, v_prefix, prefix_len, scale,
+                                                   out, lse, workspace, dev_status, stream, return_lse)
+
+
+def td_verify_attn_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, scale: float | None = None,
+                          out=None, lse=None, workspace=None, dev_status=None, stream=None, return_lse: bool = False):
+    """The same for T new tokens a sequence, causal among themselves: q [B,Hq,T,D] bf16 (seq_lens count the T tokens,
+    not the prefix) -> out [B,Hq,T,D] (+ lse [B,Hq,T])."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, T, D]")
+    return (_native or _load_native()).prefix_attn(q, k_cache, v_cache, seq_lens, k_prefix, v_prefix, prefix_len, scale,
+                                                   out, lse, workspace, dev_status, stream, return_lse)

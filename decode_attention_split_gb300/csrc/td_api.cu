@@ -608,3 +608,43 @@ extern "C" td_status td_prefill_attn_window(const void *q, const void *k_cache, 
   if (Smax > (1 << 30)) return TD_ERR_UNSUPPORTED;
   return prefill(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, window, sinks, out, lse, dev_status, stream);
 }
+
+extern "C" {
+
+size_t td_prefix_workspace_bytes(int B, int Hq, int Hkv, int Pmax, int Smax, int D, int q_len) {
+  td::PrefixPlan plan;
+  return td::plan_prefix(B, Hq, Hkv, q_len, Pmax, Smax, D, &plan) == TD_OK ? plan.bytes : 0;
+}
+
+td_status td_verify_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                                const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                int T, int Pmax, int Smax, int D, float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+  if (k_prefix == nullptr || v_prefix == nullptr || prefix_len == nullptr) return TD_ERR_INVALID_ARG;
+  td::PrefixPlan plan;
+  td_status st = td::plan_prefix(B, Hq, Hkv, T, Pmax, Smax, D, &plan);
+  if (st == TD_ERR_CUDA) return cuda_fail(cudaGetLastError());
+  if (st != TD_OK) return st;
+  if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned4(prefix_len)) return TD_ERR_UNSUPPORTED;
+  td::SplitParams own;
+  st = prepare(TD_BF16, q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, 0, out, lse, workspace,
+               workspace_bytes, dev_status, &plan.own, &own);
+  if (st != TD_OK) return st;
+  if (workspace_bytes < plan.bytes) return TD_ERR_WORKSPACE;
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+  own.out = ws + plan.off_own;
+  own.lse = reinterpret_cast<float *>(ws + plan.off_lse);
+  const td::PrefixAttn x{k_prefix, v_prefix, prefix_len, reinterpret_cast<float *>(ws + plan.off_part), out, lse, Pmax};
+  const cudaError_t e = td::launch_prefix(D, plan, x, own, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TD_OK : cuda_fail(e);
+}
+
+td_status td_decode_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                                const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                int Pmax, int Smax, int D, float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream) {
+  return td_verify_attn_prefix(q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, seq_lens, B, Hq, Hkv, 1, Pmax, Smax, D,
+                               scale, out, lse, workspace, workspace_bytes, dev_status, stream);
+}
+
+}  // extern "C"

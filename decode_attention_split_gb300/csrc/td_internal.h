@@ -145,6 +145,24 @@ cudaError_t launch_prefill(const void *q, const void *k, const void *v, const in
                            int T, int Smax, int D, float scale, void *out, float *lse, uint32_t *status,
                            cudaStream_t stream, int window = 0, int sinks = 0);
 
+// Attention over a shared prefix and each sequence's own keys (td_prefix.cu).
+struct PrefixPlan {
+  SplitPlan own;     // over the sequences' own keys
+  int tiles, chunks; // 128-row tiles of a kv head, chunks of the prefix
+  size_t off_own, off_lse, off_part, bytes;  // workspace: own's, its fp32 out and lse, the prefix's partial blocks
+};
+struct PrefixAttn {
+  const void *k, *v;  // [Hkv, Pmax, D]
+  const int32_t *prefix_len;
+  float *part;
+  void *out;          // [B, Hq, T, D] bf16
+  float *lse;         // [B, Hq, T] or null
+  int Pmax;
+};
+td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, PrefixPlan *plan);
+// own: the split parameters of the own keys, out and lse in the workspace.
+cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &own, cudaStream_t stream);
+
 // SM count of the current device (cached per device).
 int device_sm_count(int device);
 

@@ -32,6 +32,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "td_mma.cuh"
 #include "td_rope.cuh"
 #include "td_split_attn.cuh"
@@ -799,14 +801,18 @@ __device__ __forceinline__ unsigned char *align1024(unsigned char *p) {
 // they read the same then (measured on the 3B-style layer: 4k 11.4 -> 10.5 us, 32k 25.7 ->
 // 25.5 us). The other instantiation plans after the wait. TILE: the warps' step for the row
 // block's rows (tile_of_rows).
-// WIN: kWindowPad for windowed attention, else 0.
-template <int D, bool EARLY_PLAN, int TILE = kTileM16, int WIN = 0>
+// WIN: kWindowPad for windowed attention, else 0. PART: a part of an attention (a sequence's own keys behind a shared
+// prefix) whose out goes on in fp32. The kernel before it in the stream is then the other part, which this one neither
+// reads nor writes, and which waited for everything earlier before it let this one start: it runs alongside, reads
+// what others wrote past L1 alone, and its first CTA waits for the other part at the end, so that this grid's end is both's.
+template <int D, bool EARLY_PLAN, int TILE = kTileM16, int WIN = 0, bool PART = false>
 __global__ void __launch_bounds__(kThreads, 2)
     split_attn_mma_kernel(const __grid_constant__ typename MmaArgsOf<WIN>::type a) {
   constexpr int NST = kPersistentStages<D>;
   using C = MmaCfg<D, NST>;
-  using E = __nv_bfloat16;
+  using E = std::conditional_t<PART, float, __nv_bfloat16>;  // of the output
   constexpr int TR = tile_rows<TILE>();
+  static_assert(!(PART && (EARLY_PLAN || WIN != 0)), "parts have neither");
   static_assert((merge_fixed_floats<D, TR>() + part_block_floats(TR, D)) * 4 <= C::RING_BYTES,
                 "merge stages at least one chunk");
   const SplitParams &p = a.p;
@@ -831,12 +837,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t seq = 0;
   if (tid == 0) prefetch_first_item<D, kWarmRows, WIN>(p, prefetch_stages(p), blockIdx.x);
   if constexpr (EARLY_PLAN) plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red, false);
-  griddep_wait();  // inputs may come from the previous kernel in the stream
+  if constexpr (!PART) griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   if constexpr (EARLY_PLAN)
     confirm_plan<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   else
-    plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+    plan_items<WIN, PART>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   advance_after_reads(p, &s_last);  // fused step: the lengths move on once every CTA has read them
   const int S = s_chunk;
   const int W = s_prefix[p.B];
@@ -876,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     if (!ok) break;  // a copy never completed: stop taking items
   }
+  if (PART && blockIdx.x == 0) griddep_wait();
 }
 
 // Combines the kWarps partial sources left by stream_chunk (base-2 units, TR rows per warp)

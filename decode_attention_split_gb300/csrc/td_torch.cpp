@@ -547,6 +547,42 @@ PyObject *window_prefill(PyObject *, PyObject *const *a, Py_ssize_t) {
   });
 }
 
+// prefix_attn(q, k_cache, v_cache, seq_lens, k_prefix, v_prefix, prefix_len, scale, out, lse, workspace, dev_status,
+// stream, return_lse): decode for a 3-D q, else verify
+PyObject *prefix_attn(PyObject *, PyObject *const *a, Py_ssize_t) {
+  return guarded([&]() -> PyObject * {
+    const Rows c(a);
+    want(c.dt == TD_BF16, PyExc_TypeError, "attention over a prefix takes bfloat16 q and caches");
+    const at::Tensor &kp = tensor(a[4]), &vp = tensor(a[5]), &plen = tensor(a[6]);
+    want(kp.dim() == 3 && same_shape(vp, kp) && kp.size(0) == c.Hkv && kp.size(2) == c.D, PyExc_ValueError,
+         "the prefix must be [Hkv, Pmax, D], K and V alike");
+    want(kp.scalar_type() == at::kBFloat16 && vp.scalar_type() == at::kBFloat16, PyExc_TypeError,
+         "the prefix must be bfloat16");
+    want(plen.scalar_type() == at::kInt && plen.numel() == 1, PyExc_TypeError, "prefix_len must be one int32");
+    const int Pmax = extent(kp, 1);
+    const double scale = scale_of(a[7], c.D);
+    Results r(a[8], a[9], a[13], c.q);
+    const at::Tensor *ws = tensor_or_null(a[10]), *st = status_word(a[11]);
+    want(ws == nullptr || ws->scalar_type() == at::kByte, PyExc_TypeError, "workspace must be a uint8 tensor");
+    const int dev = device_of({&c.q, &c.k, &c.v, &c.lens, &kp, &vp, &plen, r.out, r.lse, ws, st});
+    const Place place(dev, a[12]);
+    r.make(c.q);
+    at::Tensor kept;
+    if (ws == nullptr) {
+      kept = kept_workspace({kWsPrefix, dev, stream_key(place), c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, Pmax}, c.q, [&] {
+        return td_prefix_workspace_bytes(c.B, c.Hq, c.Hkv, Pmax, c.Smax, c.D, c.T);
+      });
+      ws = &kept;
+    }
+    checked(c.decode ? "td_decode_attn_prefix" : "td_verify_attn_prefix",
+            td_verify_attn_prefix(ptr<void>(c.q), ptr<void>(kp), ptr<void>(vp), ptr<int32_t>(plen), ptr<void>(c.k),
+                                  ptr<void>(c.v), ptr<int32_t>(c.lens), c.B, c.Hq, c.Hkv, c.T, Pmax, c.Smax, c.D,
+                                  (float)scale, ptr<void>(r.out), ptr<float>(r.lse), ptr<void>(ws), (size_t)ws->numel(),
+                                  ptr<uint32_t>(st), place.stream()));
+    return r.give();
+  });
+}
+
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t), int N>
 PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (n != N) {
@@ -559,7 +595,7 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 #define TD_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&counted<f, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {TD_METHOD(append, 2 + kCache + 3), TD_METHOD(rope_append, 2 + kCache + 9), TD_METHOD(norm_append, 17),
                          TD_METHOD(read, kCache + 7), TD_METHOD(attn, 1 + kCache + 8),
-                         TD_METHOD(window_attn, 14), TD_METHOD(window_prefill, 12), {nullptr, nullptr, 0, nullptr}};
+                         TD_METHOD(window_attn, 14), TD_METHOD(window_prefill, 12), TD_METHOD(prefix_attn, 14), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_td_torch", "Native binding of some of the calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -415,6 +415,27 @@ td_status td_prefill_attn_window(const void *q, const void *k_cache, const void 
                                  float *lse, uint32_t *dev_status, void *stream);
 
 /*
+ * Attention of a batch that shares a prefix (a system prompt, a document), whose keys and values are stored and read
+ * once for all sequences: k_prefix, v_prefix [Hkv, Pmax, D], of which the first P = prefix_len[0] rows count (int32 on
+ * the device, clamped to [0, Pmax] with the status bits of a length). Query row (hq, t) of sequence b attends
+ *   prefix keys j < P   and   own keys j < L_b - T + t + 1 of k_cache[b]
+ * in one softmax (its position is P + L_b - T + t: td_norm_rope_kv_append takes positions). L_b may be 0 with T = 1;
+ * rows without any key give out = 0 and lse = -inf, and L_b < T sets TD_DEV_VERIFY_SHORT as in td_verify_attn. bf16,
+ * D 64 or 128. The parts over the prefix and over the own keys are kept in fp32 and joined; out is rounded once.
+ * Three launches; the workspace is td_prefix_workspace_bytes', under td_decode_workspace_bytes' rules, for one
+ * (B, Hq, Hkv, Pmax, Smax, D, q_len).
+ */
+size_t td_prefix_workspace_bytes(int B, int Hq, int Hkv, int Pmax, int Smax, int D, int q_len);
+td_status td_decode_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                                const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                int Pmax, int Smax, int D, float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream);
+td_status td_verify_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
+                                const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq, int Hkv,
+                                int T, int Pmax, int Smax, int D, float scale, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, uint32_t *dev_status, void *stream);
+
+/*
  * Diagnostic of the bounded wait (the pages describe no such call; it exists so that the
  * failure path every kernel relies on can be exercised without a fault). One CTA waits for
  * the first phase of an mbarrier that nothing arrives on and no copy completes, with the

@@ -209,11 +209,58 @@ def test_decode_and_verify_take_their_own_queries(lib):
         api.td_verify_attn_window(**attn_args(decode=True))
 
 
+PREFIX = ("q", "kp", "vp", "pl", "k", "v", "sl", "B", "Hq", "Hkv", "T", "Pmax", "Smax", "D", "scale", "out", "lse", "ws",
+          "wsb", "st", "stream")
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(kp=None), INVALID),
+    (dict(vp=None), INVALID),
+    (dict(pl=None), INVALID),
+    (dict(T=0), INVALID),
+    (dict(Hq=5), INVALID),
+    (dict(B=0), INVALID),
+    (dict(Smax=0), INVALID),
+    (dict(T=65), UNSUPPORTED),
+    (dict(D=96), UNSUPPORTED),
+    (dict(B=1025), UNSUPPORTED),
+])
+def test_prefix_attention_refuses(lib, kw, expect):
+    d = dict(q=FAKE, kp=FAKE, vp=FAKE, pl=FAKE, k=FAKE, v=FAKE, sl=FAKE, B=2, Hq=4, Hkv=2, T=3, Pmax=100, Smax=64, D=128,
+             scale=1.0, out=FAKE, lse=None, ws=FAKE, wsb=1 << 24, st=None, stream=None)
+    assert _call(lib.td_verify_attn_prefix, PREFIX, d, kw) == expect
+    if "T" not in kw:
+        order = tuple(k for k in PREFIX if k != "T")
+        assert _call(lib.td_decode_attn_prefix, order, d, kw) == expect
+
+
+@pytest.mark.parametrize("kw,error", [(k, e) for k, e in BAD_ATTN if "window" not in k and "sinks" not in k] + [
+    (dict(k_prefix=rows(3, 100, 128)), ValueError),
+    (dict(k_prefix=rows(2, 100, 64), v_prefix=rows(2, 100, 64)), ValueError),
+    (dict(v_prefix=rows(2, 99, 128)), ValueError),
+    (dict(k_prefix=torch.zeros(2, 100, 128), v_prefix=torch.zeros(2, 100, 128)), TypeError),
+    (dict(prefix_len=torch.zeros(1)), TypeError),
+    (dict(prefix_len=torch.zeros(2, dtype=torch.int32)), TypeError),
+    (dict(prefix_len=100), TypeError),
+    (dict(q=torch.zeros(2, 4, 3, 128), k_cache=torch.zeros(2, 2, 64, 128), v_cache=torch.zeros(2, 2, 64, 128)), TypeError),
+])
+def test_prefix_binding_refuses(lib, kw, error):
+    a = attn_args(k_prefix=rows(2, 100, 128), v_prefix=rows(2, 100, 128), prefix_len=torch.zeros(1, dtype=torch.int32))
+    del a["window"], a["sinks"]
+    a.update(kw)
+    with pytest.raises(error):
+        api.td_verify_attn_prefix(**a)
+    if a["q"].dim() == 4:
+        with pytest.raises(ValueError):
+            api.td_decode_attn_prefix(**a)
+
+
 def test_kernels_have_no_spills(lib):
     """Register gate (ptxas), as for the other kernels."""
     log = open(td_build.PTXAS_LOG).read()
     entries = re.findall(r"Compiling entry function '(\w+)'.*?\n(?:.*?\n)*?\s+(\d+) bytes stack frame, (\d+) bytes "
                          r"spill stores, (\d+) bytes spill loads", log)
-    for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4), ("mma_kernelILi64", 10), ("mma_kernelILi128", 10),
-                 ("cluster_kernelILi64", 6), ("cluster_kernelILi128", 6), ("Li1EEEvNS_11SplitParams", 6), ("14prefill_kernel", 4)):
+    for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4), ("mma_kernelILi64", 13), ("mma_kernelILi128", 13),
+                 ("cluster_kernelILi64", 9), ("cluster_kernelILi128", 9), ("Li1EEEvNS_11SplitParams", 6), ("14prefill_kernel", 4),
+                 ("13prefix_kernel", 2), ("merge_prefix_kernel", 2)):
         assert [(int(st), int(ld)) for name, _, st, ld in entries if k in name] == [(0, 0)] * n, k
