@@ -95,8 +95,7 @@ template <int D, bool WIN>
 __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_constant__ PfArgs a) {
   using C = PfCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q, bar_k[2], bar_v[2], bar_s[2], bar_sfree, bar_p[2], bar_vfree[2], bar_o,
-      bar_fin;
+  __shared__ __align__(8) uint64_t bar_q, bar_k[2], bar_v[2], bar_s[2], bar_sfree, bar_p[2], bar_vfree[2], bar_fin;
   __shared__ uint32_t s_taddr;
   __shared__ int s_issued[2], s_seen[3];  // wind-down: K / V tiles issued; K / V tiles, Q seen landed
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -123,7 +122,6 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
     s_seen[0] = s_seen[1] = 0;
     s_seen[2] = 1;
     mbar_init(smem_u32(&bar_sfree), kPfSoftmaxWarps);
-    mbar_init(smem_u32(&bar_o), 1);
     mbar_init(smem_u32(&bar_fin), 1);
     fence_mbar_init();
   }
@@ -220,8 +218,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < kPfKeys / 16; ++k)
           tc_mma_ts(tO, tP + b0 * (kPfKeys / 2) + 8 * k, dv + ((vb + (uint32_t)k * 16 * 128) >> 4), kIdO, kt > 0 || k > 0);
-        tc_commit(smem_u32(&bar_o));
-        tc_commit(smem_u32(&bar_vfree[b0]));  // V buffer b0 may be refilled, P buffer b0 rewritten
+        tc_commit(smem_u32(&bar_vfree[b0]));  // V buffer b0 may be refilled, P buffer b0 rewritten, O of kt read
       }
       s_seen[0] = kw;
       s_seen[1] = vw;
@@ -287,7 +284,10 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       const int vrows = min(kPfKeys, (WIN ? kend : L) - j0);
       const int g0 = WIN ? max(a.sinks - j0, 0) : 0, g1 = WIN ? min(win0 - j0, kPfKeys) : 0;  // and [g0, g1)
       if (vrows < kPfKeys || g0 < g1) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[b0]), ph))) {
+        // (the product of kt-2 first: until then the buffer's barrier may be in kt-2's phase, whose
+        // predecessor has the parity of kt's)
+        const bool before = kt < 2 || mbar_wait_bounded(smem_u32(&bar_vfree[b0]), (uint32_t)((kt - 2) >> 1) & 1u);
+        if (!__all_sync(0xffffffffu, before && mbar_wait_bounded(smem_u32(&bar_v[b0]), ph))) {
           ok = false;
           break;
         }
@@ -328,9 +328,13 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
         m_ref = mx;
       }
       // a warp rescales its rows of O when any of them must, once the previous P V product
-      // is complete (TMEM loads and stores are warp-wide)
+      // is complete (TMEM loads and stores are warp-wide). The product of kt-2 may still be
+      // running here (S of kt is issued before the product of kt-1), so the wait is on a barrier
+      // whose last phase but one, kt-3, is known complete (P of kt-1 waited for it): a barrier
+      // that every product arrives on could still be in the phase of kt-2, whose parity lets a wait for
+      // kt-1 pass at once
       if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_o), (uint32_t)(kt - 1) & 1u))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_vfree[b0 ^ 1]), (uint32_t)((kt - 1) >> 1) & 1u))) {
           ok = false;
           break;
         }
@@ -364,7 +368,8 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       if (lane == 0) mbar_arrive(smem_u32(&bar_p[b0]));
     }
     // the last P V product is complete before O is read
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_o), (uint32_t)(nkt - 1) & 1u))) ok = false;
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_vfree[(nkt - 1) & 1]), (uint32_t)((nkt - 1) >> 1) & 1u)))
+      ok = false;
   }
   ok = __syncthreads_and(ok) != 0;
   if (!ok) {
