@@ -29,6 +29,33 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 size_t elem_size(td_dtype d) { return d == TD_F32 ? 4 : 2; }
 
+// Checks the pointers of an attention call over rows and fills the parameters that follow from its arguments alone.
+td_status rows_params(const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens, int B, int Hq,
+                      int Hkv, int T, int Smax, float scale, void *out, float *lse, uint32_t *dev_status,
+                      td::SplitParams *p) {
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr || out == nullptr || !isfinite(scale))
+    return TD_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(seq_lens) ||
+      (lse != nullptr && !aligned4(lse)) || (dev_status != nullptr && !aligned4(dev_status)))
+    return TD_ERR_UNSUPPORTED;
+  *p = td::SplitParams{};
+  p->q = q;
+  p->k = k_cache;
+  p->v = v_cache;
+  p->seq_lens = seq_lens;
+  p->out = out;
+  p->lse = lse;
+  p->status = dev_status;
+  p->B = B;
+  p->Hq = Hq;
+  p->Hkv = Hkv;
+  p->G = Hq / Hkv;
+  p->T = T;
+  p->Smax = Smax;
+  p->qscale = scale * td::kLog2e;
+  return TD_OK;
+}
+
 // Checks shared by the attention calls and fills the launch parameters; TD_OK or an error.
 td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache, const int32_t *seq_lens,
                   int B, int Hq, int Hkv, int T, int Smax, int D, float scale, int split, void *out, float *lse,
@@ -37,31 +64,16 @@ td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || seq_lens == nullptr || out == nullptr)
     return TD_ERR_INVALID_ARG;
   if (!isfinite(scale)) return TD_ERR_INVALID_ARG;
-  const td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, format, window, sinks);
+  td_status st = td::plan_split(dtype, B, Hq, Hkv, T, Smax, D, split, plan, format, window, sinks);
   if (st == TD_ERR_CUDA) return cuda_fail(cudaGetLastError());
   if (st != TD_OK) return st;
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(seq_lens) ||
-      (lse != nullptr && !aligned4(lse)) || (dev_status != nullptr && !aligned4(dev_status)))
-    return TD_ERR_UNSUPPORTED;
+  st = rows_params(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, scale, out, lse, dev_status, p);
+  if (st != TD_OK) return st;
   if (workspace == nullptr || workspace_bytes < plan->bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return TD_ERR_WORKSPACE;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
-  *p = td::SplitParams{};
-  p->q = q;
-  p->k = k_cache;
-  p->v = v_cache;
-  p->seq_lens = seq_lens;
-  p->out = out;
-  p->lse = lse;
   p->ws_part = reinterpret_cast<float *>(ws + plan->off_part);
   p->counters = reinterpret_cast<int *>(ws);
-  p->status = dev_status;
-  p->B = B;
-  p->Hq = Hq;
-  p->Hkv = Hkv;
-  p->G = Hq / Hkv;
-  p->T = T;
-  p->Smax = Smax;
   p->R = plan->R;
   p->RB = plan->RB;
   p->split = split;
@@ -71,7 +83,6 @@ td_status prepare(td_dtype dtype, const void *q, const void *k_cache, const void
   p->p_target = plan->p_target;
   p->min_chunk = plan->min_chunk;
   p->warm_stages = plan->warm;
-  p->qscale = scale * td::kLog2e;
   p->done = p->counters + plan->counters_n;
   p->window = window;
   p->sinks = sinks;
@@ -626,16 +637,13 @@ td_status td_verify_attn_prefix(const void *q, const void *k_prefix, const void 
   if (st == TD_ERR_CUDA) return cuda_fail(cudaGetLastError());
   if (st != TD_OK) return st;
   if (!aligned16(k_prefix) || !aligned16(v_prefix) || !aligned4(prefix_len)) return TD_ERR_UNSUPPORTED;
-  td::SplitParams own;
-  st = prepare(TD_BF16, q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, D, scale, 0, out, lse, workspace,
-               workspace_bytes, dev_status, &plan.own, &own);
+  td::SplitParams p;
+  st = rows_params(q, k_cache, v_cache, seq_lens, B, Hq, Hkv, T, Smax, scale, out, lse, dev_status, &p);
   if (st != TD_OK) return st;
-  if (workspace_bytes < plan.bytes) return TD_ERR_WORKSPACE;
-  unsigned char *ws = static_cast<unsigned char *>(workspace);
-  own.out = ws + plan.off_own;
-  own.lse = reinterpret_cast<float *>(ws + plan.off_lse);
-  const td::PrefixAttn x{k_prefix, v_prefix, prefix_len, reinterpret_cast<float *>(ws + plan.off_part), out, lse, Pmax};
-  const cudaError_t e = td::launch_prefix(D, plan, x, own, static_cast<cudaStream_t>(stream));
+  if (workspace == nullptr || workspace_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return TD_ERR_WORKSPACE;
+  const td::PrefixAttn x{k_prefix, v_prefix, prefix_len, Pmax};
+  const cudaError_t e = td::launch_prefix(D, plan, x, p, static_cast<unsigned char *>(workspace), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TD_OK : cuda_fail(e);
 }
 

@@ -145,23 +145,40 @@ cudaError_t launch_prefill(const void *q, const void *k, const void *v, const in
                            int T, int Smax, int D, float scale, void *out, float *lse, uint32_t *status,
                            cudaStream_t stream, int window = 0, int sinks = 0);
 
+// Attention in runs (td_runs.cu): the runs' launch leaves partial blocks, the join's reads them.
+struct RunsPlan {
+  int R, RB;      // rows of a row block, row blocks of a kv head
+  int grid;
+  size_t off_blocks, bytes;  // workspace: the plan's array, the blocks (nothing of it needs zeroing)
+};
+// keys: the most a sequence attends; per_sm: CTAs that take runs, at most, an SM.
+td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, int per_sm, RunsPlan *plan);
+cudaError_t launch_runs(int D, const RunsPlan &plan, const SplitParams &p, unsigned char *ws, cudaStream_t stream);
+// The parts over a shared prefix that the join adds (td_prefix.cu).
+struct PrefixPart {
+  const float *part;
+  const int32_t *prefix_len;
+  int Pmax, tiles, chunks;
+};
+cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const unsigned char *ws, const PrefixPart *x,
+                        cudaStream_t stream);
+
 // Attention over a shared prefix and each sequence's own keys (td_prefix.cu).
 struct PrefixPlan {
-  SplitPlan own;     // over the sequences' own keys
+  RunsPlan own;      // over the sequences' own keys
   int tiles, chunks; // 128-row tiles of a kv head, chunks of the prefix
-  size_t off_own, off_lse, off_part, bytes;  // workspace: own's, its fp32 out and lse, the prefix's partial blocks
+  int grid;
+  size_t off_part, bytes;  // workspace: own's, the prefix's partial blocks
 };
 struct PrefixAttn {
   const void *k, *v;  // [Hkv, Pmax, D]
   const int32_t *prefix_len;
-  float *part;
-  void *out;          // [B, Hq, T, D] bf16
-  float *lse;         // [B, Hq, T] or null
   int Pmax;
 };
 td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, PrefixPlan *plan);
-// own: the split parameters of the own keys, out and lse in the workspace.
-cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &own, cudaStream_t stream);
+// p: queries, own keys, results.
+cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &p, unsigned char *ws,
+                          cudaStream_t stream);
 
 // SM count of the current device (cached per device).
 int device_sm_count(int device);

@@ -3,104 +3,123 @@
 // The row (b, hq, t) attends the prefix's P keys and its sequence's own keys j < L_b - T + t + 1. Softmax sums over
 // disjoint key sets join exactly: with (m, l, acc) a part's maximum, sum of 2^(s - m) and sum of 2^(s - m) v,
 //   M = max m,  out = sum 2^(m - M) acc / sum 2^(m - M) l,  lse = M + log2 sum 2^(m - M) l   (base 2).
-// Three launches, each started while the one before still runs:
-//  A. prefix_kernel: of one kv head, the rows of all sequences (B x heads of the group x T tokens) form the M side of
-//     tensor-core tiles (tcgen05, 128 rows), so each K/V tile of the prefix serves 128 rows; the prefix is cut into as
-//     many chunks as fill the GPU once. Where one sequence at a time reads P keys for G x T rows, this reads them once
-//     per 128 rows, and several tiles of rows take the same chunk at the same time, from L2.
-//  B. the split kernels over each sequence's own keys (their PART instantiations: fp32 results, alongside A).
-//  C. merge_prefix_kernel: joins a row's parts, rounds once.
-// A is bound by the tensor cores and the exponentials where many sequences share the prefix, by memory where few do; B
-// by memory. A takes one CTA per SM, so that B's CTAs share the SMs with it.
+// Two launches. In prefix_kernel, one CTA an SM, three groups of warps work side by side:
+//  * softmax warps and the warps that issue products and copies take tiles over the prefix: of one kv head, the rows of
+//    all sequences (B x heads of the group x T tokens) form the M side of tensor-core products (tcgen05, 128 rows), so each
+//    K/V tile of the prefix serves 128 rows. The prefix is cut into as many chunks as fill the GPU once. Where one sequence
+//    at a time reads P keys for G x T rows, this reads them once per 128 rows;
+//  * four warps take runs over each sequence's own keys (td_runs.cuh, mma.sync).
+// The first is bound by the tensor cores and exponentials where many sequences share the prefix and by memory where few
+// do, the second by memory: in one CTA they fill each other's waits, and neither waits for the other's launch.
+// join_kernel then joins a row's parts and rounds once.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <mutex>
 
 #include "td_internal.h"
-#include "td_split_attn.cuh"
-#include "td_split_cluster.cuh"
-#include "td_split_mma.cuh"
+#include "td_runs.cuh"
 #include "td_tc.cuh"
 
 namespace td {
 
 namespace {
 
-constexpr int kPxSoftmaxWarps = 4;             // one query row per thread
-constexpr int kPxMmaWarp = kPxSoftmaxWarps;    // issues the tensor-core products
-constexpr int kPxLoadWarp = kPxSoftmaxWarps + 1;  // issues the TMA copies
-constexpr int kPxThreads = 32 * (kPxSoftmaxWarps + 2);
-constexpr int kPxRows = 128;                   // query rows per CTA
-constexpr int kPxQRegion = kPxRows * 128;      // bytes of one swizzled [128 rows][64 bf16] region
+constexpr int kPxSoftmaxWarps = 4;             // warps 0 .. 3: one query row per thread
+constexpr int kPxRunWarp = 4;                  // 4 .. 7: runs over the own keys
+constexpr int kPxMmaWarp = 8;                  // issues the tensor-core products
+constexpr int kPxLoadWarp = 9;                 // issues the TMA copies
+constexpr int kPxThreads = 384;                // three warpgroups (the last two warps have no work)
+constexpr int kPxRows = kPrefixRows;           // query rows per tile
 constexpr int kPxKRegion = kPfKeys * 128;      // bytes of one swizzled [64 keys][64 bf16] region
-constexpr int kMaxDevices = 64;
+// Registers a thread is launched with (65536 / 384, in steps of 8), and after the split where a run needs more: the product
+// and copy warps give up what the run warps take. 128 x (168 + 232 + 40) of the launch's 384 x 168.
+constexpr int kPxRunRegs = 232, kPxIssueRegs = 40;
+static_assert(128 * (168 + kPxRunRegs + kPxIssueRegs) <= 384 * 168, "register split within the launch's");
 
+#ifndef TD_PX_ST
+#define TD_PX_ST 3
+#endif
 template <int D>
 struct PxCfg {
+  static constexpr int NST = D == 128 ? TD_PX_ST : 2 * TD_PX_ST;  // buffers of K, and of V
   static constexpr int HALVES = D / 64;
-  static constexpr int Q_TILE = HALVES * kPxQRegion;
   static constexpr int KV_TILE = HALVES * kPxKRegion;
-  static constexpr int K_OFF = Q_TILE;                // two K buffers
-  static constexpr int V_OFF = K_OFF + 2 * KV_TILE;   // two V buffers
-  static constexpr int SMEM = V_OFF + 2 * KV_TILE + 1024;  // + alignment slack
-  static constexpr int TMEM_COLS = 256;               // S (64), two P buffers (32 each), O (D)
+  static constexpr int V_OFF = NST * KV_TILE;         // the K buffers come first
+  static constexpr int RUN_OFF = V_OFF + NST * KV_TILE;  // then the rings of the run warps
+  static constexpr int LEN_OFF = RUN_OFF + kRunWarps * RunCfg<D>::RING;  // then two ints a sequence and one
+  static constexpr int SMEM = LEN_OFF + 1024;         // + alignment slack
+  static constexpr int Q_COL = 128 + D;               // columns: S (64), two P buffers (32 each), O (D), Q (D / 2)
+  static constexpr int TMEM_COLS = D == 64 ? 256 : 512;
+  static_assert(SMEM + (2 * TD_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory");
 };
 
 struct PxArgs {
+  RunArgs own;       // the sequences' own keys; its p holds the queries too
   CUtensorMap kmap;  // prefix [Hkv][Pmax][D], boxes of 64 rows
   CUtensorMap vmap;
-  const void *q;     // [B, Hq, T, D]
   const int32_t *prefix_len;
-  float *part;       // [Hkv][tiles][chunks] blocks of part_floats(D)
-  uint32_t *status;
-  int B, Hq, Hkv, T, GT, Pmax;
+  float *part;       // [Hkv][tiles][chunks] blocks of prefix_block_floats(D) (td_runs.cuh)
+  int GT, Pmax;
   int tiles;         // 128-row tiles of a kv head's B * GT rows
   int chunks;        // chunks the prefix is cut into, at most
-  float qscale;      // scale * log2(e)
 };
 
-// A chunk's partial block: acc [D / 4][128 rows][4], then m [128] (base 2) and l [128].
-__host__ __device__ constexpr int part_floats(int D) { return kPxRows * (D + 2); }
-
-// Prefix length attended, and the keys of a chunk (whole tiles).
-__device__ __forceinline__ int prefix_keys(int raw, int Pmax) { return raw < 0 ? 0 : raw > Pmax ? Pmax : raw; }
-__device__ __forceinline__ int prefix_chunk(int P, int chunks) {
-  const int tiles = (P + kPfKeys - 1) / kPfKeys;
-  return (tiles + chunks - 1) / chunks * kPfKeys;
+// A tile's work: a kv head's rows [tile * 128, + rows) over keys [c0, c0 + 64 nkt), the last tile cut at c1.
+struct PxItem {
+  int tile, kvh, chunk, rows, c0, c1, nkt;
+};
+__device__ __forceinline__ PxItem px_item(const PxArgs &a, int item, int P) {
+  PxItem w;
+  w.tile = item % a.tiles;  // the tiles of rows that read one chunk are neighbours
+  w.kvh = item / a.tiles % a.own.p.Hkv;
+  w.chunk = item / a.tiles / a.own.p.Hkv;
+  w.rows = min(kPxRows, a.own.p.B * a.GT - w.tile * kPxRows);
+  const int S = prefix_chunk(P, a.chunks);
+  w.c0 = min(w.chunk * S, P);
+  w.c1 = min(w.c0 + S, P);
+  w.nkt = (w.c1 - w.c0 + kPfKeys - 1) / kPfKeys;
+  return w;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPxThreads, 2) prefix_kernel(const __grid_constant__ PxArgs a) {
+// NT: 8-row tiles of a run's row block. Buffers and barriers go round over all of a CTA's key tiles: tile g (counted over
+// its items) uses K / V buffer g % NST and S and P buffers g % 2.
+template <int D, int NT>
+__global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ PxArgs a) {
   using C = PxCfg<D>;
+  const SplitParams &p = a.own.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q, bar_k[2], bar_v[2], bar_s[2], bar_sfree, bar_p[2], bar_vfree[2], bar_o,
-      bar_fin;
+  __shared__ __align__(8) uint64_t bar_q, bar_k[C::NST], bar_v[C::NST], bar_s[2], bar_sfree, bar_p[2], bar_kfree[C::NST],
+      bar_vfree[C::NST], bar_pfree[2], bar_fin, run_bars[kRunWarps][RunCfg<D>::STAGES];
   __shared__ uint32_t s_taddr;
   __shared__ int s_issued[2], s_seen[2];  // wind-down: K / V tiles issued, and seen landed
+  __shared__ int s_red[kRunWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char *smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
-  // the tiles of rows that read one chunk are neighbours in the grid
-  const int tile = blockIdx.x % a.tiles, kvh = blockIdx.x / a.tiles % a.Hkv, chunk = blockIdx.x / a.tiles / a.Hkv;
 
   if (tid == 0) {
     mbar_init(smem_u32(&bar_q), kPxSoftmaxWarps);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NST; ++i) {
       mbar_init(smem_u32(&bar_k[i]), 1);
       mbar_init(smem_u32(&bar_v[i]), 1);
+      mbar_init(smem_u32(&bar_kfree[i]), 1);
+      mbar_init(smem_u32(&bar_vfree[i]), 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bar_s[i]), 1);
       mbar_init(smem_u32(&bar_p[i]), kPxSoftmaxWarps);
-      mbar_init(smem_u32(&bar_vfree[i]), 1);
+      mbar_init(smem_u32(&bar_pfree[i]), 1);
     }
     s_issued[0] = s_issued[1] = 0;
     s_seen[0] = s_seen[1] = 0;
     mbar_init(smem_u32(&bar_sfree), kPxSoftmaxWarps);
-    mbar_init(smem_u32(&bar_o), 1);
     mbar_init(smem_u32(&bar_fin), 1);
     fence_mbar_init();
   }
+  if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps && lane == 0) init_ring<D>(run_bars[warp - kPxRunWarp]);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
                  "n"(C::TMEM_COLS)
@@ -111,201 +130,244 @@ __global__ void __launch_bounds__(kPxThreads, 2) prefix_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_taddr;
-  const uint32_t tS = tmem, tP = tmem + kPfKeys, tO = tmem + 128;
+  const uint32_t tS = tmem, tP = tmem + kPfKeys, tO = tmem + 128, tQ = tmem + C::Q_COL;
 
   griddep_wait();
   griddep_launch_dependents();
-  const int raw = *a.prefix_len;
-  const int P = prefix_keys(raw, a.Pmax);
-  if (tid == 0 && blockIdx.x == 0)
-    report(a.status, (raw < 0 ? TD_DEV_NEGATIVE_SEQLEN : 0u) | (raw > a.Pmax ? TD_DEV_SEQLEN_CLAMPED : 0u));
-  const int S = prefix_chunk(P, a.chunks);
-  const int c0 = min(chunk * S, P), c1 = min(c0 + S, P);
-  const int nkt = (c1 - c0 + kPfKeys - 1) / kPfKeys;
-  const int rows = min(kPxRows, a.B * a.GT - tile * kPxRows);  // rows of this tile that exist
-  const float qscale = a.qscale;
   bool ok = true;
-  int kq = 0, kw = 0, vq = 0, vw = 0;
-  float m_ref = -INFINITY, l = 0.f;  // softmax threads: this row's reference maximum and sum
 
-  if (warp == kPxMmaWarp) {
-    if (lane == 0 && nkt > 0) {
-      constexpr uint32_t kIdS = mma_idesc(kPxRows, kPfKeys, false);
-      constexpr uint32_t kIdO = mma_idesc(kPxRows, D, true);
-      const uint64_t dq = smem_desc(sb, 16, 1024);
-      const uint64_t dk = smem_desc(sb + C::K_OFF, 16, 1024);
-      const uint64_t dv = smem_desc(sb + C::V_OFF, kPxKRegion, 1024);
-      auto issue_s = [&](int kt) {
-        const uint32_t kb = (uint32_t)(kt & 1) * C::KV_TILE;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k & 3) * 32;
-          tc_mma(tS, dq + (((uint32_t)(k >> 2) * kPxQRegion + off) >> 4),
-                 dk + ((kb + (uint32_t)(k >> 2) * kPxKRegion + off) >> 4), kIdS, k > 0);
-        }
-        tc_commit(smem_u32(&bar_s[kt & 1]));
-      };
-      ok = mbar_wait_bounded(smem_u32(&bar_q), 0) && mbar_wait_bounded(smem_u32(&bar_k[0]), 0);
-      if (ok) {
-        kw = 1;
-        issue_s(0);
-      }
-      for (int kt = 0; ok && kt < nkt; ++kt) {
-        const int b0 = kt & 1, b1 = b0 ^ 1;
-        if (kt + 1 < nkt) {
-          ok = mbar_wait_bounded(smem_u32(&bar_sfree), (uint32_t)kt & 1u);
-          ok = ok && mbar_wait_bounded(smem_u32(&bar_k[b1]), (uint32_t)((kt + 1) >> 1) & 1u);
-          if (!ok) break;
-          kw = kt + 2;
-          issue_s(kt + 1);
-        }
-        ok = mbar_wait_bounded(smem_u32(&bar_p[b0]), (uint32_t)(kt >> 1) & 1u) &&
-             mbar_wait_bounded(smem_u32(&bar_v[b0]), (uint32_t)(kt >> 1) & 1u);
-        if (!ok) break;
-        vw = kt + 1;
-        tc_fence_after();
-        const uint32_t vb = (uint32_t)b0 * C::KV_TILE;
-#pragma unroll
-        for (int k = 0; k < kPfKeys / 16; ++k)
-          tc_mma_ts(tO, tP + b0 * (kPfKeys / 2) + 8 * k, dv + ((vb + (uint32_t)k * 16 * 128) >> 4), kIdO, kt > 0 || k > 0);
-        tc_commit(smem_u32(&bar_o));
-        tc_commit(smem_u32(&bar_vfree[b0]));
-      }
-      s_seen[0] = kw;
-      s_seen[1] = vw;
-    }
-    __syncwarp();
-  } else if (warp == kPxLoadWarp) {
-    if (lane == 0 && nkt > 0) {
-      auto load = [&](bool v, int kt) {
-        const int buf = kt & 1;
-        const uint32_t bar = smem_u32(v ? &bar_v[buf] : &bar_k[buf]);
-        const uint32_t dst = sb + (v ? C::V_OFF : C::K_OFF) + buf * C::KV_TILE;
-        mbar_arrive_expect_tx(bar, C::KV_TILE);
-#pragma unroll
-        for (int h = 0; h < C::HALVES; ++h)
-          tma3(dst + h * kPxKRegion, v ? &a.vmap : &a.kmap, 64 * h, c0 + kt * kPfKeys, kvh, bar);
-      };
-      for (; kq < min(nkt, 2); ++kq) {
-        load(false, kq);
-        load(true, kq);
-      }
-      vq = kq;
-      for (int j = 2; ok && j < nkt; ++j) {
-        const uint32_t ph = (uint32_t)((j - 2) >> 1) & 1u;
-        ok = mbar_wait_bounded(smem_u32(&bar_s[j & 1]), ph);
-        if (!ok) break;
-        load(false, kq++);
-        ok = mbar_wait_bounded(smem_u32(&bar_vfree[j & 1]), ph);
-        if (!ok) break;
-        load(true, vq++);
-      }
-      s_issued[0] = kq;
-      s_issued[1] = vq;
-    }
-    __syncwarp();
-  } else if (nkt > 0) {
-    // the tile's query rows, each 16-byte chunk to its place in the swizzled tile (rows that do not exist: zeros)
-    for (int idx = tid; idx < kPxRows * (D / 8); idx += 32 * kPxSoftmaxWarps) {
-      const int r = idx / (D / 8), c = idx % (D / 8);
-      const bool real = r < rows;
-      const int row = real ? tile * kPxRows + r : 0;
-      const long long at = (long long)(row / a.GT) * a.Hq * a.T + (long long)kvh * a.GT + row % a.GT;
-      cp_async_16(sb + tile_chunk(kPxRows, r, c), static_cast<const uint4 *>(a.q) + at * (D / 8) + c, real ? 16u : 0u);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    fence_proxy_async_smem();  // read next by the tensor core (asynchronous proxy)
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bar_q));
-    const int busy = (rows + 31) / 32;  // warps with rows
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    // a warp without rows only keeps the barriers' count: what its lanes of P and O hold reaches no other row
-    for (int kt = 0; kt < nkt && warp >= busy; ++kt) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[kt & 1]), (uint32_t)(kt >> 1) & 1u))) {
-        ok = false;
-        break;
-      }
+  if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps) {
+    if constexpr (NT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxRunRegs));
+    int *s_len = reinterpret_cast<int *>(smem + C::LEN_OFF);  // [B]
+    int *s_prefix = s_len + p.B;                              // [B + 1]
+    const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp;
+    const int S = plan_runs<0, true, 1>(p, rt, s_len, s_prefix, s_red);
+    leave_plan(a.own.plan, p.B, s_prefix, S, rt);
+    run_warp<D, NT, 0>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
+                       smem + C::RUN_OFF + rw * RunCfg<D>::RING, run_bars[rw]);
+  } else if (warp >= kPxMmaWarp) {
+    if constexpr (NT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxIssueRegs));
+    const int P = prefix_keys(*a.prefix_len, a.Pmax);
+    const int items = P > 0 ? a.tiles * p.Hkv * a.chunks : 0;
+    if (warp == kPxMmaWarp) {
       if (lane == 0) {
-        mbar_arrive(smem_u32(&bar_sfree));
-        mbar_arrive(smem_u32(&bar_p[kt & 1]));
+        constexpr uint32_t kIdS = mma_idesc(kPxRows, kPfKeys, false);
+        constexpr uint32_t kIdO = mma_idesc(kPxRows, D, true);
+        const uint64_t dk = smem_desc(sb, 16, 1024);
+        const uint64_t dv = smem_desc(sb + C::V_OFF, kPxKRegion, 1024);
+        int kw = 0, vw = 0;  // K and V tiles seen landed
+        // S of tile g into the S columns, once every softmax warp has read the S before it and K has landed
+        auto issue_s = [&](int g) {
+          ok = (g == 0 || mbar_wait_bounded(smem_u32(&bar_sfree), (uint32_t)(g - 1) & 1u)) &&
+               mbar_wait_bounded(smem_u32(&bar_k[g % C::NST]), (uint32_t)(g / C::NST) & 1u);
+          if (!ok) return;
+          kw = g + 1;
+          const uint32_t kb = (uint32_t)(g % C::NST) * C::KV_TILE;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)(k & 3) * 32;
+            tc_mma_ts(tS, tQ + 8 * k, dk + ((kb + (uint32_t)(k >> 2) * kPxKRegion + off) >> 4), kIdS, k > 0);
+          }
+          tc_commit(smem_u32(&bar_s[g & 1]));
+          tc_commit(smem_u32(&bar_kfree[g % C::NST]));
+        };
+        int g = 0, it = 0;
+        for (int item = blockIdx.x; ok && item < items; item += gridDim.x, ++it) {
+          const PxItem w = px_item(a, item, P);
+          if (w.nkt == 0) break;  // later items are of the same or a later chunk
+          ok = mbar_wait_bounded(smem_u32(&bar_q), (uint32_t)it & 1u);
+          if (ok) issue_s(g);
+          for (int kt = 0; ok && kt < w.nkt; ++kt, ++g) {
+            const int b0 = g & 1, buf = g % C::NST;
+            if (kt + 1 < w.nkt) issue_s(g + 1);
+            // O += P V once the softmax warps have left P of g and V has landed
+            ok = ok && mbar_wait_bounded(smem_u32(&bar_p[b0]), (uint32_t)(g >> 1) & 1u) &&
+                 mbar_wait_bounded(smem_u32(&bar_v[buf]), (uint32_t)(g / C::NST) & 1u);
+            if (!ok) break;
+            vw = g + 1;
+            tc_fence_after();
+            const uint32_t vb = (uint32_t)buf * C::KV_TILE;
+#pragma unroll
+            for (int k = 0; k < kPfKeys / 16; ++k)
+              tc_mma_ts(tO, tP + b0 * (kPfKeys / 2) + 8 * k, dv + ((vb + (uint32_t)k * 16 * 128) >> 4), kIdO,
+                        kt > 0 || k > 0);
+            tc_commit(smem_u32(&bar_pfree[b0]));
+            tc_commit(smem_u32(&bar_vfree[buf]));
+          }
+        }
+        s_seen[0] = kw;
+        s_seen[1] = vw;
       }
+      __syncwarp();
+    } else if (warp == kPxLoadWarp) {
+      if (lane == 0) {
+        int g = 0;
+        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+          const PxItem w = px_item(a, item, P);
+          if (w.nkt == 0) break;
+          for (int kt = 0; kt < w.nkt; ++kt, ++g) {
+            const int buf = g % C::NST;
+            const uint32_t ph = (uint32_t)(g / C::NST - 1) & 1u;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              // each buffer once the product that read its previous tile is complete
+              ok = g < C::NST || mbar_wait_bounded(smem_u32(v ? &bar_vfree[buf] : &bar_kfree[buf]), ph);
+              if (!ok) break;
+              const uint32_t bar = smem_u32(v ? &bar_v[buf] : &bar_k[buf]);
+              const uint32_t dst = sb + (v ? C::V_OFF : 0) + buf * C::KV_TILE;
+              mbar_arrive_expect_tx(bar, C::KV_TILE);
+#pragma unroll
+              for (int h = 0; h < C::HALVES; ++h)
+                tma3(dst + h * kPxKRegion, v ? &a.vmap : &a.kmap, 64 * h, w.c0 + kt * kPfKeys, w.kvh, bar);
+              s_issued[v] = g + 1;
+            }
+            if (!ok) break;
+          }
+        }
+      }
+      __syncwarp();
     }
-    for (int kt = 0; kt < nkt && warp < busy; ++kt) {
-      const int b0 = kt & 1;
-      const uint32_t ph = (uint32_t)(kt >> 1) & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[b0]), ph))) {
-        ok = false;
-        break;
+  } else {
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const float qscale = p.qscale;
+    const int raw = *a.prefix_len;
+    const int P = prefix_keys(raw, a.Pmax);
+    if (tid == 0 && blockIdx.x == 0)
+      report(p.status, (raw < 0 ? TD_DEV_NEGATIVE_SEQLEN : 0u) | (raw > a.Pmax ? TD_DEV_SEQLEN_CLAMPED : 0u));
+    const int items = P > 0 ? a.tiles * p.Hkv * a.chunks : 0;
+    int g = 0;
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+      const PxItem w = px_item(a, item, P);
+      if (w.nkt == 0) break;
+      const int busy = (w.rows + 31) / 32;  // warps with rows
+      if (warp < busy) {
+        // this thread's query row into its TMEM lane, a column per pair of dims (rows that do not exist: zeros)
+        const int row = min(w.tile * kPxRows + tid, p.B * a.GT - 1);
+        const uint4 *qrow = static_cast<const uint4 *>(p.q) +
+                            ((long long)(row / a.GT) * p.Hq * p.T + (long long)w.kvh * a.GT + row % a.GT) * (D / 8);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t x[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = tid < w.rows ? qrow[8 * c + i] : make_uint4(0u, 0u, 0u, 0u);
+            x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+          }
+          tmem_st32(tQ + lane_base + 32 * c, x);
+        }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_q));
+      // a warp without rows only keeps the barriers' count: what its lanes of P and O hold reaches no other row
+      const int g0 = g;
+      g += w.nkt;
+      for (int k = g0; k < g && warp >= busy; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[k & 1]), (uint32_t)(k >> 1) & 1u))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bar_sfree));
+          mbar_arrive(smem_u32(&bar_p[k & 1]));
+        }
+      }
+      if (warp >= busy) continue;
+      float m_ref = -INFINITY, l = 0.f;  // this row's reference maximum and sum
+      for (int k = g0; k < g; ++k) {
+        const int b0 = k & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[b0]), (uint32_t)(k >> 1) & 1u))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int vis = min(kPfKeys, w.c1 - w.c0 - (k - g0) * kPfKeys);  // keys of the tile (fewer at the prefix's end alone)
+        if (vis < kPfKeys) {
+          // V rows behind the prefix, once landed: zeroed (a masked p of 0 must not meet a stale value)
+          const int buf = k % C::NST;
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[buf]), (uint32_t)(k / C::NST) & 1u))) {
+            ok = false;
+            break;
+          }
+          unsigned char *vt = smem + C::V_OFF + buf * C::KV_TILE;
+          for (int idx = tid; idx < (kPfKeys - vis) * (D / 8); idx += 32 * busy) {
+            const int r = vis + idx / (D / 8), c = idx % (D / 8);
+            *reinterpret_cast<uint4 *>(vt + tile_chunk(kPfKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();  // read next by the tensor core (asynchronous proxy)
+        }
+        float sv[kPfKeys];
+        tmem_ld64(tS + lane_base, sv);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_sfree));
+        if (vis < kPfKeys) {
+#pragma unroll
+          for (int i = 0; i < kPfKeys; ++i)
+            if (i >= vis) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
+        }
+        // the reference maximum moves only when the row's rises more than kRescaleGap above it (a row's first scores
+        // always move it); only then are O and l rescaled, once the previous product is complete
+        const float mx = (qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv)) * qscale;
+        const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
+        const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
+        if (move) {
+          l *= alpha;
+          m_ref = mx;
+        }
+        if (k > g0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0 ^ 1]), (uint32_t)((k - 1) >> 1) & 1u))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tO + lane_base + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(tO + lane_base + c, o);
+          }
+        }
+        const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
+        const SeenFirst seen{vis};
+        uint32_t pk[kPfKeys / 2];
+        if (vis == kPfKeys)
+          l += p_row<false>(sv, qscale, nbase, seen, pk);
+        else
+          l += p_row<true>(sv, qscale, nbase, seen, pk);
+        // into P buffer b0, once the product of tile k - 2 has read it
+        if (k >= 2) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0]), (uint32_t)((k - 2) >> 1) & 1u))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        tmem_st32(tP + b0 * (kPfKeys / 2) + lane_base, pk);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_p[b0]));
+      }
+      // the partial block, once the last product is complete: 512 consecutive bytes a warp and store
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u))) ok = false;
+      if (!ok) break;
       tc_fence_after();
-      const int vis = min(kPfKeys, c1 - c0 - kt * kPfKeys);  // keys of the tile (fewer at the prefix's end alone)
-      if (vis < kPfKeys) {
-        // V rows behind the prefix, once landed: zeroed (a masked p of 0 must not meet a stale value)
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[b0]), ph))) {
-          ok = false;
-          break;
-        }
-        unsigned char *vt = smem + C::V_OFF + b0 * C::KV_TILE;
-        for (int idx = tid; idx < (kPfKeys - vis) * (D / 8); idx += 32 * busy) {
-          const int r = vis + idx / (D / 8), c = idx % (D / 8);
-          *reinterpret_cast<uint4 *>(vt + tile_chunk(kPfKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
-      float sv[kPfKeys];
-      tmem_ld64(tS + lane_base, sv);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_sfree));
-      if (vis < kPfKeys) {
+      float *blk = a.part + (((long long)w.kvh * a.tiles + w.tile) * a.chunks + w.chunk) * prefix_block_floats(D);
 #pragma unroll
-        for (int i = 0; i < kPfKeys; ++i)
-          if (i >= vis) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
-      }
-      const float mx = (qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv)) * qscale;
-      const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
-      const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
-      if (move) {
-        l *= alpha;
-        m_ref = mx;
-      }
-      if (kt > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_o), (uint32_t)(kt - 1) & 1u))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(tO + lane_base + c, o);
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(tO + lane_base + c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
-          tmem_st32(tO + lane_base + c, o);
-        }
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4 *>(blk + ((c + i) / 4 * kPxRows + tid) * 4) =
+              make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
-      const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
-      const SeenFirst seen{vis};
-      uint32_t pk[kPfKeys / 2];
-      if (vis == kPfKeys)
-        l += p_row<false>(sv, qscale, nbase, seen, pk);
-      else
-        l += p_row<true>(sv, qscale, nbase, seen, pk);
-      if (kt >= 2) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_vfree[b0]), (uint32_t)((kt - 2) >> 1) & 1u))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      tmem_st32(tP + b0 * (kPfKeys / 2) + lane_base, pk);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_p[b0]));
+      blk[kPxRows * D + tid] = m_ref;
+      blk[kPxRows * (D + 1) + tid] = l;
     }
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_o), (uint32_t)(nkt - 1) & 1u))) ok = false;
   }
   ok = __syncthreads_and(ok) != 0;
   if (!ok) {
@@ -315,210 +377,86 @@ __global__ void __launch_bounds__(kPxThreads, 2) prefix_kernel(const __grid_cons
       mbar_wait_bounded(smem_u32(&bar_fin), 0);
     }
     if (tid == kPxLoadWarp * 32) {
-      for (int kt = s_seen[0]; kt < s_issued[0]; ++kt)
-        mbar_wait_bounded(smem_u32(&bar_k[kt & 1]), (uint32_t)(kt >> 1) & 1u);
-      for (int kt = s_seen[1]; kt < s_issued[1]; ++kt)
-        mbar_wait_bounded(smem_u32(&bar_v[kt & 1]), (uint32_t)(kt >> 1) & 1u);
-      report(a.status, TD_DEV_WAIT_TIMEOUT);
+      for (int g = s_seen[0]; g < s_issued[0]; ++g)
+        mbar_wait_bounded(smem_u32(&bar_k[g % C::NST]), (uint32_t)(g / C::NST) & 1u);
+      for (int g = s_seen[1]; g < s_issued[1]; ++g)
+        mbar_wait_bounded(smem_u32(&bar_v[g % C::NST]), (uint32_t)(g / C::NST) & 1u);
+      report(p.status, TD_DEV_WAIT_TIMEOUT);
     }
-  }
-  __syncthreads();
-  tc_fence_after();
-  if (warp < kPxSoftmaxWarps && nkt > 0 && warp * 32 < rows) {
-    // the partial block: 512 consecutive bytes a warp and store
-    float *blk = a.part + (((long long)kvh * a.tiles + tile) * a.chunks + chunk) * part_floats(D);
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-#pragma unroll
-    for (int c = 0; c < D; c += 32) {
-      float o[32];
-      tmem_ld32(tO + lane_base + c, o);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4)
-        *reinterpret_cast<float4 *>(blk + ((c + i) / 4 * kPxRows + tid) * 4) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-    }
-    blk[kPxRows * D + tid] = m_ref;
-    blk[kPxRows * (D + 1) + tid] = ok ? l : 0.f;
   }
   tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::TMEM_COLS) : "memory");
 }
 
-struct MergeArgs {
-  const float *part;      // prefix_kernel's blocks
-  const float *own, *own_lse;  // [B, Hq, T, D] and [B, Hq, T] (natural log) of the sequences' own keys
-  const int32_t *prefix_len;
-  void *out;              // [B, Hq, T, D] bf16
-  float *lse;             // [B, Hq, T] or null
-  int B, Hq, Hkv, T, GT, Pmax, tiles, chunks;
-};
-
-// Joins the parts of 32 rows (one tile's), 32 dims: a lane a row, a warp four dims.
-constexpr int kJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) merge_prefix_kernel(const MergeArgs a) {
-  const int slab = blockIdx.x % (D / 32), group = blockIdx.x / (D / 32) % (a.tiles * 4), kvh = blockIdx.x / (D / 32) / (a.tiles * 4);
-  const int tile = group / 4, lane = threadIdx.x & 31;
-  const int r = group % 4 * 32 + lane, row = tile * kPxRows + r;
-  const int d4 = slab * 8 + threadIdx.x / 32;
-  griddep_wait();
-  griddep_launch_dependents();
-  if (row >= a.B * a.GT) return;
-  const int P = prefix_keys(__ldcg(a.prefix_len), a.Pmax);
-  const int S = prefix_chunk(P, a.chunks);
-  const int nc = P > 0 ? (P + S - 1) / S : 0;
-  const float *blk = a.part + ((long long)kvh * a.tiles + tile) * a.chunks * part_floats(D);
-  const long long at = (long long)(row / a.GT) * a.Hq * a.T + (long long)kvh * a.GT + row % a.GT;
-  const float own2 = __ldcg(a.own_lse + at) * kLog2e;
-  float M = own2, L = own2 == -INFINITY ? 0.f : 1.f;
-  float4 A = __ldcg(reinterpret_cast<const float4 *>(a.own + at * D) + d4);
-  if (L == 0.f) A = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 8;  // chunks whose loads are in flight at once
-  for (int c0 = 0; c0 < nc; c0 += kBatch) {
-    float m[kBatch], l[kBatch];
-    float4 x[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const float *pb = blk + (long long)(c0 + i) * part_floats(D);
-      const bool in = c0 + i < nc;
-      m[i] = in ? __ldcg(pb + kPxRows * D + r) : -INFINITY;
-      l[i] = in ? __ldcg(pb + kPxRows * (D + 1) + r) : 0.f;
-      x[i] = in ? __ldcg(reinterpret_cast<const float4 *>(pb) + d4 * kPxRows + r) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float Mn = M;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (l[i] > 0.f) Mn = fmaxf(Mn, m[i]);
-    const float base = Mn == -INFINITY ? 0.f : Mn;
-    const float alpha = exp2f(M - base);
-    L *= alpha;
-    A.x *= alpha, A.y *= alpha, A.z *= alpha, A.w *= alpha;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (l[i] > 0.f) {
-        const float f = exp2f(m[i] - base);
-        L = fmaf(l[i], f, L);
-        A.x = fmaf(x[i].x, f, A.x), A.y = fmaf(x[i].y, f, A.y), A.z = fmaf(x[i].z, f, A.z), A.w = fmaf(x[i].w, f, A.w);
-      }
-    }
-    M = Mn;
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + d4 * 4) =
-      make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
-  if (a.lse != nullptr && d4 == 0) a.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+template <int D, int NT>
+cudaError_t launch_nt(const PxArgs &a, int grid, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(reinterpret_cast<const void *>(&prefix_kernel<D, NT>),
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PxCfg<D>::SMEM + (2 * TD_MAX_BATCH + 1) * (int)sizeof(int));
+  });
+  if (attr != cudaSuccess) return attr;
+  const size_t smem = PxCfg<D>::SMEM + (2 * (size_t)a.own.p.B + 1) * sizeof(int);
+  return launch_pdl(prefix_kernel<D, NT>, dim3(grid), dim3(kPxThreads), smem, stream, a);
 }
 
 template <int D>
-cudaError_t opt_in() {
-  static std::mutex mu;
-  static bool done[kMaxDevices] = {};
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  if (done[device]) return cudaSuccess;
-  constexpr int persistent = MmaCfg<D, kPersistentStages<D>>::RING_BYTES + 1024;
-  const struct {
-    const void *fn;
-    int smem;
-    bool cluster;
-  } all[] = {{reinterpret_cast<const void *>(&prefix_kernel<D>), PxCfg<D>::SMEM, false},
-             {reinterpret_cast<const void *>(&split_attn_mma_kernel<D, false, kTileN8, 0, true>), persistent, false},
-             {reinterpret_cast<const void *>(&split_attn_mma_kernel<D, false, kTileM16, 0, true>), persistent, false},
-             {reinterpret_cast<const void *>(&split_attn_mma_kernel<D, false, kTileN24, 0, true>), persistent, false},
-             {reinterpret_cast<const void *>(&split_attn_cluster_kernel<D, kTileN8, 0, true>), cluster_smem<D>(), true},
-             {reinterpret_cast<const void *>(&split_attn_cluster_kernel<D, kTileM16, 0, true>), cluster_smem<D>(), true},
-             {reinterpret_cast<const void *>(&split_attn_cluster_kernel<D, kTileN24, 0, true>), cluster_smem<D>(), true}};
-  for (const auto &k : all) {
-    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
-    if (e == cudaSuccess && k.cluster) e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  done[device] = true;
-  return cudaSuccess;
-}
-
-// The split kernels over the sequences' own keys: fp32 out and lse (p.out, p.lse).
-template <int D>
-cudaError_t launch_own(const SplitPlan &plan, const SplitParams &p, cudaStream_t stream) {
-  MmaArgs a;
-  if (!encode_cache_map(&a.kmap, p.k, p.B, p.Hkv, p.Smax, D) || !encode_cache_map(&a.vmap, p.v, p.B, p.Hkv, p.Smax, D))
-    return cudaErrorInvalidValue;
-  a.p = p;
-  const int tile = tile_of_rows(p.R);
-  if (plan.cluster > 0) {
-    cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = cluster_config(D, plan.grid, plan.cluster, stream, attr);
-    if (tile == kTileN8) return cudaLaunchKernelEx(&cfg, split_attn_cluster_kernel<D, kTileN8, 0, true>, a);
-    if (tile == kTileM16) return cudaLaunchKernelEx(&cfg, split_attn_cluster_kernel<D, kTileM16, 0, true>, a);
-    return cudaLaunchKernelEx(&cfg, split_attn_cluster_kernel<D, kTileN24, 0, true>, a);
-  }
-  const dim3 grid(plan.grid), block(kThreads);
-  if (tile == kTileN8) return launch_pdl(split_attn_mma_kernel<D, false, kTileN8, 0, true>, grid, block, plan.smem, stream, a);
-  if (tile == kTileM16) return launch_pdl(split_attn_mma_kernel<D, false, kTileM16, 0, true>, grid, block, plan.smem, stream, a);
-  return launch_pdl(split_attn_mma_kernel<D, false, kTileN24, 0, true>, grid, block, plan.smem, stream, a);
-}
-
-template <int D>
-cudaError_t launch_d(const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &own, cudaStream_t stream) {
-  cudaError_t e = opt_in<D>();
-  if (e != cudaSuccess) return e;
+cudaError_t launch_d(const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &p, unsigned char *ws, float *part,
+                     cudaStream_t stream) {
   PxArgs a;
-  if (!encode_cache_map(&a.kmap, x.k, 1, own.Hkv, x.Pmax, D) || !encode_cache_map(&a.vmap, x.v, 1, own.Hkv, x.Pmax, D))
+  if (!fill_runs(&a.own, D, plan.own, p, ws) || !encode_cache_map(&a.kmap, x.k, 1, p.Hkv, x.Pmax, D) ||
+      !encode_cache_map(&a.vmap, x.v, 1, p.Hkv, x.Pmax, D))
     return cudaErrorInvalidValue;
-  a.q = own.q;
   a.prefix_len = x.prefix_len;
-  a.part = x.part;
-  a.status = own.status;
-  a.B = own.B, a.Hq = own.Hq, a.Hkv = own.Hkv, a.T = own.T, a.GT = own.G * own.T, a.Pmax = x.Pmax;
+  a.part = part;
+  a.GT = p.G * p.T, a.Pmax = x.Pmax;
   a.tiles = plan.tiles, a.chunks = plan.chunks;
-  a.qscale = own.qscale;
-  e = launch_pdl(prefix_kernel<D>, dim3((unsigned)(plan.tiles * own.Hkv * plan.chunks)), dim3(kPxThreads), PxCfg<D>::SMEM,
-                 stream, a);
-  if (e == cudaSuccess) e = launch_own<D>(plan.own, own, stream);
-  if (e != cudaSuccess) return e;
-  const MergeArgs m{x.part, static_cast<const float *>(own.out), own.lse, x.prefix_len, x.out, x.lse, own.B, own.Hq,
-                    own.Hkv, own.T, a.GT, x.Pmax, plan.tiles, plan.chunks};
-  return launch_pdl(merge_prefix_kernel<D>, dim3((unsigned)(own.Hkv * plan.tiles * 4 * (D / 32))), dim3(kJoinThreads), 0,
-                    stream, m);
+  const int nt = (plan.own.R + 7) / 8;
+  return nt == 1   ? launch_nt<D, 1>(a, plan.grid, stream)
+         : nt == 2 ? launch_nt<D, 2>(a, plan.grid, stream)
+                   : launch_nt<D, 3>(a, plan.grid, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-#ifndef TD_PX_PER
-#define TD_PX_PER 1
-#endif
 td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, PrefixPlan *plan) {
-  const td_status st = plan_split(TD_BF16, B, Hq, Hkv, T, Smax, D, 0, &plan->own);
+  if (D != 64 && D != 128) return TD_ERR_UNSUPPORTED;
+  if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Smax < 1 || Pmax < 1 || Hq % Hkv != 0) return TD_ERR_INVALID_ARG;
+  if (B > TD_MAX_BATCH || Smax > (1 << 30) || Pmax > (1 << 30) || T > Smax) return TD_ERR_UNSUPPORTED;
+  const td_status st = plan_attn_runs(B, Hq, Hkv, T, Smax, D, 1, &plan->own);
   if (st != TD_OK) return st;
-  if (Pmax < 1) return TD_ERR_INVALID_ARG;
-  if (Pmax > (1 << 30)) return TD_ERR_UNSUPPORTED;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return TD_ERR_CUDA;
   const long long rows = (long long)B * (Hq / Hkv) * T;
   const long long tiles = (rows + kPxRows - 1) / kPxRows;
   const long long groups = tiles * Hkv;
+  const int sms = device_sm_count(device);
   // chunks that fill the GPU once, of at least two tiles of keys
-  long long chunks = TD_PX_PER * (long long)device_sm_count(device) / groups;
+  long long chunks = sms / groups;
   chunks = std::min(chunks, ((long long)Pmax + 2 * kPfKeys - 1) / (2 * kPfKeys));
   if (chunks < 1) chunks = 1;
   if (groups * chunks * 16 > 0x7fffffffLL || rows > (1 << 26)) return TD_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;
   plan->chunks = (int)chunks;
-  const size_t out_rows = (size_t)B * Hq * T;
-  plan->off_own = align256(plan->own.bytes);
-  plan->off_lse = plan->off_own + align256(out_rows * D * sizeof(float));
-  plan->off_part = plan->off_lse + align256(out_rows * sizeof(float));
-  plan->bytes = plan->off_part + align256((size_t)(groups * chunks) * part_floats(D) * sizeof(float));
+  plan->grid = (int)std::min((long long)sms, std::max((long long)plan->own.grid, groups * chunks));
+  plan->off_part = align256(plan->own.bytes);
+  plan->bytes = plan->off_part + align256((size_t)(groups * chunks) * prefix_block_floats(D) * sizeof(float));
   return TD_OK;
 }
 
-cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &own, cudaStream_t stream) {
-  const cudaError_t e = D == 64 ? launch_d<64>(plan, x, own, stream) : launch_d<128>(plan, x, own, stream);
-  if (e != cudaSuccess) cudaGetLastError();  // reported once, by this call
+cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &p, unsigned char *ws,
+                          cudaStream_t stream) {
+  float *part = reinterpret_cast<float *>(ws + plan.off_part);
+  cudaError_t e = D == 64 ? launch_d<64>(plan, x, p, ws, part, stream) : launch_d<128>(plan, x, p, ws, part, stream);
+  const PrefixPart joined{part, x.prefix_len, x.Pmax, plan.tiles, plan.chunks};
+  if (e == cudaSuccess) e = launch_join(D, plan.own, p, ws, &joined, stream);
   return e;
 }
 

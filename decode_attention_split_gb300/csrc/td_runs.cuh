@@ -1,0 +1,439 @@
+// Split attention in equal runs of 16-key steps, a run a warp, for bf16 caches; the parts of a row meet in a launch
+// of their own (join_kernel).
+//
+// The keys of every group (sequence, kv head, row block of at most 24 rows) are cut into steps of 16, one group after
+// another, and the steps into equal runs. Each warp takes one run on its own: lane 0 keeps its ring of stages (16 keys of
+// K and V each, TMA) full across the ends of groups, so a warp that finishes one group and starts the next has
+// copies in flight all the time, and no barrier ties the warps of a CTA together once the runs are planned. Where
+// a CTA's warps share a chunk instead (split_attn_mma_kernel), starting and finishing a chunk costs a CTA as much as a few
+// stages of 64 keys, and chunks of one size leave CTAs idle: many short sequences, windows among them, pay both.
+// A warp leaves each group it met as one partial block, so a row has as many parts as runs touch its group.
+#pragma once
+
+#include "td_internal.h"
+#include "td_split_mma.cuh"
+
+namespace td {
+
+#ifndef TD_RUN_ST
+#define TD_RUN_ST 3
+#endif
+#ifndef TD_RUN_GU
+#define TD_RUN_GU 1
+#endif
+#ifndef TD_RUN_MIN
+#define TD_RUN_MIN(R) 2
+#endif
+constexpr int kRunWarps = 4;
+constexpr int kRunThreads = 32 * kRunWarps;
+constexpr int kRunKeys = 16;  // keys of a step and stage
+static_assert(kRunThreads == kThreads, "lengths_unchanged is written for CTAs of kThreads");
+
+template <int D>
+struct RunCfg {
+  static constexpr int STAGES = D == 128 ? TD_RUN_ST : 2 * TD_RUN_ST;  // of a warp's ring
+  static constexpr int HALVES = D / 64;
+  static constexpr int BOX = kRunKeys * 128;             // 16 rows x 128 bytes
+  static constexpr int TILE = HALVES * BOX;              // K or V of a stage
+  static constexpr int RING = STAGES * 2 * TILE;
+  static constexpr int SMEM = kRunWarps * RING + 1024;   // + alignment slack; then two ints a sequence and one
+};
+
+struct RunArgs {
+  CUtensorMap kmap;  // caches [B*Hkv][Smax][D], boxes of 16 rows
+  CUtensorMap vmap;
+  SplitParams p;
+  int *plan;         // workspace: [B + 1] units before each sequence, then the units of a run
+};
+bool fill_runs(RunArgs *a, int D, const RunsPlan &plan, const SplitParams &p, unsigned char *ws);
+
+// A partial block: acc [D / 4][R][4] (sums of 2^(s - m) v), then m [R] (base 2) and l [R]; whole 16-byte units, so that
+// every block's sums can be read four at a time.
+__host__ __device__ constexpr int run_block_floats(int R, int D) { return (R * (D + 2) + 3) / 4 * 4; }
+
+// Units of a group of `keys` keys: its steps, and as many units as starting and finishing it costs, ahead of its own.
+constexpr int kRunGroupUnits = TD_RUN_GU;
+__device__ __forceinline__ int run_steps(int keys) { return (keys + kRunKeys - 1) / kRunKeys; }
+__device__ __forceinline__ int run_units(int keys) { return keys > 0 ? run_steps(keys) + kRunGroupUnits : 0; }
+// The block of group g's keys in run r: runs and groups advance together, so every (group, run) that meet have their own.
+__device__ __forceinline__ long long run_block(long long g, int r) { return g + r; }
+
+// A barrier of the kRunThreads threads that take runs (id 0 where they are the whole CTA).
+template <int ID>
+__device__ __forceinline__ void run_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kRunThreads) : "memory");
+}
+
+// Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]); returns the units of a
+// run. By kRunThreads threads, `tid` theirs, meeting at barrier BAR. REPORT: with the status bits that the lengths raise.
+// Ends with a barrier.
+template <int WIN, bool REPORT, int BAR>
+__device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefix, int *s_red) {
+  const int lane = tid & 31, warp = tid >> 5;
+  const int U = p.Hkv * p.RB, per = (p.B + kRunThreads - 1) / kRunThreads, b0 = tid * per;
+  int seg = 0;
+  uint32_t bits = 0;
+  for (int b = b0; b < min(b0 + per, p.B); ++b) {
+    const int L = attended_len(p, ld_relaxed(p.seq_lens + b), bits);
+    s_len[b] = L;
+    seg += run_units(keys_of<WIN>(p, L)) * U;
+  }
+  if (REPORT && blockIdx.x == 0) report(p.status, bits);
+  int incl = seg;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  run_barrier<BAR>();  // s_red may still be read by an earlier plan
+  if (lane == 31) s_red[warp] = incl;
+  run_barrier<BAR>();
+  int W = 0, before = incl - seg;
+#pragma unroll
+  for (int w = 0; w < kRunWarps; ++w) {
+    if (w < warp) before += s_red[w];
+    W += s_red[w];
+  }
+  for (int b = b0; b < min(b0 + per, p.B); ++b) {
+    s_prefix[b] = before;
+    before += run_units(keys_of<WIN>(p, s_len[b])) * U;
+  }
+  if (tid == 0) s_prefix[p.B] = W;
+  run_barrier<BAR>();
+  const int runs = gridDim.x * kRunWarps;
+  return max((W + runs - 1) / runs, TD_RUN_MIN(p.R));
+}
+
+// Where a warp is in its run: group `ug` of sequence b, steps [s, e) of it left in this run.
+struct RunCursor {
+  int b, ug, s, e;
+  int base;  // units before this group
+};
+
+// Moves the cursor to the next group with steps in units [.., u1); e = s where none is left.
+template <int WIN>
+__device__ __forceinline__ void next_group(const SplitParams &p, const int *s_len, int u1, RunCursor &c) {
+  const int U = p.Hkv * p.RB;
+  c.s = c.e = 0;
+  c.base += run_units(keys_of<WIN>(p, s_len[c.b]));
+  if (++c.ug == U) {
+    c.ug = 0;
+    do {
+      if (++c.b >= p.B) return;
+    } while (s_len[c.b] == 0);
+  }
+  if (c.base + kRunGroupUnits < u1) c.e = min(run_steps(keys_of<WIN>(p, s_len[c.b])), u1 - c.base - kRunGroupUnits);
+}
+
+// A warp's ring: its barriers, by one thread.
+template <int D>
+__device__ __forceinline__ void init_ring(uint64_t *bars) {
+#pragma unroll
+  for (int i = 0; i < RunCfg<D>::STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+  fence_mbar_init();
+}
+
+// What the join needs of the plan, from the first CTA.
+__device__ __forceinline__ void leave_plan(int *plan, int B, const int *s_prefix, int S, int tid) {
+  if (blockIdx.x != 0) return;
+  for (int b = tid; b <= B; b += kRunThreads) plan[b] = s_prefix[b];
+  if (tid == 0) plan[B + 1] = S;
+}
+
+// One warp's run: number `run`, S units long. The warp's ring (1024-byte aligned) and its barriers (initialised, one arrival).
+// WIN: kWindowPad for windowed attention, else 0.
+template <int D, int NT, int WIN>
+__device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                         const int *s_len, const int *s_prefix, int S, int run, unsigned char *ring_p,
+                                         uint64_t *bars) {
+  using C = RunCfg<D>;
+  constexpr int KSD = D / 16, NL = 2 * NT;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const uint32_t ring = smem_u32(ring_p);
+  const int W = s_prefix[p.B], GT = p.G * p.T;
+  const int u0 = (int)min((long long)run * S, (long long)W), u1 = (int)min((long long)u0 + S, (long long)W);
+  const uint64_t policy = l2_evict_first_policy();
+
+  // the first group of the run
+  RunCursor c{};
+  if (u0 < u1) {
+    int lo = 0, hi = p.B - 1;  // the last sequence whose units start at or before u0 (those without keys have none)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_prefix[mid] <= u0) lo = mid; else hi = mid - 1;
+    }
+    const int n = run_units(keys_of<WIN>(p, s_len[lo]));
+    c.b = lo;
+    c.ug = (u0 - s_prefix[lo]) / n;
+    c.base = s_prefix[lo] + c.ug * n;
+    c.s = max(u0 - c.base - kRunGroupUnits, 0);
+    c.e = max(min(n, u1 - c.base) - kRunGroupUnits, 0);
+    if (c.s >= c.e) next_group<WIN>(p, s_len, u1, c);
+  }
+  RunCursor ahead = c;  // the next step to be fetched
+  int fetched = 0, used = 0;
+  auto fetch = [&]() {  // lane 0 of a warp whose ring has room
+    const int buf = fetched % C::STAGES;
+    const uint32_t bar = smem_u32(&bars[buf]);
+    const uint32_t kdst = ring + buf * 2 * C::TILE, vdst = kdst + C::TILE;
+    const int key = ahead.s * kRunKeys, z = ahead.b * p.Hkv + ahead.ug / p.RB;
+    int row = key;
+    if constexpr (WIN != 0) {
+      const WindowSpan span = window_span<WIN>(p.window, p.sinks, p.T, s_len[ahead.b]);
+      if (key >= span.head) row += span.shift;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive_expect_tx(bar, 2 * C::TILE);
+#pragma unroll
+    for (int h = 0; h < C::HALVES; ++h) {
+      tma_load_3d(kdst + h * C::BOX, &kmap, 64 * h, row, z, bar, policy);
+      tma_load_3d(vdst + h * C::BOX, &vmap, 64 * h, row, z, bar, policy);
+    }
+  };
+  auto step_ahead = [&]() {  // the cursor is the warp's, whichever lane issues
+    if (ahead.s >= ahead.e) return;
+    if (lane == 0) fetch();
+    ++fetched;
+    if (++ahead.s == ahead.e) next_group<WIN>(p, s_len, u1, ahead);
+  };
+#pragma unroll 1
+  for (int i = 0; i < C::STAGES; ++i) step_ahead();
+
+  bool ok = true;
+  while (ok && c.s < c.e) {
+    // one group: its query rows as B fragments of each n tile
+    const int rb = c.ug % p.RB, kvh = c.ug / p.RB, L = s_len[c.b];
+    const int keys = keys_of<WIN>(p, L);
+    WindowSpan span = {};
+    if constexpr (WIN != 0) span = window_span<WIN>(p.window, p.sinks, p.T, L);
+    uint32_t qb[NT][KSD][2];
+    int lim[NL];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + gid, gr = rb * p.R + r;
+      const bool there = r < p.R && gr < GT;
+      const uint32_t *qrow = static_cast<const uint32_t *>(p.q) +
+                             ((long long)c.b * p.Hq * p.T + (long long)kvh * GT + (there ? gr : 0)) * (D / 2) + tig;
+#pragma unroll
+      for (int j = 0; j < KSD; ++j) {
+        qb[nt][j][0] = there ? __ldcg(qrow + 8 * j) : 0u;
+        qb[nt][j][1] = there ? __ldcg(qrow + 8 * j + 4) : 0u;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rl = 8 * nt + 2 * tig + e, gl = rb * p.R + rl;
+        lim[2 * nt + e] = rl < p.R && gl < GT ? max(L - p.T + gl % p.T + 1 - span.shift, 0) : 0;
+      }
+    }
+    float o[NT][KSD][4], m_run[NL], l_run[NL];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < KSD; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+#pragma unroll
+    for (int h = 0; h < NL; ++h) m_run[h] = -INFINITY, l_run[h] = 0.f;
+#pragma unroll 1
+    for (; c.s < c.e; ++c.s) {
+      const int buf = used % C::STAGES;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bars[buf]), (uint32_t)(used / C::STAGES) & 1u))) {
+        ok = false;
+        break;
+      }
+      const uint32_t kt = ring + buf * 2 * C::TILE, vt = kt + C::TILE;
+      const int key0 = c.s * kRunKeys;
+      // V rows that no row of the batch sees: behind the sequence's end, or padding of the window's head. Zeroed, so
+      // that a masked probability meets no stale value
+      int z0 = keys - key0, z1 = kRunKeys;
+      if (WIN != 0 && key0 < span.head) z0 = p.sinks - key0, z1 = min(z1, span.head - key0);
+      if (z0 < z1) {
+        unsigned char *vrow = ring_p + buf * 2 * C::TILE + C::TILE;
+        z0 = max(z0, 0);
+        for (int i = lane; i < (z1 - z0) * (D / 8); i += 32)
+          *reinterpret_cast<uint4 *>(vrow + tma_swz<kRunKeys>(z0 + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();  // precedes the stage's next refill by the TMA unit
+        __syncwarp();
+      }
+      if constexpr (NT == 1)
+        warp_keys16_n8<D, WIN, kRunKeys>(qb[0], kt, vt, 0, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
+      else
+        warp_keys16_nt<D, WIN, NT, kRunKeys>(qb, kt, vt, 0, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
+      ++used;
+      __syncwarp();  // every lane has read the stage
+      step_ahead();
+    }
+    // this run's part of the group
+    float *blk = p.ws_part + run_block(((long long)c.b * p.Hkv + kvh) * p.RB + rb, run) * run_block_floats(p.R, D);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = l_run[2 * nt + e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int r = 8 * nt + 2 * tig + e;
+        if (r >= p.R) continue;
+        float *row = blk + 4 * r + (gid & 3);
+#pragma unroll
+        for (int dt = 0; dt < KSD; ++dt) {
+          row[(4 * dt + gid / 4) * 4 * p.R] = o[nt][dt][e];
+          row[(4 * dt + 2 + gid / 4) * 4 * p.R] = o[nt][dt][2 + e];
+        }
+        if (gid == 0) {
+          blk[p.R * D + r] = m_run[2 * nt + e];
+          blk[p.R * (D + 1) + r] = ok ? l : 0.f;
+        }
+      }
+    if (ok) next_group<WIN>(p, s_len, u1, c);
+  }
+  if (!ok) {
+    // a copy never completed: the others in flight are waited for (bounded) before the ring goes
+    if (lane == 0) {
+      for (int i = used; i < fetched; ++i)
+        mbar_wait_bounded(smem_u32(&bars[i % C::STAGES]), (uint32_t)(i / C::STAGES) & 1u);
+      report(p.status, TD_DEV_WAIT_TIMEOUT);
+    }
+  }
+}
+
+template <int D, int NT, int WIN>
+__global__ void __launch_bounds__(kRunThreads, 2) runs_kernel(const __grid_constant__ RunArgs a) {
+  using C = RunCfg<D>;
+  const SplitParams &p = a.p;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ int s_red[kRunWarps];
+  __shared__ __align__(8) uint64_t s_bars[kRunWarps][C::STAGES];
+  int *s_len = reinterpret_cast<int *>(smem_raw + C::SMEM);  // [B]
+  int *s_prefix = s_len + p.B;                               // [B + 1]
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if ((tid & 31) == 0) init_ring<D>(s_bars[warp]);
+  // planned on the lengths as they read before the wait for the previous kernel, again if they read otherwise after it
+  int S = plan_runs<WIN, false, 0>(p, tid, s_len, s_prefix, s_red);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!lengths_unchanged(p, s_len)) S = plan_runs<WIN, true, 0>(p, tid, s_len, s_prefix, s_red);
+  leave_plan(a.plan, p.B, s_prefix, S, tid);
+  run_warp<D, NT, WIN>(p, a.kmap, a.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + warp,
+                       align1024(smem_raw) + warp * C::RING, s_bars[warp]);
+}
+
+// Joins the parts of a row: those that the runs left of its own keys and, of a batch behind a shared prefix, one per
+// chunk of the prefix (blocks acc [D / 4][128 rows][4], m [128], l [128] of 128-row tiles).
+struct JoinArgs {
+  const float *runs;      // runs_kernel's blocks
+  const int *plan;        // and what it left in RunArgs::plan
+  const float *prefix;    // [Hkv][tiles][chunks] blocks, or null
+  const int32_t *prefix_len;
+  void *out;              // [B, Hq, T, D] bf16
+  float *lse;             // [B, Hq, T] or null
+  int B, Hq, Hkv, T, GT, R, RB, Pmax, tiles, chunks;
+};
+
+// Prefix length attended, and the keys of a chunk of it (whole tiles of 64).
+__device__ __forceinline__ int prefix_keys(int raw, int Pmax) { return raw < 0 ? 0 : raw > Pmax ? Pmax : raw; }
+__device__ __forceinline__ int prefix_chunk(int P, int chunks) { return ((P + 63) / 64 + chunks - 1) / chunks * 64; }
+constexpr int kPrefixRows = 128;  // query rows of a tile over the prefix
+__host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRows * (D + 2); }
+
+// Grid: kv heads x 32-row groups of their B * GT rows x slabs of dims. A lane has a row, a warp eight dims and every
+// SPLIT-th of the row's parts (its runs', then the prefix's); the warps of a row's dims meet in shared memory. What bounds it
+// is the chain of loads (the plan, a part's m and l and sums, one batch after another), so a batch is asked for at once,
+// and where rows are few their parts are spread over SPLIT warps.
+constexpr int kJoinThreads = 256;
+template <int D, bool PREFIX, int SPLIT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
+  constexpr int COLS = kJoinThreads / 32 / SPLIT;  // warps side by side, eight dims each
+  constexpr int SLABS = D / 8 / COLS, kBatch = 4;  // kBatch parts' loads in flight at once
+  const int rows = a.B * a.GT, groups = (rows + 31) / 32;
+  const int slab = blockIdx.x % SLABS, group = blockIdx.x / SLABS % groups, kvh = blockIdx.x / SLABS / groups;
+  const int warp = threadIdx.x / 32, part0 = warp / COLS, d8 = slab * COLS + warp % COLS;
+  const int row = min(group * 32 + (int)(threadIdx.x & 31), rows - 1);  // (the last group's lanes repeat a row)
+  const int b = row / a.GT, gt = row % a.GT, rb = gt / a.R, r = gt % a.R;
+  griddep_wait();
+  griddep_launch_dependents();
+  // the runs that hold steps of this row's group, and the chunks of the prefix
+  const int U = a.Hkv * a.RB, first = __ldcg(a.plan + b), next = __ldcg(a.plan + b + 1), S = __ldcg(a.plan + a.B + 1);
+  const int P = PREFIX ? prefix_keys(__ldcg(a.prefix_len), a.Pmax) : 0;
+  const int units = (next - first) / U, base = first + (kvh * a.RB + rb) * units;
+  const int r0 = (base + kRunGroupUnits) / S, n_runs = units > 0 ? (base + units - 1) / S + 1 - r0 : 0;
+  const int C = PREFIX ? prefix_chunk(P, a.chunks) : 0, n = n_runs + (P > 0 ? (P + C - 1) / C : 0);
+  const int BF = run_block_floats(a.R, D);
+  const float *runs = a.runs + run_block(((long long)b * a.Hkv + kvh) * a.RB + rb, r0) * BF;
+  const float *chunks = a.prefix + ((long long)kvh * a.tiles + row / kPrefixRows) * a.chunks * prefix_block_floats(D);
+  float M = -INFINITY, L = 0.f, A[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) A[k] = 0.f;
+  for (int p0 = part0; p0 < n; p0 += SPLIT * kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 x[kBatch], y[kBatch];
+    float Mn = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int p = p0 + i * SPLIT;
+      const bool own = !PREFIX || p < n_runs;
+      const float *pb = own ? runs + (long long)p * BF : chunks + (long long)(p - n_runs) * prefix_block_floats(D);
+      const int R = own ? a.R : kPrefixRows, at = own ? r : row % kPrefixRows;
+      m[i] = -INFINITY, l[i] = 0.f;
+      if (p < n) {
+        m[i] = __ldcg(pb + R * D + at);
+        l[i] = __ldcg(pb + R * (D + 1) + at);
+        x[i] = __ldcg(reinterpret_cast<const float4 *>(pb) + 2 * d8 * R + at);
+        y[i] = __ldcg(reinterpret_cast<const float4 *>(pb) + (2 * d8 + 1) * R + at);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (l[i] > 0.f) Mn = fmaxf(Mn, m[i]);  // a part without keys (l = 0) counts nothing
+    const float ref = Mn == -INFINITY ? 0.f : Mn;
+    const float alpha = exp2f(M - ref);
+    L *= alpha;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) A[k] *= alpha;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (l[i] > 0.f) {
+        const float f = exp2f(m[i] - ref);
+        L = fmaf(l[i], f, L);
+        A[0] = fmaf(x[i].x, f, A[0]), A[1] = fmaf(x[i].y, f, A[1]), A[2] = fmaf(x[i].z, f, A[2]), A[3] = fmaf(x[i].w, f, A[3]);
+        A[4] = fmaf(y[i].x, f, A[4]), A[5] = fmaf(y[i].y, f, A[5]), A[6] = fmaf(y[i].z, f, A[6]), A[7] = fmaf(y[i].w, f, A[7]);
+      }
+    }
+    M = Mn;
+  }
+  if constexpr (SPLIT > 1) {
+    __shared__ float s_acc[8][kJoinThreads];
+    __shared__ float2 s_ml[kJoinThreads];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s_acc[k][threadIdx.x] = A[k];
+    s_ml[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (part0 != 0) return;
+    float2 ml[SPLIT];
+    M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int j = 0; j < SPLIT; ++j) {
+      ml[j] = s_ml[threadIdx.x + 32 * COLS * j];
+      if (ml[j].y > 0.f) M = fmaxf(M, ml[j].x);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) A[k] = 0.f;
+#pragma unroll
+    for (int j = 0; j < SPLIT; ++j) {
+      if (ml[j].y > 0.f) {
+        const float f = exp2f(ml[j].x - M);
+        L = fmaf(ml[j].y, f, L);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) A[k] = fmaf(s_acc[k][threadIdx.x + 32 * COLS * j], f, A[k]);
+      }
+    }
+  }
+  if (group * 32 + (int)(threadIdx.x & 31) >= rows) return;
+  const long long at = (long long)b * a.Hq * a.T + (long long)kvh * a.GT + gt;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + d8 * 8) =
+      make_uint4(pack_bf16x2(A[0] * inv, A[1] * inv), pack_bf16x2(A[2] * inv, A[3] * inv),
+                 pack_bf16x2(A[4] * inv, A[5] * inv), pack_bf16x2(A[6] * inv, A[7] * inv));
+  if (a.lse != nullptr && d8 == 0) a.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+}  // namespace td

@@ -179,9 +179,7 @@ __device__ __forceinline__ int first_chunk_size(const SplitParams &p, long long 
 // Exclusive prefix over the per-sequence item counts, computed by the whole CTA.
 // s_len[b] receives the clamped length; returns the chunk size through *s_chunk and the
 // item total in s_prefix[B]. s_red holds 2 * kWarps values.
-// AHEAD: the whole kernel runs ahead of the wait for the previous one (the PART kernels), so the lengths are read as
-// they are before that wait.
-template <int WIN = 0, bool AHEAD = false>
+template <int WIN = 0>
 static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefix, int *s_chunk, long long *s_red,
                                   bool report_bits = true) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -197,7 +195,7 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
     if (b < p.B) {
       // before the wait for the previous kernel the lengths may be written meanwhile: read
       // them where that kernel's writes land, not through L1
-      const int L = attended_len(p, report_bits && !AHEAD ? p.seq_lens[b] : ld_relaxed(p.seq_lens + b), bits);
+      const int L = attended_len(p, report_bits ? p.seq_lens[b] : ld_relaxed(p.seq_lens + b), bits);
       s_len[b] = L;
       tot += keys_of<WIN>(p, L);
       lmax = max(lmax, keys_of<WIN>(p, L));

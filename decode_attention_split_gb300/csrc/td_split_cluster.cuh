@@ -19,8 +19,7 @@
 namespace td {
 
 // TILE: the warps' step for the group's rows (tile_of_rows). WIN: kWindowPad for windowed attention, else 0.
-// PART: as in split_attn_mma_kernel.
-template <int D, int TILE = kTileM16, int WIN = 0, bool PART = false>
+template <int D, int TILE = kTileM16, int WIN = 0>
 __global__ void __launch_bounds__(kThreads, 1)
     split_attn_cluster_kernel(const __grid_constant__ typename MmaArgsOf<WIN>::type a) {
   constexpr int NST = kClusterStages<D>;
@@ -64,10 +63,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       prefetch_chunk_l2<D>(p, b, kvh, g0, min(g0 + Sg, keys), prefetch_stages(p));
   }
-  if constexpr (!PART) griddep_wait();  // seq_lens and the cache may come from the previous kernel in the stream
+  griddep_wait();  // seq_lens and the cache may come from the previous kernel in the stream
   griddep_launch_dependents();
   uint32_t bits = 0;
-  const int L = attended_len(p, PART ? ld_relaxed(p.seq_lens + b) : p.seq_lens[b], bits);
+  const int L = attended_len(p, p.seq_lens[b], bits);
   if (tid == 0 && rank == 0 && kvh == 0 && rb == 0) report(p.status, bits);
   __syncthreads();  // barrier initialisation is visible before any wait
   advance_after_reads(p, &s_flag);  // fused step: the lengths move on once every CTA has read them
@@ -125,16 +124,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const long long orow = out_row_of(p, b, kvh, rb, r);
-      if constexpr (PART)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + orow * D + d) = A;
-      else
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + d) =
-            make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + orow * D + d) =
+          make_uint2(pack_bf16x2(A.x, A.y), pack_bf16x2(A.z, A.w));
       if (d == 0 && p.lse != nullptr) p.lse[orow] = s_lse[r];
     }
   }
   cluster_sync_all();  // no CTA leaves while CTA 0 may still read its shared memory
-  if (PART && blockIdx.x == 0) griddep_wait();
 }
 
 template <int D>

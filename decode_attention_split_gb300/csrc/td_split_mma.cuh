@@ -15,7 +15,7 @@
 // heads) takes the narrow tile instead: keys on the M side and the rows on the 8-wide N side
 // (S^T = K Q^T, O^T += V^T P^T; warp_keys16_n8), half the tensor-core tiles per step; a row
 // block of 17 to 24 rows (a speculative-verify chunk of a grouped kv head: 4 heads x 6
-// tokens) takes the same layout with three 8-wide N tiles (warp_keys16_n24), so each K/V tile
+// tokens) takes the same layout with three 8-wide N tiles (warp_keys16_nt), so each K/V tile
 // in shared memory serves all 24 rows once.
 //
 // K/V stages of 64 rows are fetched by the TMA engine (cp.async.bulk.tensor: one thread
@@ -31,8 +31,6 @@
 #pragma once
 
 #include <cudaTypedefs.h>
-
-#include <type_traits>
 
 #include "td_mma.cuh"
 #include "td_rope.cuh"
@@ -52,7 +50,7 @@ bool encode_cache_map(CUtensorMap *map, const void *base, int B, int Hkv, int Sm
 //   kTileN8   at most 8 rows: keys on the m side, the rows on one 8-wide n tile (warp_keys16_n8);
 //   kTileM16  9 to 16 rows: the rows on the m side of one 16-row tile, keys on n (warp_keys16);
 //   kTileN24  17 to 24 rows: keys on the m side, the rows on three 8-wide n tiles
-//             (warp_keys16_n24).
+//             (warp_keys16_nt).
 enum : int { kTileM16 = 0, kTileN8 = 1, kTileN24 = 2 };
 constexpr int kMaxTileRows = 24;
 // Rows of a tile's combine area and partial blocks.
@@ -295,11 +293,11 @@ __device__ __forceinline__ void warp_keys16(const uint32_t (&qa)[D / 16][4], uin
 // run over the 8 lanes of one tig. Half the tensor-core tiles, exponentials and output
 // registers of warp_keys16 when a kv head has 8 query rows or fewer (decode with grouped
 // heads). o[dt] holds O^T of dims 16*dt + gid (+8) and rows 2*tig (+1).
-template <int D, int WIN = 0>
+template <int D, int WIN = 0, int TK = 64>
 __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], uint32_t kt, uint32_t vt, int kr,
                                                int key0, const int (&lim)[2], float qscale, float (&o)[D / 16][4],
                                                float (&m_run)[2], float (&l_run)[2], int window = 0, int sinks = 0) {
-  constexpr int TK = 64, KSD = D / 16;
+  constexpr int KSD = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
   // two accumulators (even and odd k steps) halve the dependent chain of tensor-core tiles
   float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -357,34 +355,36 @@ __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], 
   }
 }
 
-// The narrow step for 17 to 24 query rows: warp_keys16_n8's layout with three 8-wide n tiles
+// The narrow step for up to 8 NT query rows: warp_keys16_n8's layout with NT 8-wide n tiles
 // (rows 8 nt .. 8 nt + 7 on tile nt), so one K and one V fragment load per 16 keys serve all
-// 24 rows. A thread holds keys gid and gid + 8 of rows 8 nt + 2 tig (+1) of each tile, i.e. six
-// rows, reduced over the 8 lanes that share a tig. o[nt][dt] holds O^T of dims 16 dt + gid (+8)
-// and rows 8 nt + 2 tig (+1); the row limits, maxima and sums are indexed 2 nt + e.
-template <int D, int WIN = 0>
-__device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][2], uint32_t kt, uint32_t vt, int kr,
-                                                int key0, const int (&lim)[6], float qscale, float (&o)[3][D / 16][4],
-                                                float (&m_run)[6], float (&l_run)[6], int window = 0, int sinks = 0) {
-  constexpr int TK = 64, KSD = D / 16;
+// of them (three tiles: the 17 to 24 rows of kTileN24). A thread holds keys gid and gid + 8 of
+// rows 8 nt + 2 tig (+1) of each tile, i.e. 2 NT rows, reduced over the 8 lanes that share a tig.
+// o[nt][dt] holds O^T of dims 16 dt + gid (+8) and rows 8 nt + 2 tig (+1); the row limits, maxima
+// and sums are indexed 2 nt + e. TK: rows of the tiles at kt and vt.
+template <int D, int WIN = 0, int NT = 3, int TK = 64>
+__device__ __forceinline__ void warp_keys16_nt(const uint32_t (&qb)[NT][D / 16][2], uint32_t kt, uint32_t vt, int kr,
+                                               int key0, const int (&lim)[2 * NT], float qscale,
+                                               float (&o)[NT][D / 16][4], float (&m_run)[2 * NT], float (&l_run)[2 * NT],
+                                               int window = 0, int sinks = 0) {
+  constexpr int KSD = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
-  // three independent accumulators, one per n tile
-  float sc[3][4];
+  // independent accumulators, one per n tile
+  float sc[NT][4];
 #pragma unroll
-  for (int nt = 0; nt < 3; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+  for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
   const int krow = kr + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
   for (int j = 0; j < KSD; ++j) {
     uint32_t ak[4];
     ldmatrix_x4(ak, kt + tma_swz<TK>(krow, 2 * j + (lane >> 4)));
 #pragma unroll
-    for (int nt = 0; nt < 3; ++nt) mma_bf16_16816(sc[nt], ak, qb[nt][j][0], qb[nt][j][1]);
+    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(sc[nt], ak, qb[nt][j][0], qb[nt][j][1]);
   }
   // scale to base-2 units and mask; element i of tile nt is key gid + 8 (i >> 1) of row
   // 8 nt + 2 tig + (i & 1)
-  float alpha[6];
+  float alpha[2 * NT];
 #pragma unroll
-  for (int nt = 0; nt < 3; ++nt) {
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int ri = 2 * nt + e;
@@ -410,10 +410,10 @@ __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][
   }
   bool rescale = false;
 #pragma unroll
-  for (int ri = 0; ri < 6; ++ri) rescale |= alpha[ri] != 1.f;
+  for (int ri = 0; ri < 2 * NT; ++ri) rescale |= alpha[ri] != 1.f;
   if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-    for (int nt = 0; nt < 3; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int dt = 0; dt < KSD; ++dt) {
         o[nt][dt][0] *= alpha[2 * nt];
@@ -423,9 +423,9 @@ __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][
       }
   }
   // P^T of each n tile as B operands: keys 2 tig (+1) (+8) of row 8 nt + gid
-  uint32_t pb[3][2];
+  uint32_t pb[NT][2];
 #pragma unroll
-  for (int nt = 0; nt < 3; ++nt) {
+  for (int nt = 0; nt < NT; ++nt) {
     pb[nt][0] = movmatrix_trans(pack_bf16x2(sc[nt][0], sc[nt][1]));
     pb[nt][1] = movmatrix_trans(pack_bf16x2(sc[nt][2], sc[nt][3]));
   }
@@ -435,7 +435,7 @@ __device__ __forceinline__ void warp_keys16_n24(const uint32_t (&qb)[3][D / 16][
     uint32_t av[4];
     ldmatrix_x4_trans(av, vt + tma_swz<TK>(vrow, 2 * dt + ((lane >> 3) & 1)));
 #pragma unroll
-    for (int nt = 0; nt < 3; ++nt) mma_bf16_16816(o[nt][dt], av, pb[nt][0], pb[nt][1]);
+    for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(o[nt][dt], av, pb[nt][0], pb[nt][1]);
   }
 }
 
@@ -631,7 +631,7 @@ __device__ bool stream_chunk(const typename MmaArgsOf<WIN>::type &a, unsigned ch
     const int key0 = j0 + kr;
     if (key0 < c1) {
       if constexpr (TILE == kTileN24)
-        warp_keys16_n24<D, WIN>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
+        warp_keys16_nt<D, WIN>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
       else if constexpr (TILE == kTileN8)
         warp_keys16_n8<D, WIN>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
       else
@@ -801,18 +801,14 @@ __device__ __forceinline__ unsigned char *align1024(unsigned char *p) {
 // they read the same then (measured on the 3B-style layer: 4k 11.4 -> 10.5 us, 32k 25.7 ->
 // 25.5 us). The other instantiation plans after the wait. TILE: the warps' step for the row
 // block's rows (tile_of_rows).
-// WIN: kWindowPad for windowed attention, else 0. PART: a part of an attention (a sequence's own keys behind a shared
-// prefix) whose out goes on in fp32. The kernel before it in the stream is then the other part, which this one neither
-// reads nor writes, and which waited for everything earlier before it let this one start: it runs alongside, reads
-// what others wrote past L1 alone, and its first CTA waits for the other part at the end, so that this grid's end is both's.
-template <int D, bool EARLY_PLAN, int TILE = kTileM16, int WIN = 0, bool PART = false>
+// WIN: kWindowPad for windowed attention, else 0.
+template <int D, bool EARLY_PLAN, int TILE = kTileM16, int WIN = 0>
 __global__ void __launch_bounds__(kThreads, 2)
     split_attn_mma_kernel(const __grid_constant__ typename MmaArgsOf<WIN>::type a) {
   constexpr int NST = kPersistentStages<D>;
   using C = MmaCfg<D, NST>;
-  using E = std::conditional_t<PART, float, __nv_bfloat16>;  // of the output
+  using E = __nv_bfloat16;
   constexpr int TR = tile_rows<TILE>();
-  static_assert(!(PART && (EARLY_PLAN || WIN != 0)), "parts have neither");
   static_assert((merge_fixed_floats<D, TR>() + part_block_floats(TR, D)) * 4 <= C::RING_BYTES,
                 "merge stages at least one chunk");
   const SplitParams &p = a.p;
@@ -837,12 +833,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t seq = 0;
   if (tid == 0) prefetch_first_item<D, kWarmRows, WIN>(p, prefetch_stages(p), blockIdx.x);
   if constexpr (EARLY_PLAN) plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red, false);
-  if constexpr (!PART) griddep_wait();  // inputs may come from the previous kernel in the stream
+  griddep_wait();  // inputs may come from the previous kernel in the stream
   griddep_launch_dependents();
   if constexpr (EARLY_PLAN)
     confirm_plan<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   else
-    plan_items<WIN, PART>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
+    plan_items<WIN>(p, s_len, s_prefix, &s_chunk, s_red);  // ends with __syncthreads
   advance_after_reads(p, &s_last);  // fused step: the lengths move on once every CTA has read them
   const int S = s_chunk;
   const int W = s_prefix[p.B];
@@ -882,7 +878,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     if (!ok) break;  // a copy never completed: stop taking items
   }
-  if (PART && blockIdx.x == 0) griddep_wait();
 }
 
 // Combines the kWarps partial sources left by stream_chunk (base-2 units, TR rows per warp)
