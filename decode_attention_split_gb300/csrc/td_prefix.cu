@@ -25,38 +25,47 @@ namespace td {
 
 namespace {
 
-constexpr int kPxSoftmaxWarps = 4;             // warps 0 .. 3: one query row per thread
-constexpr int kPxRunWarp = 4;                  // 4 .. 7: runs over the own keys
-constexpr int kPxMmaWarp = 8;                  // issues the tensor-core products
-constexpr int kPxLoadWarp = 9;                 // issues the TMA copies
-constexpr int kPxThreads = 384;                // three warpgroups (the last two warps have no work)
+constexpr int kPxSoftmaxWarps = 8;             // warps 0 .. 7: warps w and w + 4 share the rows of TMEM lanes 32 w ..
+constexpr int kPxRunWarp = 8;                  // 8 .. 11: runs over the own keys
+constexpr int kPxMmaWarp = 12;                 // issues the tensor-core products
+constexpr int kPxLoadWarp = 13;                // issues the TMA copies
+constexpr int kPxThreads = 512;                // four warpgroups (the last two warps have no work)
 constexpr int kPxRows = kPrefixRows;           // query rows per tile
-constexpr int kPxKRegion = kPfKeys * 128;      // bytes of one swizzled [64 keys][64 bf16] region
-// Registers a thread is launched with (65536 / 384, in steps of 8), and after the split where a run needs more: the product
-// and copy warps give up what the run warps take. 128 x (168 + 232 + 40) of the launch's 384 x 168.
-constexpr int kPxRunRegs = 232, kPxIssueRegs = 40;
-static_assert(128 * (168 + kPxRunRegs + kPxIssueRegs) <= 384 * 168, "register split within the launch's");
+constexpr int kPxKeys = kPrefixKeys;           // keys per tile
+constexpr int kPxHalf = kPxKeys / 2;           // of them, one softmax thread's
+constexpr int kPxKRegion = kPxKeys * 128;      // bytes of one swizzled [128 keys][64 bf16] region
+// Base-2 rise of a row's maximum before the reference moves. Probabilities and sums are floating point, so a reference 2^32
+// below the maximum costs no bits (fp32 holds 2^32 times a value of up to 2^75 over 2^20 keys), while every move makes a
+// warp wait for the product before it and rescale its rows of O: with a rise of 8 and now and then a key of four times the
+// others' strength, some row of the 128 moved in nearly every tile (490 cycles of a tile's 3600, 175 with 32).
+constexpr float kPxGap = 32.f;
+// Registers a thread: launched with 128 (65536 / 512), then split between softmax, run, and product and copy warps. A run
+// over row blocks of more than 8 rows needs more than 200, and the softmax warps then keep to what they have.
+__host__ __device__ constexpr int px_soft_regs(int NT) { return NT == 1 ? 136 : 128; }
+__host__ __device__ constexpr int px_run_regs(int NT) { return NT == 1 ? 200 : 216; }
+constexpr int kPxIssueRegs = 40;
+static_assert(256 * px_soft_regs(1) + 128 * px_run_regs(1) + 128 * kPxIssueRegs <= 512 * 128 &&
+                  256 * px_soft_regs(3) + 128 * px_run_regs(3) + 128 * kPxIssueRegs <= 512 * 128,
+              "register split within the launch's");
 
-#ifndef TD_PX_ST
-#define TD_PX_ST 3
-#endif
 template <int D>
 struct PxCfg {
-  static constexpr int NST = D == 128 ? TD_PX_ST : 2 * TD_PX_ST;  // buffers of K, and of V
+  static constexpr int NST = D == 128 ? 2 : 4;  // buffers of K, and of V
   static constexpr int HALVES = D / 64;
   static constexpr int KV_TILE = HALVES * kPxKRegion;
   static constexpr int V_OFF = NST * KV_TILE;         // the K buffers come first
   static constexpr int RUN_OFF = V_OFF + NST * KV_TILE;  // then the rings of the run warps
-  static constexpr int LEN_OFF = RUN_OFF + kRunWarps * RunCfg<D>::RING;  // then two ints a sequence and one
+  using Run = RunCfg<D, 2>;
+  static constexpr int LEN_OFF = RUN_OFF + kRunWarps * Run::RING;  // then two ints a sequence and one
   static constexpr int SMEM = LEN_OFF + 1024;         // + alignment slack
-  static constexpr int Q_COL = 128 + D;               // columns: S (64), two P buffers (32 each), O (D), Q (D / 2)
-  static constexpr int TMEM_COLS = D == 64 ? 256 : 512;
+  static constexpr int O_COL = 256, Q_COL = O_COL + D;  // columns: S (128), two P buffers (64 each), O (D), Q (D / 2)
+  static constexpr int TMEM_COLS = 512;
   static_assert(SMEM + (2 * TD_MAX_BATCH + 1) * 4 + 1024 <= 227 * 1024, "shared memory");
 };
 
 struct PxArgs {
   RunArgs own;       // the sequences' own keys; its p holds the queries too
-  CUtensorMap kmap;  // prefix [Hkv][Pmax][D], boxes of 64 rows
+  CUtensorMap kmap;  // prefix [Hkv][Pmax][D], boxes of 128 rows
   CUtensorMap vmap;
   const int32_t *prefix_len;
   float *part;       // [Hkv][tiles][chunks] blocks of prefix_block_floats(D) (td_runs.cuh)
@@ -65,7 +74,7 @@ struct PxArgs {
   int chunks;        // chunks the prefix is cut into, at most
 };
 
-// A tile's work: a kv head's rows [tile * 128, + rows) over keys [c0, c0 + 64 nkt), the last tile cut at c1.
+// A tile's work: a kv head's rows [tile * 128, + rows) over keys [c0, c0 + 128 nkt), the last tile cut at c1.
 struct PxItem {
   int tile, kvh, chunk, rows, c0, c1, nkt;
 };
@@ -78,7 +87,7 @@ __device__ __forceinline__ PxItem px_item(const PxArgs &a, int item, int P) {
   const int S = prefix_chunk(P, a.chunks);
   w.c0 = min(w.chunk * S, P);
   w.c1 = min(w.c0 + S, P);
-  w.nkt = (w.c1 - w.c0 + kPfKeys - 1) / kPfKeys;
+  w.nkt = (w.c1 - w.c0 + kPxKeys - 1) / kPxKeys;
   return w;
 }
 
@@ -90,10 +99,11 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
   const SplitParams &p = a.own.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_q, bar_k[C::NST], bar_v[C::NST], bar_s[2], bar_sfree, bar_p[2], bar_kfree[C::NST],
-      bar_vfree[C::NST], bar_pfree[2], bar_fin, run_bars[kRunWarps][RunCfg<D>::STAGES];
+      bar_vfree[C::NST], bar_pfree[2], bar_fin, run_bars[kRunWarps][C::Run::STAGES];
   __shared__ uint32_t s_taddr;
   __shared__ int s_issued[2], s_seen[2];  // wind-down: K / V tiles issued, and seen landed
   __shared__ int s_red[kRunWarps];
+  __shared__ float s_max[2][2][kPxRows];  // by tile's parity and half: a row's maximum over the half's keys, then its sum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char *smem = align1024(smem_raw);
   const uint32_t sb = smem_u32(smem);
@@ -119,7 +129,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     mbar_init(smem_u32(&bar_fin), 1);
     fence_mbar_init();
   }
-  if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps && lane == 0) init_ring<D>(run_bars[warp - kPxRunWarp]);
+  if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps && lane == 0) init_ring<C::Run::STAGES>(run_bars[warp - kPxRunWarp]);
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
                  "n"(C::TMEM_COLS)
@@ -130,28 +140,28 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_taddr;
-  const uint32_t tS = tmem, tP = tmem + kPfKeys, tO = tmem + 128, tQ = tmem + C::Q_COL;
+  const uint32_t tS = tmem, tP = tmem + kPxKeys, tO = tmem + C::O_COL, tQ = tmem + C::Q_COL;
 
   griddep_wait();
   griddep_launch_dependents();
   bool ok = true;
 
   if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps) {
-    if constexpr (NT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxRunRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(px_run_regs(NT)));
     int *s_len = reinterpret_cast<int *>(smem + C::LEN_OFF);  // [B]
     int *s_prefix = s_len + p.B;                              // [B + 1]
     const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp;
     const int S = plan_runs<0, true, 1>(p, rt, s_len, s_prefix, s_red);
     leave_plan(a.own.plan, p.B, s_prefix, S, rt);
-    run_warp<D, NT, 0>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
-                       smem + C::RUN_OFF + rw * RunCfg<D>::RING, run_bars[rw]);
+    run_warp<D, NT, 0, 2>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
+                       smem + C::RUN_OFF + rw * C::Run::RING, run_bars[rw]);
   } else if (warp >= kPxMmaWarp) {
-    if constexpr (NT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxIssueRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxIssueRegs));
     const int P = prefix_keys(*a.prefix_len, a.Pmax);
     const int items = P > 0 ? a.tiles * p.Hkv * a.chunks : 0;
     if (warp == kPxMmaWarp) {
       if (lane == 0) {
-        constexpr uint32_t kIdS = mma_idesc(kPxRows, kPfKeys, false);
+        constexpr uint32_t kIdS = mma_idesc(kPxRows, kPxKeys, false);
         constexpr uint32_t kIdO = mma_idesc(kPxRows, D, true);
         const uint64_t dk = smem_desc(sb, 16, 1024);
         const uint64_t dv = smem_desc(sb + C::V_OFF, kPxKRegion, 1024);
@@ -189,8 +199,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             tc_fence_after();
             const uint32_t vb = (uint32_t)buf * C::KV_TILE;
 #pragma unroll
-            for (int k = 0; k < kPfKeys / 16; ++k)
-              tc_mma_ts(tO, tP + b0 * (kPfKeys / 2) + 8 * k, dv + ((vb + (uint32_t)k * 16 * 128) >> 4), kIdO,
+            for (int k = 0; k < kPxKeys / 16; ++k)
+              tc_mma_ts(tO, tP + b0 * (kPxKeys / 2) + 8 * k, dv + ((vb + (uint32_t)k * 16 * 128) >> 4), kIdO,
                         kt > 0 || k > 0);
             tc_commit(smem_u32(&bar_pfree[b0]));
             tc_commit(smem_u32(&bar_vfree[buf]));
@@ -202,6 +212,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
       __syncwarp();
     } else if (warp == kPxLoadWarp) {
       if (lane == 0) {
+        const uint64_t policy = l2_evict_first_policy();
         int g = 0;
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
           const PxItem w = px_item(a, item, P);
@@ -219,7 +230,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
               mbar_arrive_expect_tx(bar, C::KV_TILE);
 #pragma unroll
               for (int h = 0; h < C::HALVES; ++h)
-                tma3(dst + h * kPxKRegion, v ? &a.vmap : &a.kmap, 64 * h, w.c0 + kt * kPfKeys, w.kvh, bar);
+                tma_load_3d(dst + h * kPxKRegion, v ? &a.vmap : &a.kmap, 64 * h, w.c0 + kt * kPxKeys, w.kvh, bar, policy);
               s_issued[v] = g + 1;
             }
             if (!ok) break;
@@ -229,144 +240,168 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
       __syncwarp();
     }
   } else {
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    if constexpr (px_soft_regs(NT) > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(px_soft_regs(NT)));
+    // thread `row` of half `half` (0: warps 0 .. 3) takes keys 64 half .. of the row's 128 a tile, and dims D / 2 half ..
+    // of its output; the two of a row meet in s_max
+    const int quarter = warp & 3, half = warp >> 2, row = tid & (kPxRows - 1);
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const float qscale = p.qscale;
+    const int nrows = p.B * a.GT;
+    auto meet = [&]() {  // the two warps of a quarter's rows
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+    };
+    // this thread's half of its query row, asked for ahead of the prefix's length (past the last item: a row in vain)
+    uint4 qv[D / 16];
+    auto fetch_q = [&](int item) {
+      const int at = item % a.tiles * kPxRows + row, kvh = item / a.tiles % p.Hkv;
+      const bool real = at < nrows;
+      const uint4 *qrow = static_cast<const uint4 *>(p.q) + half * (D / 16) +
+                          (real ? (long long)(at / a.GT) * p.Hq * p.T + (long long)kvh * a.GT + at % a.GT : 0) * (D / 8);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) qv[i] = real ? qrow[i] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    fetch_q(blockIdx.x);
     const int raw = *a.prefix_len;
     const int P = prefix_keys(raw, a.Pmax);
     if (tid == 0 && blockIdx.x == 0)
       report(p.status, (raw < 0 ? TD_DEV_NEGATIVE_SEQLEN : 0u) | (raw > a.Pmax ? TD_DEV_SEQLEN_CLAMPED : 0u));
     const int items = P > 0 ? a.tiles * p.Hkv * a.chunks : 0;
     int g = 0;
-    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < items; item += gridDim.x, fetch_q(item)) {
       const PxItem w = px_item(a, item, P);
       if (w.nkt == 0) break;
-      const int busy = (w.rows + 31) / 32;  // warps with rows
-      if (warp < busy) {
-        // this thread's query row into its TMEM lane, a column per pair of dims (rows that do not exist: zeros)
-        const int row = min(w.tile * kPxRows + tid, p.B * a.GT - 1);
-        const uint4 *qrow = static_cast<const uint4 *>(p.q) +
-                            ((long long)(row / a.GT) * p.Hq * p.T + (long long)w.kvh * a.GT + row % a.GT) * (D / 8);
+      const int busy = (w.rows + 31) / 32;  // quarters with rows
+      // the query row into its TMEM lane, a column per pair of dims (rows that do not exist: zeros)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t x[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 y = tid < w.rows ? qrow[8 * c + i] : make_uint4(0u, 0u, 0u, 0u);
-            x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
-          }
-          tmem_st32(tQ + lane_base + 32 * c, x);
-        }
+      for (int c = 0; c < D / 64; ++c) {
+        const uint32_t x[16] = {qv[4 * c].x,     qv[4 * c].y,     qv[4 * c].z,     qv[4 * c].w,
+                                qv[4 * c + 1].x, qv[4 * c + 1].y, qv[4 * c + 1].z, qv[4 * c + 1].w,
+                                qv[4 * c + 2].x, qv[4 * c + 2].y, qv[4 * c + 2].z, qv[4 * c + 2].w,
+                                qv[4 * c + 3].x, qv[4 * c + 3].y, qv[4 * c + 3].z, qv[4 * c + 3].w};
+        tmem_st16(tQ + lane_base + half * (D / 4) + 16 * c, x);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bar_q));
+      if (lane == 0 && ok) mbar_arrive(smem_u32(&bar_q));
       // a warp without rows only keeps the barriers' count: what its lanes of P and O hold reaches no other row
       const int g0 = g;
       g += w.nkt;
-      for (int k = g0; k < g && warp >= busy; ++k) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[k & 1]), (uint32_t)(k >> 1) & 1u))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
+      for (int k = g0; ok && k < g && quarter >= busy; ++k) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[k & 1]), (uint32_t)(k >> 1) & 1u));
+        if (ok && lane == 0) {
           mbar_arrive(smem_u32(&bar_sfree));
           mbar_arrive(smem_u32(&bar_p[k & 1]));
         }
       }
-      if (warp >= busy) continue;
-      float m_ref = -INFINITY, l = 0.f;  // this row's reference maximum and sum
+      if (quarter >= busy) continue;
+      // (a warp whose wait gave up takes part in nothing but the meetings from then on, which the other warp counts on)
+      const int keys = w.c1 - w.c0;
+      float m_ref = -INFINITY, l = 0.f;  // this row's reference maximum, and its sum over this thread's keys
       for (int k = g0; k < g; ++k) {
         const int b0 = k & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[b0]), (uint32_t)(k >> 1) & 1u))) {
-          ok = false;
-          break;
-        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[b0]), (uint32_t)(k >> 1) & 1u));
         tc_fence_after();
-        const int vis = min(kPfKeys, w.c1 - w.c0 - (k - g0) * kPfKeys);  // keys of the tile (fewer at the prefix's end alone)
-        if (vis < kPfKeys) {
+        // keys of the tile (fewer at the prefix's end alone), and of this half of it
+        const int left = keys - (k - g0) * kPxKeys, vis = min(kPxHalf, left - half * kPxHalf);
+        if (ok && left < kPxKeys) {
           // V rows behind the prefix, once landed: zeroed (a masked p of 0 must not meet a stale value)
           const int buf = k % C::NST;
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[buf]), (uint32_t)(k / C::NST) & 1u))) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_v[buf]), (uint32_t)(k / C::NST) & 1u));
           unsigned char *vt = smem + C::V_OFF + buf * C::KV_TILE;
-          for (int idx = tid; idx < (kPfKeys - vis) * (D / 8); idx += 32 * busy) {
-            const int r = vis + idx / (D / 8), c = idx % (D / 8);
-            *reinterpret_cast<uint4 *>(vt + tile_chunk(kPfKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int idx = 32 * (quarter + half * busy) + lane; ok && idx < (kPxKeys - left) * (D / 8); idx += 64 * busy) {
+            const int r = left + idx / (D / 8), c = idx % (D / 8);
+            *reinterpret_cast<uint4 *>(vt + tile_chunk(kPxKeys, r, c)) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();  // read next by the tensor core (asynchronous proxy)
         }
-        float sv[kPfKeys];
-        tmem_ld64(tS + lane_base, sv);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bar_sfree));
-        if (vis < kPfKeys) {
+        float sv[kPxHalf];
+        float mx = -INFINITY;
+        if (ok) {
+          tmem_ld64(tS + lane_base + half * kPxHalf, sv);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bar_sfree));
+          if (left < kPxKeys) {
 #pragma unroll
-          for (int i = 0; i < kPfKeys; ++i)
-            if (i >= vis) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
+            for (int i = 0; i < kPxHalf; ++i)
+              if (i >= vis) sv[i] = qscale >= 0.f ? -INFINITY : INFINITY;
+          }
+          if (vis > 0) mx = (qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv)) * qscale;
         }
-        // the reference maximum moves only when the row's rises more than kRescaleGap above it (a row's first scores
+        // the row's maximum over both halves
+        s_max[b0][half][row] = mx;
+        meet();
+        mx = fmaxf(mx, s_max[b0][half ^ 1][row]);
+        if (!ok) continue;
+        // the reference maximum moves only when the row's rises more than kPxGap above it (a row's first scores
         // always move it); only then are O and l rescaled, once the previous product is complete
-        const float mx = (qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv)) * qscale;
-        const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
+        const bool move = mx > m_ref + kPxGap || (m_ref == -INFINITY && mx > -INFINITY);
         const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
         if (move) {
           l *= alpha;
           m_ref = mx;
         }
         if (k > g0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0 ^ 1]), (uint32_t)((k - 1) >> 1) & 1u))) {
-            ok = false;
-            break;
-          }
+          // (the product of k - 2 may still run: S of k is issued before the product of k - 1. Each of the two barriers'
+          // phase before is known complete, so neither wait can pass a phase early)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0 ^ 1]), (uint32_t)((k - 1) >> 1) & 1u));
+          if (!ok) continue;
           tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 16) {  // (16 at a time: the scores are held meanwhile)
+            uint32_t o[16];
+            tmem_ld16(tO + lane_base + half * (D / 2) + c, o);
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(tO + lane_base + c, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(tO + lane_base + c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + lane_base + half * (D / 2) + c, o);
           }
         }
         const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
-        const SeenFirst seen{vis};
-        uint32_t pk[kPfKeys / 2];
-        if (vis == kPfKeys)
-          l += p_row<false>(sv, qscale, nbase, seen, pk);
-        else
-          l += p_row<true>(sv, qscale, nbase, seen, pk);
-        // into P buffer b0, once the product of tile k - 2 has read it
+        // P of this half into P buffer b0, once the product of tile k - 2 has read it
         if (k >= 2) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0]), (uint32_t)((k - 2) >> 1) & 1u))) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[b0]), (uint32_t)((k - 2) >> 1) & 1u));
+          if (!ok) continue;
           tc_fence_after();
         }
-        tmem_st32(tP + b0 * (kPfKeys / 2) + lane_base, pk);
+#pragma unroll
+        for (int c = 0; c < kPxHalf; c += 32) {
+          const SeenFirst seen{vis - c};
+          uint32_t pk[16];
+          const float(&part)[32] = reinterpret_cast<const float(&)[32]>(sv[c]);
+          if (left >= kPxKeys)
+            l += p_row<false>(part, qscale, nbase, seen, pk);
+          else
+            l += p_row<true>(part, qscale, nbase, seen, pk);
+          tmem_st16(tP + b0 * (kPxKeys / 2) + half * (kPxHalf / 2) + c / 2 + lane_base, pk);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_p[b0]));
       }
+      s_max[g & 1][half][row] = l;
+      meet();
+      l += s_max[g & 1][half ^ 1][row];
       // the partial block, once the last product is complete: 512 consecutive bytes a warp and store
-      if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_pfree[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u))) ok = false;
-      if (!ok) break;
+      ok = ok && __all_sync(0xffffffffu,
+                            mbar_wait_bounded(smem_u32(&bar_pfree[(g - 1) & 1]), (uint32_t)((g - 1) >> 1) & 1u));
+      if (!ok) continue;
       tc_fence_after();
-      float *blk = a.part + (((long long)w.kvh * a.tiles + w.tile) * a.chunks + w.chunk) * prefix_block_floats(D);
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      const PxItem here = px_item(a, item, P);  // (again: its numbers are not held over the tiles)
+      float *blk = a.part + (((long long)here.kvh * a.tiles + here.tile) * a.chunks + here.chunk) * prefix_block_floats(D);
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32) {
         float o[32];
-        tmem_ld32(tO + lane_base + c, o);
+        const int d0 = half * (D / 2) + c;
+        tmem_ld32_waited(tO + lane_base + d0, o);
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4 *>(blk + ((c + i) / 4 * kPxRows + tid) * 4) =
+          *reinterpret_cast<float4 *>(blk + ((d0 + i) / 4 * kPxRows + row) * 4) =
               make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
-      blk[kPxRows * D + tid] = m_ref;
-      blk[kPxRows * (D + 1) + tid] = l;
+      if (half == 0) {
+        blk[kPxRows * D + row] = m_ref;
+        blk[kPxRows * (D + 1) + row] = l;
+      }
     }
   }
   ok = __syncthreads_and(ok) != 0;
@@ -409,8 +444,8 @@ template <int D>
 cudaError_t launch_d(const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &p, unsigned char *ws, float *part,
                      cudaStream_t stream) {
   PxArgs a;
-  if (!fill_runs(&a.own, D, plan.own, p, ws) || !encode_cache_map(&a.kmap, x.k, 1, p.Hkv, x.Pmax, D) ||
-      !encode_cache_map(&a.vmap, x.v, 1, p.Hkv, x.Pmax, D))
+  if (!fill_runs(&a.own, D, plan.own, p, ws) || !encode_cache_map(&a.kmap, x.k, 1, p.Hkv, x.Pmax, D, kPxKeys) ||
+      !encode_cache_map(&a.vmap, x.v, 1, p.Hkv, x.Pmax, D, kPxKeys))
     return cudaErrorInvalidValue;
   a.prefix_len = x.prefix_len;
   a.part = part;
@@ -438,9 +473,9 @@ td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, 
   const long long tiles = (rows + kPxRows - 1) / kPxRows;
   const long long groups = tiles * Hkv;
   const int sms = device_sm_count(device);
-  // chunks that fill the GPU once, of at least two tiles of keys
+  // chunks that fill the GPU once
   long long chunks = sms / groups;
-  chunks = std::min(chunks, ((long long)Pmax + 2 * kPfKeys - 1) / (2 * kPfKeys));
+  chunks = std::min(chunks, ((long long)Pmax + kPxKeys - 1) / kPxKeys);
   if (chunks < 1) chunks = 1;
   if (groups * chunks * 16 > 0x7fffffffLL || rows > (1 << 26)) return TD_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;

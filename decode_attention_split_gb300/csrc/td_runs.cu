@@ -4,12 +4,6 @@
 
 #include "td_runs.cuh"
 
-#ifndef TD_JOIN_1
-#define TD_JOIN_1 300
-#endif
-#ifndef TD_JOIN_2
-#define TD_JOIN_2 76
-#endif
 namespace td {
 
 namespace {
@@ -28,12 +22,12 @@ cudaError_t launch_nt(const RunArgs &a, int grid, cudaStream_t stream) {
     if (!done[device]) {
       const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 RunCfg<D>::SMEM + (2 * TD_MAX_BATCH + 1) * (int)sizeof(int));
+                                                 RunCfg<D, kRunStages>::SMEM + (2 * TD_MAX_BATCH + 1) * (int)sizeof(int));
       if (e != cudaSuccess) return e;
       done[device] = true;
     }
   }
-  const size_t smem = RunCfg<D>::SMEM + (2 * (size_t)a.p.B + 1) * sizeof(int);
+  const size_t smem = RunCfg<D, kRunStages>::SMEM + (2 * (size_t)a.p.B + 1) * sizeof(int);
   return launch_pdl(kernel, dim3(grid), dim3(kRunThreads), smem, stream, a);
 }
 
@@ -51,18 +45,16 @@ cudaError_t launch_join_split(const JoinArgs &a, cudaStream_t stream) {
   return launch_pdl(join_kernel<D, PREFIX, SPLIT>, dim3((unsigned)(groups * (D / 64) * SPLIT)), dim3(kJoinThreads), 0, stream, a);
 }
 
-template <int D>
-cudaError_t launch_join_d(const JoinArgs &a, bool prefix, cudaStream_t stream) {
-  // CTAs without a split; few of them are split until there is one an SM
-  const long long ctas = ((long long)a.B * a.GT + 31) / 32 * a.Hkv * (D / 64);
-  const int split = ctas >= TD_JOIN_1 ? 1 : ctas >= TD_JOIN_2 ? 2 : 4;
-  if (prefix)
-    return split == 1   ? launch_join_split<D, true, 1>(a, stream)
-           : split == 2 ? launch_join_split<D, true, 2>(a, stream)
-                        : launch_join_split<D, true, 4>(a, stream);
-  return split == 1   ? launch_join_split<D, false, 1>(a, stream)
-         : split == 2 ? launch_join_split<D, false, 2>(a, stream)
-                      : launch_join_split<D, false, 4>(a, stream);
+template <int D, bool PREFIX>
+cudaError_t launch_join_d(const JoinArgs &a, cudaStream_t stream) {
+  // one batch of loads a thread for the prefix's chunks and a few runs, while the CTAs fit the GPU at once
+  const long long ctas = ((long long)a.B * a.GT + 31) / 32 * a.Hkv * (D / 64);  // without a split
+  int split = 1;
+  while (split < 8 && split * 4 < a.chunks + 3 && ctas * split * 2 <= 2 * 152) split *= 2;
+  return split == 1   ? launch_join_split<D, PREFIX, 1>(a, stream)
+         : split == 2 ? launch_join_split<D, PREFIX, 2>(a, stream)
+         : split == 4 ? launch_join_split<D, PREFIX, 4>(a, stream)
+                      : launch_join_split<D, PREFIX, 8>(a, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -80,7 +72,7 @@ td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, int per
   const long long groups = (long long)B * Hkv * RB;
   const long long most = groups * ((keys + kRunKeys - 1) / kRunKeys + kRunGroupUnits);
   if (most >= (1LL << 30)) return TD_ERR_UNSUPPORTED;
-  const long long ctas = (most / (kRunGroupUnits + 1) + kRunWarps) / kRunWarps;
+  const long long ctas = (most / kRunLeast + kRunWarps) / kRunWarps;
   plan->grid = (int)std::min((long long)per_sm * sms, ctas);
   plan->off_blocks = align256(((size_t)B + 2) * sizeof(int));
   plan->bytes = plan->off_blocks + align256((size_t)(groups + plan->grid * kRunWarps) * run_block_floats(plan->R, D) * sizeof(float));
@@ -111,7 +103,8 @@ cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const
   a.out = p.out, a.lse = p.lse;
   a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.T = p.T, a.GT = p.G * p.T, a.R = plan.R, a.RB = plan.RB;
   if (x != nullptr) a.prefix = x->part, a.prefix_len = x->prefix_len, a.Pmax = x->Pmax, a.tiles = x->tiles, a.chunks = x->chunks;
-  return D == 64 ? launch_join_d<64>(a, x != nullptr, stream) : launch_join_d<128>(a, x != nullptr, stream);
+  if (x != nullptr) return D == 64 ? launch_join_d<64, true>(a, stream) : launch_join_d<128, true>(a, stream);
+  return D == 64 ? launch_join_d<64, false>(a, stream) : launch_join_d<128, false>(a, stream);
 }
 
 }  // namespace td

@@ -15,23 +15,16 @@
 
 namespace td {
 
-#ifndef TD_RUN_ST
-#define TD_RUN_ST 3
-#endif
-#ifndef TD_RUN_GU
-#define TD_RUN_GU 1
-#endif
-#ifndef TD_RUN_MIN
-#define TD_RUN_MIN(R) 2
-#endif
 constexpr int kRunWarps = 4;
 constexpr int kRunThreads = 32 * kRunWarps;
 constexpr int kRunKeys = 16;  // keys of a step and stage
+constexpr int kRunStages = 3; // of a warp's ring in runs_kernel (two CTAs an SM)
 static_assert(kRunThreads == kThreads, "lengths_unchanged is written for CTAs of kThreads");
 
-template <int D>
+// ST: stages of a warp's ring at D = 128 (twice as many at 64).
+template <int D, int ST>
 struct RunCfg {
-  static constexpr int STAGES = D == 128 ? TD_RUN_ST : 2 * TD_RUN_ST;  // of a warp's ring
+  static constexpr int STAGES = D == 128 ? ST : 2 * ST;
   static constexpr int HALVES = D / 64;
   static constexpr int BOX = kRunKeys * 128;             // 16 rows x 128 bytes
   static constexpr int TILE = HALVES * BOX;              // K or V of a stage
@@ -52,7 +45,8 @@ bool fill_runs(RunArgs *a, int D, const RunsPlan &plan, const SplitParams &p, un
 __host__ __device__ constexpr int run_block_floats(int R, int D) { return (R * (D + 2) + 3) / 4 * 4; }
 
 // Units of a group of `keys` keys: its steps, and as many units as starting and finishing it costs, ahead of its own.
-constexpr int kRunGroupUnits = TD_RUN_GU;
+constexpr int kRunGroupUnits = 1;
+constexpr int kRunLeast = 2;  // units of the shortest run
 __device__ __forceinline__ int run_steps(int keys) { return (keys + kRunKeys - 1) / kRunKeys; }
 __device__ __forceinline__ int run_units(int keys) { return keys > 0 ? run_steps(keys) + kRunGroupUnits : 0; }
 // The block of group g's keys in run r: runs and groups advance together, so every (group, run) that meet have their own.
@@ -101,7 +95,7 @@ __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefi
   if (tid == 0) s_prefix[p.B] = W;
   run_barrier<BAR>();
   const int runs = gridDim.x * kRunWarps;
-  return max((W + runs - 1) / runs, TD_RUN_MIN(p.R));
+  return max((W + runs - 1) / runs, kRunLeast);
 }
 
 // Where a warp is in its run: group `ug` of sequence b, steps [s, e) of it left in this run.
@@ -126,10 +120,10 @@ __device__ __forceinline__ void next_group(const SplitParams &p, const int *s_le
 }
 
 // A warp's ring: its barriers, by one thread.
-template <int D>
+template <int STAGES>
 __device__ __forceinline__ void init_ring(uint64_t *bars) {
 #pragma unroll
-  for (int i = 0; i < RunCfg<D>::STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+  for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
   fence_mbar_init();
 }
 
@@ -142,11 +136,11 @@ __device__ __forceinline__ void leave_plan(int *plan, int B, const int *s_prefix
 
 // One warp's run: number `run`, S units long. The warp's ring (1024-byte aligned) and its barriers (initialised, one arrival).
 // WIN: kWindowPad for windowed attention, else 0.
-template <int D, int NT, int WIN>
+template <int D, int NT, int WIN, int ST>
 __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                          const int *s_len, const int *s_prefix, int S, int run, unsigned char *ring_p,
                                          uint64_t *bars) {
-  using C = RunCfg<D>;
+  using C = RunCfg<D, ST>;
   constexpr int KSD = D / 16, NL = 2 * NT;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const uint32_t ring = smem_u32(ring_p);
@@ -298,7 +292,7 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
 
 template <int D, int NT, int WIN>
 __global__ void __launch_bounds__(kRunThreads, 2) runs_kernel(const __grid_constant__ RunArgs a) {
-  using C = RunCfg<D>;
+  using C = RunCfg<D, kRunStages>;
   const SplitParams &p = a.p;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ int s_red[kRunWarps];
@@ -306,14 +300,14 @@ __global__ void __launch_bounds__(kRunThreads, 2) runs_kernel(const __grid_const
   int *s_len = reinterpret_cast<int *>(smem_raw + C::SMEM);  // [B]
   int *s_prefix = s_len + p.B;                               // [B + 1]
   const int tid = threadIdx.x, warp = tid >> 5;
-  if ((tid & 31) == 0) init_ring<D>(s_bars[warp]);
+  if ((tid & 31) == 0) init_ring<C::STAGES>(s_bars[warp]);
   // planned on the lengths as they read before the wait for the previous kernel, again if they read otherwise after it
   int S = plan_runs<WIN, false, 0>(p, tid, s_len, s_prefix, s_red);
   griddep_wait();
   griddep_launch_dependents();
   if (!lengths_unchanged(p, s_len)) S = plan_runs<WIN, true, 0>(p, tid, s_len, s_prefix, s_red);
   leave_plan(a.plan, p.B, s_prefix, S, tid);
-  run_warp<D, NT, WIN>(p, a.kmap, a.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + warp,
+  run_warp<D, NT, WIN, kRunStages>(p, a.kmap, a.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + warp,
                        align1024(smem_raw) + warp * C::RING, s_bars[warp]);
 }
 
@@ -329,9 +323,10 @@ struct JoinArgs {
   int B, Hq, Hkv, T, GT, R, RB, Pmax, tiles, chunks;
 };
 
-// Prefix length attended, and the keys of a chunk of it (whole tiles of 64).
+// Prefix length attended, and the keys of a chunk of it (whole tiles).
+constexpr int kPrefixKeys = 128;
 __device__ __forceinline__ int prefix_keys(int raw, int Pmax) { return raw < 0 ? 0 : raw > Pmax ? Pmax : raw; }
-__device__ __forceinline__ int prefix_chunk(int P, int chunks) { return ((P + 63) / 64 + chunks - 1) / chunks * 64; }
+__device__ __forceinline__ int prefix_chunk(int P, int chunks) { return ((P + kPrefixKeys - 1) / kPrefixKeys + chunks - 1) / chunks * kPrefixKeys; }
 constexpr int kPrefixRows = 128;  // query rows of a tile over the prefix
 __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRows * (D + 2); }
 
@@ -341,7 +336,7 @@ __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRow
 // and where rows are few their parts are spread over SPLIT warps.
 constexpr int kJoinThreads = 256;
 template <int D, bool PREFIX, int SPLIT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a) {
   constexpr int COLS = kJoinThreads / 32 / SPLIT;  // warps side by side, eight dims each
   constexpr int SLABS = D / 8 / COLS, kBatch = 4;  // kBatch parts' loads in flight at once
   const int rows = a.B * a.GT, groups = (rows + 31) / 32;

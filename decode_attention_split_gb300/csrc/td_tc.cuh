@@ -92,6 +92,44 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// The same with its wait in one statement, as tmem_ld64.
+__device__ __forceinline__ void tmem_ld32_waited(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane, waited for.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane, waited for.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&w)[32]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]), "r"(w[16]), "r"(w[17]), "r"(w[18]), "r"(w[19]), "r"(w[20]), "r"(w[21]), "r"(w[22]), "r"(w[23]), "r"(w[24]), "r"(w[25]), "r"(w[26]), "r"(w[27]), "r"(w[28]), "r"(w[29]), "r"(w[30]), "r"(w[31]) : "memory");
@@ -119,16 +157,16 @@ struct SeenBits {
 // The low n of 32 bits (n any integer).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
-// One row's probabilities 2^(s * qscale + nbase) for the 64 scores sv, packed in bf16 pairs
+// One row's probabilities 2^(s * qscale + nbase) for N scores sv of it, packed in bf16 pairs
 // into pk; MASK: keys that the row does not see get 0. Returns their fp32 sum (in packed pairs, two
 // partial sums, so the additions do not form one chain).
-template <bool MASK, typename Seen>
-__device__ __forceinline__ float p_row(const float (&sv)[kPfKeys], float qscale, float nbase, const Seen &seen,
-                                       uint32_t (&pk)[kPfKeys / 2]) {
+template <bool MASK, int N, typename Seen>
+__device__ __forceinline__ float p_row(const float (&sv)[N], float qscale, float nbase, const Seen &seen,
+                                       uint32_t (&pk)[N / 2]) {
   float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 sc2 = make_float2(qscale, qscale), nb2 = make_float2(nbase, nbase);
 #pragma unroll
-  for (int i = 0; i < kPfKeys; i += 2) {
+  for (int i = 0; i < N; i += 2) {
     const float2 x = ffma2(make_float2(sv[i], sv[i + 1]), sc2, nb2);
     float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
     if (MASK) {
@@ -142,18 +180,20 @@ __device__ __forceinline__ float p_row(const float (&sv)[kPfKeys], float qscale,
   return t.x + t.y;
 }
 
-// The largest (MIN: smallest) of a row's 64 scores.
-template <bool MIN>
-__device__ __forceinline__ float row_extreme(const float (&sv)[kPfKeys]) {
-  float e[8];
+// The largest (MIN: smallest) of N scores of a row (N 32 or 64), in chains of eight.
+template <bool MIN, int N>
+__device__ __forceinline__ float row_extreme(const float (&sv)[N]) {
+  float e[N / 8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < N / 8; ++j) {
     const float *v = sv + 8 * j;
     e[j] = MIN ? fmin3f(fmin3f(v[0], v[1], v[2]), fmin3f(v[3], v[4], v[5]), fminf(v[6], v[7]))
                : fmax3f(fmax3f(v[0], v[1], v[2]), fmax3f(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
   }
-  return MIN ? fmin3f(fmin3f(e[0], e[1], e[2]), fmin3f(e[3], e[4], e[5]), fminf(e[6], e[7]))
-             : fmax3f(fmax3f(e[0], e[1], e[2]), fmax3f(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
+  if constexpr (N == 32) return MIN ? fminf(fmin3f(e[0], e[1], e[2]), e[3]) : fmaxf(fmax3f(e[0], e[1], e[2]), e[3]);
+  else
+    return MIN ? fmin3f(fmin3f(e[0], e[1], e[2]), fmin3f(e[3], e[4], e[5]), fminf(e[6], e[7]))
+               : fmax3f(fmax3f(e[0], e[1], e[2]), fmax3f(e[3], e[4], e[5]), fmaxf(e[6], e[7]));
 }
 
 // Byte offset of 16-byte chunk c of row r in a tile of `rows` rows kept as 128-byte-swizzled

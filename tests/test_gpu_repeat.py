@@ -1,4 +1,4 @@
-"""The tensor-core prefill gives the same bits call after call while another stream keeps memory busy, so that
+"""The tensor-core prefill and the shared-prefix attention give the same bits call after call while another stream keeps memory busy, so that
 its copies land late and in ever different orders (a wait that lets a product's reader pass too early shows here)."""
 import pytest
 import torch
@@ -40,5 +40,32 @@ def test_prefill_repeats_itself(td, D, T, L, window):
         with torch.cuda.stream(side):
             b.copy_(a)
         got.append(call())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
+
+
+@pytest.mark.parametrize("D,G,T,B,P", [(128, 4, 6, 33, 2048), (64, 3, 6, 33, 1999), (128, 4, 1, 70, 2047), (64, 8, 1, 40, 300)])
+def test_prefix_attention_repeats_itself(td, D, G, T, B, P):
+    Hkv, S = 3, 300
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+
+    def rows(*s):
+        return torch.randn(*s, generator=g, device="cuda")
+    q = rows(B, Hkv * G, T, D).bfloat16()
+    ramp = torch.linspace(0.2, 6.0, P, device="cuda")[None, :, None]   # scores that rise by more than the lag the maximum is let
+    kp, vp = (rows(Hkv, P, D) * ramp).bfloat16(), rows(Hkv, P, D).bfloat16()
+    k, v = rows(B, Hkv, S, D).bfloat16(), rows(B, Hkv, S, D).bfloat16()
+    lens = torch.randint(T, S + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    plen = torch.tensor([P], dtype=torch.int32, device="cuda")
+    a = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    b = torch.empty_like(a)
+    want = td.td_verify_attn_prefix(q, kp, vp, plen, k, v, lens, return_lse=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(150):
+        with torch.cuda.stream(side):
+            b.copy_(a)
+        got.append(td.td_verify_attn_prefix(q, kp, vp, plen, k, v, lens, return_lse=True))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
