@@ -145,22 +145,21 @@ cudaError_t launch_prefill(const void *q, const void *k, const void *v, const in
                            int T, int Smax, int D, float scale, void *out, float *lse, uint32_t *status,
                            cudaStream_t stream, int window = 0, int sinks = 0);
 
-// Attention in runs (td_runs.cu): the runs' launch leaves partial blocks, the join's reads them.
+// Attention in runs (td_runs.cuh): the warps that take them leave partial blocks, the join's launch reads them.
 struct RunsPlan {
   int R, RB;      // rows of a row block, row blocks of a kv head
   int grid;
   size_t off_blocks, bytes;  // workspace: the plan's array, the blocks (nothing of it needs zeroing)
 };
-// keys: the most a sequence attends; per_sm: CTAs that take runs, at most, an SM.
-td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, int per_sm, RunsPlan *plan);
-cudaError_t launch_runs(int D, const RunsPlan &plan, const SplitParams &p, unsigned char *ws, cudaStream_t stream);
+// keys: the most a sequence attends.
+td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, RunsPlan *plan);
 // The parts over a shared prefix that the join adds (td_prefix.cu).
 struct PrefixPart {
   const float *part;
   const int32_t *prefix_len;
   int Pmax, tiles, chunks;
 };
-cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const unsigned char *ws, const PrefixPart *x,
+cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const unsigned char *ws, const PrefixPart &x,
                         cudaStream_t stream);
 
 // Attention over a shared prefix and each sequence's own keys (td_prefix.cu).

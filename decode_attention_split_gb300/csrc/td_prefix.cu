@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     int *s_len = reinterpret_cast<int *>(smem + C::LEN_OFF);  // [B]
     int *s_prefix = s_len + p.B;                              // [B + 1]
     const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp;
-    const int S = plan_runs<0, true, 1>(p, rt, s_len, s_prefix, s_red);
+    const int S = plan_runs<1>(p, rt, s_len, s_prefix, s_red);
     leave_plan(a.own.plan, p.B, s_prefix, S, rt);
-    run_warp<D, NT, 0, 2>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
+    run_warp<D, NT, 2>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
                        smem + C::RUN_OFF + rw * C::Run::RING, run_bars[rw]);
   } else if (warp >= kPxMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxIssueRegs));
@@ -465,7 +465,7 @@ td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, 
   if (D != 64 && D != 128) return TD_ERR_UNSUPPORTED;
   if (B < 1 || Hq < 1 || Hkv < 1 || T < 1 || Smax < 1 || Pmax < 1 || Hq % Hkv != 0) return TD_ERR_INVALID_ARG;
   if (B > TD_MAX_BATCH || Smax > (1 << 30) || Pmax > (1 << 30) || T > Smax) return TD_ERR_UNSUPPORTED;
-  const td_status st = plan_attn_runs(B, Hq, Hkv, T, Smax, D, 1, &plan->own);
+  const td_status st = plan_attn_runs(B, Hq, Hkv, T, Smax, D, &plan->own);
   if (st != TD_OK) return st;
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return TD_ERR_CUDA;
@@ -477,7 +477,7 @@ td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, 
   long long chunks = sms / groups;
   chunks = std::min(chunks, ((long long)Pmax + kPxKeys - 1) / kPxKeys);
   if (chunks < 1) chunks = 1;
-  if (groups * chunks * 16 > 0x7fffffffLL || rows > (1 << 26)) return TD_ERR_UNSUPPORTED;
+  if (groups * chunks * 16 > 0x7fffffffLL) return TD_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;
   plan->chunks = (int)chunks;
   plan->grid = (int)std::min((long long)sms, std::max((long long)plan->own.grid, groups * chunks));
@@ -491,7 +491,7 @@ cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, co
   float *part = reinterpret_cast<float *>(ws + plan.off_part);
   cudaError_t e = D == 64 ? launch_d<64>(plan, x, p, ws, part, stream) : launch_d<128>(plan, x, p, ws, part, stream);
   const PrefixPart joined{part, x.prefix_len, x.Pmax, plan.tiles, plan.chunks};
-  if (e == cudaSuccess) e = launch_join(D, plan.own, p, ws, &joined, stream);
+  if (e == cudaSuccess) e = launch_join(D, plan.own, p, ws, joined, stream);
   return e;
 }
 

@@ -18,8 +18,6 @@ namespace td {
 constexpr int kRunWarps = 4;
 constexpr int kRunThreads = 32 * kRunWarps;
 constexpr int kRunKeys = 16;  // keys of a step and stage
-constexpr int kRunStages = 3; // of a warp's ring in runs_kernel (two CTAs an SM)
-static_assert(kRunThreads == kThreads, "lengths_unchanged is written for CTAs of kThreads");
 
 // ST: stages of a warp's ring at D = 128 (twice as many at 64).
 template <int D, int ST>
@@ -29,7 +27,6 @@ struct RunCfg {
   static constexpr int BOX = kRunKeys * 128;             // 16 rows x 128 bytes
   static constexpr int TILE = HALVES * BOX;              // K or V of a stage
   static constexpr int RING = STAGES * 2 * TILE;
-  static constexpr int SMEM = kRunWarps * RING + 1024;   // + alignment slack; then two ints a sequence and one
 };
 
 struct RunArgs {
@@ -52,34 +49,33 @@ __device__ __forceinline__ int run_units(int keys) { return keys > 0 ? run_steps
 // The block of group g's keys in run r: runs and groups advance together, so every (group, run) that meet have their own.
 __device__ __forceinline__ long long run_block(long long g, int r) { return g + r; }
 
-// A barrier of the kRunThreads threads that take runs (id 0 where they are the whole CTA).
+// A barrier of the kRunThreads threads that take runs.
 template <int ID>
 __device__ __forceinline__ void run_barrier() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kRunThreads) : "memory");
 }
 
 // Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]); returns the units of a
-// run. By kRunThreads threads, `tid` theirs, meeting at barrier BAR. REPORT: with the status bits that the lengths raise.
-// Ends with a barrier.
-template <int WIN, bool REPORT, int BAR>
+// run; reports the status bits that the lengths raise. By kRunThreads threads, `tid` theirs, meeting at barrier BAR. Ends
+// with a barrier.
+template <int BAR>
 __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefix, int *s_red) {
   const int lane = tid & 31, warp = tid >> 5;
   const int U = p.Hkv * p.RB, per = (p.B + kRunThreads - 1) / kRunThreads, b0 = tid * per;
   int seg = 0;
   uint32_t bits = 0;
   for (int b = b0; b < min(b0 + per, p.B); ++b) {
-    const int L = attended_len(p, ld_relaxed(p.seq_lens + b), bits);
+    const int L = attended_len(p, p.seq_lens[b], bits);
     s_len[b] = L;
-    seg += run_units(keys_of<WIN>(p, L)) * U;
+    seg += run_units(L) * U;
   }
-  if (REPORT && blockIdx.x == 0) report(p.status, bits);
+  if (blockIdx.x == 0) report(p.status, bits);
   int incl = seg;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  run_barrier<BAR>();  // s_red may still be read by an earlier plan
   if (lane == 31) s_red[warp] = incl;
   run_barrier<BAR>();
   int W = 0, before = incl - seg;
@@ -90,7 +86,7 @@ __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefi
   }
   for (int b = b0; b < min(b0 + per, p.B); ++b) {
     s_prefix[b] = before;
-    before += run_units(keys_of<WIN>(p, s_len[b])) * U;
+    before += run_units(s_len[b]) * U;
   }
   if (tid == 0) s_prefix[p.B] = W;
   run_barrier<BAR>();
@@ -105,18 +101,17 @@ struct RunCursor {
 };
 
 // Moves the cursor to the next group with steps in units [.., u1); e = s where none is left.
-template <int WIN>
 __device__ __forceinline__ void next_group(const SplitParams &p, const int *s_len, int u1, RunCursor &c) {
   const int U = p.Hkv * p.RB;
   c.s = c.e = 0;
-  c.base += run_units(keys_of<WIN>(p, s_len[c.b]));
+  c.base += run_units(s_len[c.b]);
   if (++c.ug == U) {
     c.ug = 0;
     do {
       if (++c.b >= p.B) return;
     } while (s_len[c.b] == 0);
   }
-  if (c.base + kRunGroupUnits < u1) c.e = min(run_steps(keys_of<WIN>(p, s_len[c.b])), u1 - c.base - kRunGroupUnits);
+  if (c.base + kRunGroupUnits < u1) c.e = min(run_steps(s_len[c.b]), u1 - c.base - kRunGroupUnits);
 }
 
 // A warp's ring: its barriers, by one thread.
@@ -135,8 +130,7 @@ __device__ __forceinline__ void leave_plan(int *plan, int B, const int *s_prefix
 }
 
 // One warp's run: number `run`, S units long. The warp's ring (1024-byte aligned) and its barriers (initialised, one arrival).
-// WIN: kWindowPad for windowed attention, else 0.
-template <int D, int NT, int WIN, int ST>
+template <int D, int NT, int ST>
 __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                          const int *s_len, const int *s_prefix, int S, int run, unsigned char *ring_p,
                                          uint64_t *bars) {
@@ -156,13 +150,13 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
       const int mid = (lo + hi + 1) >> 1;
       if (s_prefix[mid] <= u0) lo = mid; else hi = mid - 1;
     }
-    const int n = run_units(keys_of<WIN>(p, s_len[lo]));
+    const int n = run_units(s_len[lo]);
     c.b = lo;
     c.ug = (u0 - s_prefix[lo]) / n;
     c.base = s_prefix[lo] + c.ug * n;
     c.s = max(u0 - c.base - kRunGroupUnits, 0);
     c.e = max(min(n, u1 - c.base) - kRunGroupUnits, 0);
-    if (c.s >= c.e) next_group<WIN>(p, s_len, u1, c);
+    if (c.s >= c.e) next_group(p, s_len, u1, c);
   }
   RunCursor ahead = c;  // the next step to be fetched
   int fetched = 0, used = 0;
@@ -171,24 +165,19 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
     const uint32_t bar = smem_u32(&bars[buf]);
     const uint32_t kdst = ring + buf * 2 * C::TILE, vdst = kdst + C::TILE;
     const int key = ahead.s * kRunKeys, z = ahead.b * p.Hkv + ahead.ug / p.RB;
-    int row = key;
-    if constexpr (WIN != 0) {
-      const WindowSpan span = window_span<WIN>(p.window, p.sinks, p.T, s_len[ahead.b]);
-      if (key >= span.head) row += span.shift;
-    }
     fence_proxy_async_smem();
     mbar_arrive_expect_tx(bar, 2 * C::TILE);
 #pragma unroll
     for (int h = 0; h < C::HALVES; ++h) {
-      tma_load_3d(kdst + h * C::BOX, &kmap, 64 * h, row, z, bar, policy);
-      tma_load_3d(vdst + h * C::BOX, &vmap, 64 * h, row, z, bar, policy);
+      tma_load_3d(kdst + h * C::BOX, &kmap, 64 * h, key, z, bar, policy);
+      tma_load_3d(vdst + h * C::BOX, &vmap, 64 * h, key, z, bar, policy);
     }
   };
   auto step_ahead = [&]() {  // the cursor is the warp's, whichever lane issues
     if (ahead.s >= ahead.e) return;
     if (lane == 0) fetch();
     ++fetched;
-    if (++ahead.s == ahead.e) next_group<WIN>(p, s_len, u1, ahead);
+    if (++ahead.s == ahead.e) next_group(p, s_len, u1, ahead);
   };
 #pragma unroll 1
   for (int i = 0; i < C::STAGES; ++i) step_ahead();
@@ -197,9 +186,6 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
   while (ok && c.s < c.e) {
     // one group: its query rows as B fragments of each n tile
     const int rb = c.ug % p.RB, kvh = c.ug / p.RB, L = s_len[c.b];
-    const int keys = keys_of<WIN>(p, L);
-    WindowSpan span = {};
-    if constexpr (WIN != 0) span = window_span<WIN>(p.window, p.sinks, p.T, L);
     uint32_t qb[NT][KSD][2];
     int lim[NL];
 #pragma unroll
@@ -216,7 +202,7 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rl = 8 * nt + 2 * tig + e, gl = rb * p.R + rl;
-        lim[2 * nt + e] = rl < p.R && gl < GT ? max(L - p.T + gl % p.T + 1 - span.shift, 0) : 0;
+        lim[2 * nt + e] = rl < p.R && gl < GT ? max(L - p.T + gl % p.T + 1, 0) : 0;
       }
     }
     float o[NT][KSD][4], m_run[NL], l_run[NL];
@@ -235,22 +221,19 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
       }
       const uint32_t kt = ring + buf * 2 * C::TILE, vt = kt + C::TILE;
       const int key0 = c.s * kRunKeys;
-      // V rows that no row of the batch sees: behind the sequence's end, or padding of the window's head. Zeroed, so
-      // that a masked probability meets no stale value
-      int z0 = keys - key0, z1 = kRunKeys;
-      if (WIN != 0 && key0 < span.head) z0 = p.sinks - key0, z1 = min(z1, span.head - key0);
-      if (z0 < z1) {
+      // V rows behind the sequence's end: zeroed, so that a masked probability meets no stale value
+      const int z0 = L - key0;
+      if (z0 < kRunKeys) {
         unsigned char *vrow = ring_p + buf * 2 * C::TILE + C::TILE;
-        z0 = max(z0, 0);
-        for (int i = lane; i < (z1 - z0) * (D / 8); i += 32)
+        for (int i = lane; i < (kRunKeys - z0) * (D / 8); i += 32)
           *reinterpret_cast<uint4 *>(vrow + tma_swz<kRunKeys>(z0 + i / (D / 8), i % (D / 8))) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async_smem();  // precedes the stage's next refill by the TMA unit
         __syncwarp();
       }
       if constexpr (NT == 1)
-        warp_keys16_n8<D, WIN, kRunKeys>(qb[0], kt, vt, 0, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
+        warp_keys16_n8<D, 0, kRunKeys>(qb[0], kt, vt, 0, key0, lim, p.qscale, o[0], m_run, l_run);
       else
-        warp_keys16_nt<D, WIN, NT, kRunKeys>(qb, kt, vt, 0, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
+        warp_keys16_nt<D, 0, NT, kRunKeys>(qb, kt, vt, 0, key0, lim, p.qscale, o, m_run, l_run);
       ++used;
       __syncwarp();  // every lane has read the stage
       step_ahead();
@@ -278,7 +261,7 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
           blk[p.R * (D + 1) + r] = ok ? l : 0.f;
         }
       }
-    if (ok) next_group<WIN>(p, s_len, u1, c);
+    if (ok) next_group(p, s_len, u1, c);
   }
   if (!ok) {
     // a copy never completed: the others in flight are waited for (bounded) before the ring goes
@@ -290,33 +273,12 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
   }
 }
 
-template <int D, int NT, int WIN>
-__global__ void __launch_bounds__(kRunThreads, 2) runs_kernel(const __grid_constant__ RunArgs a) {
-  using C = RunCfg<D, kRunStages>;
-  const SplitParams &p = a.p;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ int s_red[kRunWarps];
-  __shared__ __align__(8) uint64_t s_bars[kRunWarps][C::STAGES];
-  int *s_len = reinterpret_cast<int *>(smem_raw + C::SMEM);  // [B]
-  int *s_prefix = s_len + p.B;                               // [B + 1]
-  const int tid = threadIdx.x, warp = tid >> 5;
-  if ((tid & 31) == 0) init_ring<C::STAGES>(s_bars[warp]);
-  // planned on the lengths as they read before the wait for the previous kernel, again if they read otherwise after it
-  int S = plan_runs<WIN, false, 0>(p, tid, s_len, s_prefix, s_red);
-  griddep_wait();
-  griddep_launch_dependents();
-  if (!lengths_unchanged(p, s_len)) S = plan_runs<WIN, true, 0>(p, tid, s_len, s_prefix, s_red);
-  leave_plan(a.plan, p.B, s_prefix, S, tid);
-  run_warp<D, NT, WIN, kRunStages>(p, a.kmap, a.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + warp,
-                       align1024(smem_raw) + warp * C::RING, s_bars[warp]);
-}
-
-// Joins the parts of a row: those that the runs left of its own keys and, of a batch behind a shared prefix, one per
-// chunk of the prefix (blocks acc [D / 4][128 rows][4], m [128], l [128] of 128-row tiles).
+// Joins the parts of a row: those that the runs left of its own keys and one per chunk of the shared
+// prefix (blocks acc [D / 4][128 rows][4], m [128], l [128] of 128-row tiles).
 struct JoinArgs {
   const float *runs;      // runs_kernel's blocks
   const int *plan;        // and what it left in RunArgs::plan
-  const float *prefix;    // [Hkv][tiles][chunks] blocks, or null
+  const float *prefix;    // [Hkv][tiles][chunks] blocks
   const int32_t *prefix_len;
   void *out;              // [B, Hq, T, D] bf16
   float *lse;             // [B, Hq, T] or null
@@ -335,7 +297,7 @@ __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRow
 // is the chain of loads (the plan, a part's m and l and sums, one batch after another), so a batch is asked for at once,
 // and where rows are few their parts are spread over SPLIT warps.
 constexpr int kJoinThreads = 256;
-template <int D, bool PREFIX, int SPLIT>
+template <int D, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a) {
   constexpr int COLS = kJoinThreads / 32 / SPLIT;  // warps side by side, eight dims each
   constexpr int SLABS = D / 8 / COLS, kBatch = 4;  // kBatch parts' loads in flight at once
@@ -348,10 +310,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
   griddep_launch_dependents();
   // the runs that hold steps of this row's group, and the chunks of the prefix
   const int U = a.Hkv * a.RB, first = __ldcg(a.plan + b), next = __ldcg(a.plan + b + 1), S = __ldcg(a.plan + a.B + 1);
-  const int P = PREFIX ? prefix_keys(__ldcg(a.prefix_len), a.Pmax) : 0;
+  const int P = prefix_keys(__ldcg(a.prefix_len), a.Pmax);
   const int units = (next - first) / U, base = first + (kvh * a.RB + rb) * units;
   const int r0 = (base + kRunGroupUnits) / S, n_runs = units > 0 ? (base + units - 1) / S + 1 - r0 : 0;
-  const int C = PREFIX ? prefix_chunk(P, a.chunks) : 0, n = n_runs + (P > 0 ? (P + C - 1) / C : 0);
+  const int C = prefix_chunk(P, a.chunks), n = n_runs + (P > 0 ? (P + C - 1) / C : 0);
   const int BF = run_block_floats(a.R, D);
   const float *runs = a.runs + run_block(((long long)b * a.Hkv + kvh) * a.RB + rb, r0) * BF;
   const float *chunks = a.prefix + ((long long)kvh * a.tiles + row / kPrefixRows) * a.chunks * prefix_block_floats(D);
@@ -365,7 +327,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int p = p0 + i * SPLIT;
-      const bool own = !PREFIX || p < n_runs;
+      const bool own = p < n_runs;
       const float *pb = own ? runs + (long long)p * BF : chunks + (long long)(p - n_runs) * prefix_block_floats(D);
       const int R = own ? a.R : kPrefixRows, at = own ? r : row % kPrefixRows;
       m[i] = -INFINITY, l[i] = 0.f;

@@ -262,5 +262,5 @@ def test_kernels_have_no_spills(lib):
                          r"spill stores, (\d+) bytes spill loads", log)
     for k, n in (("norm_append_kernel", 4), ("norm_append_rows_kernel", 4), ("mma_kernelILi64", 10), ("mma_kernelILi128", 10),
                  ("cluster_kernelILi64", 6), ("cluster_kernelILi128", 6), ("Li1EEEvNS_11SplitParams", 6), ("14prefill_kernel", 4),
-                 ("13prefix_kernel", 6), ("runs_kernel", 6), ("join_kernel", 16)):
+                 ("13prefix_kernel", 6), ("join_kernel", 8)):
         assert [(int(st), int(ld)) for name, _, st, ld in entries if k in name] == [(0, 0)] * n, k
