@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       // P = 2^(s - m) as bf16 pairs into P buffer b0, once the P V product of kt-2 has read it
       const float nbase = m_ref == -INFINITY ? 0.f : -m_ref;
       uint32_t pk[kPfKeys / 2];
-      if (full)
+      // (a masked score times a scale other than 0 is -inf, whose probability is 0 without a second mask)
+      if (full || (WIN && qscale != 0.f))
         l += p_row<false>(sv, qscale, nbase, seen, pk);
       else
         l += p_row<true>(sv, qscale, nbase, seen, pk);

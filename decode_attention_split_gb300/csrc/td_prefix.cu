@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
           const SeenFirst seen{vis - c};
           uint32_t pk[16];
           const float(&part)[32] = reinterpret_cast<const float(&)[32]>(sv[c]);
-          if (left >= kPxKeys)
+          if (left >= kPxKeys || qscale != 0.f)  // (a masked score times a scale other than 0 is -inf: probability 0)
             l += p_row<false>(part, qscale, nbase, seen, pk);
           else
             l += p_row<true>(part, qscale, nbase, seen, pk);
