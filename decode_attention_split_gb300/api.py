@@ -127,7 +127,7 @@ def _cached_workspace(nbytes: int, device: torch.device, stream_ptr: int, shape_
     """A zero-filled workspace per (device, stream, call shape).
 
     The library leaves the counter area of a workspace zero only for its own layout, and the
-    layout follows the call's shape arguments, so a workspace is never shared across shapes."""
+    layout follows the call's shape arguments and dtype, so a workspace is never shared across them."""
     key = (device.index, stream_ptr) + shape_key
     with _ws_lock:
         ws = _ws_cache.pop(key, None)
@@ -174,7 +174,7 @@ def _attn(name, q4, k_cache, v_cache, seq_lens, scale, split, out, lse, workspac
         sp = _stream(stream, dev)
         if workspace is None:
             need = td_decode_workspace_bytes(B, Hq, Hkv, Smax, D, T, split)
-            workspace = _cached_workspace(need, dev, sp, (B, Hq, Hkv, Smax, D, T, split))
+            workspace = _cached_workspace(need, dev, sp, (q4.dtype, B, Hq, Hkv, Smax, D, T, split))
         if workspace.dtype != torch.uint8:
             raise TypeError("workspace must be a uint8 tensor")
         fn = getattr(lib(), name)
@@ -332,7 +332,7 @@ def td_rope_append_attn(q, k_new, v_new, k_cache, v_cache, seq_lens, scale: floa
         sp = _stream(stream, dev)
         if workspace is None:
             need = td_decode_workspace_bytes(B, Hq, Hkv, Smax, D, T, split)
-            workspace = _cached_workspace(need, dev, sp, (B, Hq, Hkv, Smax, D, T, split))
+            workspace = _cached_workspace(need, dev, sp, (q.dtype, B, Hq, Hkv, Smax, D, T, split))
         if workspace.dtype != torch.uint8:
             raise TypeError("workspace must be a uint8 tensor")
         st = lib().td_rope_append_attn(_code(q), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cos_t), _ptr(sin_t),

@@ -514,3 +514,21 @@ def test_dirty_workspace_is_reported(td):
     td.td_decode_attn(q, k, v, sl, case.scale, 64, workspace=ws, dev_status=st)
     torch.cuda.synchronize()
     assert int(st.item()) & td.DEV_WORKSPACE_DIRTY
+
+
+def test_types_in_turn_on_kept_workspaces(td):
+    """Verify calls of one shape in both types without a workspace: the layouts differ, so each type keeps its own."""
+    B, Hq, Hkv, S, D, T = 8, 32, 8, 4000, 128, 6
+    g = torch.Generator(device="cuda").manual_seed(41)
+    lens = torch.tensor([4000, 3000, 2000, 1000, 500, 4000, 100, 3999], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args, want = {}, {}
+    for dt in (torch.bfloat16, torch.float32):
+        q, k, v = (torch.randn(B, h, n, D, generator=g, device="cuda").to(dt) for h, n in ((Hq, T), (Hkv, S), (Hkv, S)))
+        args[dt] = (q, k, v, lens)
+        ws = torch.zeros(td.td_decode_workspace_bytes(B, Hq, Hkv, S, D, T), dtype=torch.uint8, device="cuda")
+        want[dt] = td.td_verify_attn(*args[dt], workspace=ws)
+    for dt in (torch.bfloat16, torch.float32) * 2:
+        assert torch.equal(td.td_verify_attn(*args[dt], dev_status=st), want[dt]), dt
+    torch.cuda.synchronize()
+    assert int(st) == 0
