@@ -1,6 +1,7 @@
 // Host-side interfaces between the td translation units (not part of the public ABI).
 #pragma once
 
+#include <mutex>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -200,5 +201,24 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// One kernel's opt-in to more than 48 KB of dynamic shared memory, made once per device (static at its launch).
+class OptIn {
+ public:
+  cudaError_t operator()(const void *fn, int smem) {
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu_);
+    if (done_[device]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    done_[device] = e == cudaSuccess;
+    return e;
+  }
+
+ private:
+  static constexpr int kMaxDevices = 64;
+  std::mutex mu_;
+  bool done_[kMaxDevices] = {};
+};
 
 }  // namespace td

@@ -463,12 +463,8 @@ cudaError_t launch_prefill_d(PfArgs &a, const void *q, const void *k, const void
       !pf_map(&a.kmap, k, (long long)a.B * a.Hkv, a.Smax, D, kPfKeys) ||
       !pf_map(&a.vmap, v, (long long)a.B * a.Hkv, a.Smax, D, kPfKeys))
     return cudaErrorInvalidValue;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(reinterpret_cast<const void *>(&prefill_kernel<D, WIN>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
-  });
+  static OptIn opt_in;
+  const cudaError_t attr = opt_in(reinterpret_cast<const void *>(&prefill_kernel<D, WIN>), PfCfg<D>::SMEM);
   if (attr != cudaSuccess) return attr;
   const dim3 grid((unsigned)(a.B * a.Hq), (unsigned)((a.T + kPfRows - 1) / kPfRows));
   return launch_pdl(prefill_kernel<D, WIN>, grid, dim3(kPfThreads), PfCfg<D>::SMEM, stream, a);

@@ -15,7 +15,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "td_internal.h"
 #include "td_runs.cuh"
@@ -40,9 +39,9 @@ constexpr int kPxKRegion = kPxKeys * 128;      // bytes of one swizzled [128 key
 // others' strength, some row of the 128 moved in nearly every tile (490 cycles of a tile's 3600, 175 with 32).
 constexpr float kPxGap = 32.f;
 // Registers a thread: launched with 128 (65536 / 512), then split between softmax, run, and product and copy warps. A run
-// over row blocks of more than 8 rows needs more than 200, and the softmax warps then keep to what they have.
-__host__ __device__ constexpr int px_soft_regs(int NT) { return NT == 1 ? 136 : 128; }
-__host__ __device__ constexpr int px_run_regs(int NT) { return NT == 1 ? 200 : 216; }
+// over row blocks of more than 16 rows needs more than 200, and the softmax warps then keep to what they have.
+__host__ __device__ constexpr int px_soft_regs(int NT) { return NT <= 2 ? 136 : 128; }
+__host__ __device__ constexpr int px_run_regs(int NT) { return NT <= 2 ? 200 : 216; }
 constexpr int kPxIssueRegs = 40;
 static_assert(256 * px_soft_regs(1) + 128 * px_run_regs(1) + 128 * kPxIssueRegs <= 512 * 128 &&
                   256 * px_soft_regs(3) + 128 * px_run_regs(3) + 128 * kPxIssueRegs <= 512 * 128,
@@ -295,14 +294,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
       }
       if (quarter >= busy) continue;
       // (a warp whose wait gave up takes part in nothing but the meetings from then on, which the other warp counts on)
-      const int keys = w.c1 - w.c0;
       float m_ref = -INFINITY, l = 0.f;  // this row's reference maximum, and its sum over this thread's keys
       for (int k = g0; k < g; ++k) {
         const int b0 = k & 1;
         ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar_s[b0]), (uint32_t)(k >> 1) & 1u));
         tc_fence_after();
         // keys of the tile (fewer at the prefix's end alone), and of this half of it
-        const int left = keys - (k - g0) * kPxKeys, vis = min(kPxHalf, left - half * kPxHalf);
+        const int left = w.c1 - w.c0 - (k - g0) * kPxKeys, vis = min(kPxHalf, left - half * kPxHalf);
         if (ok && left < kPxKeys) {
           // V rows behind the prefix, once landed: zeroed (a masked p of 0 must not meet a stale value)
           const int buf = k % C::NST;
@@ -428,14 +426,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 
 template <int D, int NT>
 cudaError_t launch_nt(const PxArgs &a, int grid, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(reinterpret_cast<const void *>(&prefix_kernel<D, NT>),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                PxCfg<D>::SMEM + (2 * TD_MAX_BATCH + 1) * (int)sizeof(int));
-  });
-  if (attr != cudaSuccess) return attr;
+  static OptIn opt_in;
+  const cudaError_t e = opt_in(reinterpret_cast<const void *>(&prefix_kernel<D, NT>),
+                               PxCfg<D>::SMEM + (2 * TD_MAX_BATCH + 1) * (int)sizeof(int));
+  if (e != cudaSuccess) return e;
   const size_t smem = PxCfg<D>::SMEM + (2 * (size_t)a.own.p.B + 1) * sizeof(int);
   return launch_pdl(prefix_kernel<D, NT>, dim3(grid), dim3(kPxThreads), smem, stream, a);
 }

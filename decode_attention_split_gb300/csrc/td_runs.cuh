@@ -6,7 +6,7 @@
 // K and V each, TMA) full across the ends of groups, so a warp that finishes one group and starts the next has
 // copies in flight all the time, and no barrier ties the warps of a CTA together once the runs are planned. Where
 // a CTA's warps share a chunk instead (split_attn_mma_kernel), starting and finishing a chunk costs a CTA as much as a few
-// stages of 64 keys, and chunks of one size leave CTAs idle: many short sequences, windows among them, pay both.
+// stages of 64 keys, and chunks of one size leave CTAs idle: many short sequences pay both.
 // A warp leaves each group it met as one partial block, so a row has as many parts as runs touch its group.
 #pragma once
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
     }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (l[i] > 0.f) Mn = fmaxf(Mn, m[i]);  // a part without keys (l = 0) counts nothing
+      if (l[i] != 0.f) Mn = fmaxf(Mn, m[i]);  // a part without keys (l = 0) counts nothing; a NaN stays one
     const float ref = Mn == -INFINITY ? 0.f : Mn;
     const float alpha = exp2f(M - ref);
     L *= alpha;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
     for (int k = 0; k < 8; ++k) A[k] *= alpha;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (l[i] > 0.f) {
+      if (l[i] != 0.f) {
         const float f = exp2f(m[i] - ref);
         L = fmaf(l[i], f, L);
         A[0] = fmaf(x[i].x, f, A[0]), A[1] = fmaf(x[i].y, f, A[1]), A[2] = fmaf(x[i].z, f, A[2]), A[3] = fmaf(x[i].w, f, A[3]);
@@ -370,14 +370,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
 #pragma unroll
     for (int j = 0; j < SPLIT; ++j) {
       ml[j] = s_ml[threadIdx.x + 32 * COLS * j];
-      if (ml[j].y > 0.f) M = fmaxf(M, ml[j].x);
+      if (ml[j].y != 0.f) M = fmaxf(M, ml[j].x);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) A[k] = 0.f;
 #pragma unroll
     for (int j = 0; j < SPLIT; ++j) {
-      if (ml[j].y > 0.f) {
-        const float f = exp2f(ml[j].x - M);
+      if (ml[j].y != 0.f) {
+        const float f = exp2f(ml[j].x - (M == -INFINITY ? 0.f : M));
         L = fmaf(ml[j].y, f, L);
 #pragma unroll
         for (int k = 0; k < 8; ++k) A[k] = fmaf(s_acc[k][threadIdx.x + 32 * COLS * j], f, A[k]);
@@ -386,11 +386,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
   }
   if (group * 32 + (int)(threadIdx.x & 31) >= rows) return;
   const long long at = (long long)b * a.Hq * a.T + (long long)kvh * a.GT + gt;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at * D + d8 * 8) =
       make_uint4(pack_bf16x2(A[0] * inv, A[1] * inv), pack_bf16x2(A[2] * inv, A[3] * inv),
                  pack_bf16x2(A[4] * inv, A[5] * inv), pack_bf16x2(A[6] * inv, A[7] * inv));
-  if (a.lse != nullptr && d8 == 0) a.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+  if (a.lse != nullptr && d8 == 0) a.lse[at] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
 }  // namespace td

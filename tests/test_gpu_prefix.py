@@ -126,6 +126,59 @@ def test_a_large_maximum_late_in_the_prefix(td):
     p.check(*p.run(td))
 
 
+@pytest.mark.parametrize("T", [1, 5])
+def test_nan_reaches_the_rows_that_see_it_and_no_other(td, T):
+    D, Hq, Hkv, S = 128, 8, 2, 100
+    p = Problem(D, Hq, Hkv, T, 500, 500, S, [100, 60, T], seed=31)
+    clean, clean_lse = p.run(td)
+    p.kp[1, 300, 7] = float("nan")                    # a key of the prefix, kv head 1
+    out, lse = p.run(td)
+    assert torch.equal(out[:, :4], clean[:, :4]) and torch.equal(lse[:, :4], clean_lse[:, :4])
+    assert out[:, 4:].isnan().all() and lse[:, 4:].isnan().all()
+    p = Problem(D, Hq, Hkv, T, 500, 500, S, [100, 60, T], seed=31)
+    p.v[1, 0, 20, 5] = float("nan")                   # a value element of sequence 1, kv head 0
+    p.k[2, 1, 0, 0] = float("inf")                    # a key of sequence 2, kv head 1
+    out, lse = p.run(td)
+    assert out[1, :4, :, 5].isnan().all() and torch.equal(out[1, :4, :, 6:], clean[1, :4, :, 6:])
+    # its scores are infinite with the query element's sign: infinity makes a row NaN, minus infinity weighs nothing
+    up = (p.q[2, 4:, :, 0] > 0)
+    sees = torch.from_numpy(p.see[2, :, p.Pmax])
+    assert torch.equal(out[2, 4:].isnan().all(-1), up & sees)
+    assert out[2, 4:].isfinite().all(-1).equal(~(up & sees))
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[1, 4:], clean[1, 4:]) and torch.equal(out[2, :4], clean[2, :4])
+
+
+def test_a_long_chunk_behind_a_prefix(td):
+    """A hundred new tokens a sequence: many row blocks over the own keys, tiles of rows inside one sequence."""
+    p = Problem(64, 6, 2, 100, 400, 333, 180, [180, 100, 133], seed=32)
+    p.check(*p.run(td))
+
+
+@pytest.mark.parametrize("D,T,P", [(128, 1, 5), (64, 6, 0), (128, 3, 2000)])
+def test_long_own_keys_of_few_sequences(td, D, T, P):
+    """Each row's own keys in many runs (more parts than the join takes at a time), behind a short prefix or none."""
+    p = Problem(D, 4, 1, T, 2000, P, 20000, [20000, 0 if T == 1 else T, 13001], seed=34)
+    p.check(*p.run(td))
+
+
+def test_any_workspace_contents(td):
+    p = Problem(128, 8, 2, 6, 700, 650, 300, [300, 6, 90, 2], seed=35)
+    q = p.q.shape
+    want = p.run(td)
+    for fill in (0, 255, 127):
+        n = td.td_prefix_workspace_bytes(q[0], q[1], 2, 700, 300, 128, 6)
+        got = p.run(td, workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_the_largest_batch(td):
+    B = 1024
+    lens = [(7 * i) % 33 for i in range(B)]
+    p = Problem(64, 2, 1, 1, 100, 77, 32, lens, seed=33)
+    out, lse = p.run(td)
+    p.check(out, lse)
+
+
 def test_empty_everywhere(td):
     p = Problem(128, 4, 2, 1, 64, 0, 32, [0, 0], seed=8)
     out, lse = p.run(td)
