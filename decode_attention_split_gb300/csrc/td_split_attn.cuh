@@ -171,7 +171,7 @@ __device__ __forceinline__ int first_chunk_size(const SplitParams &p, long long 
   if (want < p.min_chunk) want = p.min_chunk;
   const long long fits = ((long long)longest + p.ns_ws - 1) / p.ns_ws;
   if (want < fits) want = fits;
-  if constexpr (WIN != 0) return (int)((want + 15) / 16 * 16);  // chunks start at multiples of 16 keys
+  if constexpr (WIN != 0) return (int)min((want + 15) / 16, p.Smax / 16 + 2LL) * 16;  // chunks start at multiples of 16 keys
   int S = (int)(want > p.Smax ? p.Smax : want);
   return S < 1 ? 1 : S;
 }
@@ -249,7 +249,8 @@ static __device__ void plan_items(const SplitParams &p, int *s_len, int *s_prefi
       const long long drop = ((long long)longest + n_long - 2) / (n_long - 1);
       if (grow < drop) grow = drop;
       grow = (grow + 15) / 16 * 16;
-      S = (int)(grow > p.Smax && WIN == 0 ? p.Smax : grow);
+      if constexpr (WIN != 0) S = (int)min(grow, (p.Smax / 16 + 2LL) * 16);  // (a window's keys: Smax + 15 at most)
+      else S = (int)(grow > p.Smax ? p.Smax : grow);
       continue;  // the same decision in every thread
     }
     int before = incl - seg;

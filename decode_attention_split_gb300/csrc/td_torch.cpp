@@ -515,7 +515,8 @@ PyObject *window_attn(PyObject *, PyObject *const *a, Py_ssize_t) {
     at::Tensor kept;
     if (ws == nullptr) {
       kept = kept_workspace(
-          {kWsWindow, dev, stream_key(place), c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, split, window, sinks}, c.q,
+          {kWsWindow, dev, stream_key(place), c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, split, window, sinks,
+           c.dt}, c.q,
           [&] { return td_window_workspace_bytes(c.B, c.Hq, c.Hkv, c.Smax, c.D, c.T, window, sinks, split); });
       ws = &kept;
     }

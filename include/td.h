@@ -32,6 +32,12 @@
  *                  its next step; "tinydecode"'s prefill path is causal over the prompt).
  *   td_*_q8        an 8-bit KV cache: int8 codes with one fp32 scale per row (the per-row
  *                  INT8 scheme "llm-decode-cuda" applies to its weights, for the K/V bytes).
+ *   td_norm_rope_kv_append  the rotating cache write of layers that first norm every head of
+ *                  the queries and keys (root mean square, learned weights).
+ *   td_*_attn_window  decode, verify and prefill attention over a sliding window of the cache
+ *                  whose first rows stay visible (sinks).
+ *   td_*_attn_prefix  decode and verify attention of a batch whose sequences share a prefix,
+ *                  stored and read once, ahead of their own rows.
  *   td_*_f8        an 8-bit KV cache in blocks: e4m3 codes with one fp32 scale per block of
  *                  tokens and kv head, written (optionally rotated first, by positions with
  *                  several axes), read back, and attended.
@@ -100,10 +106,10 @@ int td_last_cuda_error(void);
  * Workspace for td_decode_attn / td_verify_attn, in bytes, for the current CUDA device.
  * q_len = T (1 for decode); split as passed to the attention call (0 = automatic).
  * The workspace holds a counter area followed by per-split partials; their layout follows
- * the shape arguments. It must be zero-filled (e.g. cudaMemset) before its first use; every
+ * the shape arguments and the dtype. It must be zero-filled (e.g. cudaMemset) before its first use; every
  * call that runs to completion leaves its counter area zero again, so the workspace can be
- * reused by later calls with the same (B, Hq, Hkv, Smax, D, q_len, split) on one stream.
- * Before using it for other shapes, zero it again (or use another). Calls running
+ * reused by later calls with the same dtype and (B, Hq, Hkv, Smax, D, q_len, split) on one stream.
+ * Before using it for others, zero it again (or use another). Calls running
  * concurrently need separate workspaces. Returns 0 for invalid arguments.
  */
 size_t td_decode_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int split);
@@ -397,8 +403,8 @@ td_status td_prefill_attn(const void *q, const void *k_cache, const void *v_cach
  * no token of a call sees are never used, whatever they hold; a value that one token of a verify chunk or of a prompt's
  * tile of 128 sees and another does not must be finite for both (a weight of 0 times NaN is NaN), as in the plain calls.
  * td_decode_attn_window and td_verify_attn_window: TD_F32 and TD_BF16; split is 0 or a multiple of 16; a workspace of
- * td_window_workspace_bytes, used as td_decode_workspace_bytes says, for one (B, Hq, Hkv, Smax, D, q_len, window,
- * sinks, split). Their cost follows the window, not the context: per sequence and kv head they read
+ * td_window_workspace_bytes, used as td_decode_workspace_bytes says, for one dtype and (B, Hq, Hkv, Smax, D, q_len,
+ * window, sinks, split). Their cost follows the window, not the context: per sequence and kv head they read
  * min(L, sinks + window + T - 1) rows. td_prefill_attn_window: bf16, whole tiles of 64 keys.
  */
 size_t td_window_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int window, int sinks, int split);
@@ -422,8 +428,8 @@ td_status td_prefill_attn_window(const void *q, const void *k_cache, const void 
  * in one softmax (its position is P + L_b - T + t: td_norm_rope_kv_append takes positions). L_b may be 0 with T = 1;
  * rows without any key give out = 0 and lse = -inf, and L_b < T sets TD_DEV_VERIFY_SHORT as in td_verify_attn. bf16,
  * D 64 or 128. The parts over the prefix and over the own keys are kept in fp32 and joined; out is rounded once.
- * Three launches; the workspace is td_prefix_workspace_bytes', under td_decode_workspace_bytes' rules, for one
- * (B, Hq, Hkv, Pmax, Smax, D, q_len).
+ * Two launches. The workspace is td_prefix_workspace_bytes', 256-byte aligned; it need not be zeroed and keeps nothing
+ * from one call to the next, so any calls on one stream may share it.
  */
 size_t td_prefix_workspace_bytes(int B, int Hq, int Hkv, int Pmax, int Smax, int D, int q_len);
 td_status td_decode_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,

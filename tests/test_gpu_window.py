@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from decode_attention_split_gb300.workloads import rope_tables
 from masked_ref import check, window_mask
 
 pytestmark = pytest.mark.gpu
@@ -144,6 +145,49 @@ def test_zero_and_negative_scale(td, scale):
         p = Problem("bf16", 128, 4, 2, T, 400, [390], 90, 5, seed=9)
         p.scale = scale
         p.check(*p.run(td, prompt=prompt))
+
+
+def test_a_layer_from_prompt_to_tokens(td):
+    """A windowed layer as it is used: the prompt's rows normed, rotated and appended, its attention, then a verify chunk
+    and single tokens; each attention against the plain one over the rows in the cache."""
+    D, Hq, Hkv, S, window, sinks = 128, 8, 2, 260, 48, 4
+    g = torch.Generator().manual_seed(13)
+
+    def draw(*s):
+        return torch.randn(*s, generator=g).bfloat16().cuda()
+    kc, vc = draw(2, Hkv, S, D), draw(2, Hkv, S, D)
+    lens = torch.tensor([0, 17], dtype=torch.int32).cuda()
+    w = (1 + 0.1 * torch.randn(D, generator=g)).cuda()
+    cos, sin = (t.cuda() for t in rope_tables(S, D))
+    for step, T in enumerate((200, 6, 1, 1, 3)):
+        q = td.td_norm_rope_kv_append(draw(2, Hkv, T, D), draw(2, Hkv, T, D), kc, vc, lens, w, cos, sin,
+                                      q=draw(2, Hq, T, D), q_weight=w)
+        if T > 100:
+            out, lse = td.td_prefill_attn_window(q, kc, vc, lens, window, sinks, return_lse=True)
+        elif T > 1:
+            out, lse = td.td_verify_attn_window(q, kc, vc, lens, window, sinks, return_lse=True)
+        else:
+            out, lse = td.td_decode_attn_window(q[:, :, 0].contiguous(), kc, vc, lens, window, sinks, return_lse=True)
+        torch.cuda.synchronize()
+        check(out.cpu().view(q.shape), lse.cpu().view(q.shape[:-1]), q.cpu(), kc.cpu(), vc.cpu(),
+              window_mask(lens.tolist(), T, S, window, sinks), D ** -0.5, f"step {step}")
+    assert lens.tolist() == [211, 228]
+
+
+def test_types_in_turn_on_kept_workspaces(td):
+    """Both types of one shape without a workspace: their layouts differ (24 rows are one row block in bf16, six in fp32)."""
+    lens = [4000, 3000, 2000, 1000, 500, 4000, 100, 3999]
+    p = {dt: Problem(dt, 128, 32, 8, 6, 4000, lens, 2500, 16, seed=15) for dt in DT}
+    want = {dt: [x.clone() for x in p[dt].run(td, workspace=torch.zeros(
+        td.td_window_workspace_bytes(8, 32, 8, 4000, 128, 2500, 16, q_len=6), dtype=torch.uint8, device="cuda"))] for dt in DT}
+    for dt in ("bf16", "f32", "bf16", "f32"):
+        assert all(torch.equal(x, y) for x, y in zip(p[dt].run(td), want[dt])), dt
+
+
+def test_the_largest_batch(td):
+    lens = [(11 * i) % 41 for i in range(1024)]
+    p = Problem("bf16", 64, 2, 1, 1, 40, lens, 9, 2, seed=14)
+    p.check(*p.run(td))
 
 
 def test_own_workspace_streams_and_graph(td):
