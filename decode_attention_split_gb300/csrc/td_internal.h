@@ -150,7 +150,7 @@ cudaError_t launch_prefill(const void *q, const void *k, const void *v, const in
 struct RunsPlan {
   int R, RB;      // rows of a row block, row blocks of a kv head
   int grid;
-  size_t off_blocks, bytes;  // workspace: the plan's array, the blocks (nothing of it needs zeroing)
+  size_t bytes;   // workspace: the blocks (nothing of it needs zeroing)
 };
 // keys: the most a sequence attends.
 td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, RunsPlan *plan);
@@ -159,6 +159,7 @@ struct PrefixPart {
   const float *part;
   const int32_t *prefix_len;
   int Pmax, tiles, chunks;
+  int grid;  // CTAs whose warps took the runs
 };
 cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const unsigned char *ws, const PrefixPart &x,
                         cudaStream_t stream);

@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     int *s_prefix = s_len + p.B;                              // [B + 1]
     const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp;
     const int S = plan_runs<1>(p, rt, s_len, s_prefix, s_red);
-    leave_plan(a.own.plan, p.B, s_prefix, S, rt);
     run_warp<D, NT, 2>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
                        smem + C::RUN_OFF + rw * C::Run::RING, run_bars[rw]);
   } else if (warp >= kPxMmaWarp) {
@@ -483,8 +482,11 @@ td_status plan_prefix(int B, int Hq, int Hkv, int T, int Pmax, int Smax, int D, 
 cudaError_t launch_prefix(int D, const PrefixPlan &plan, const PrefixAttn &x, const SplitParams &p, unsigned char *ws,
                           cudaStream_t stream) {
   float *part = reinterpret_cast<float *>(ws + plan.off_part);
+  // another thread's call on this stream and workspace comes before or after both launches, not between them
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
   cudaError_t e = D == 64 ? launch_d<64>(plan, x, p, ws, part, stream) : launch_d<128>(plan, x, p, ws, part, stream);
-  const PrefixPart joined{part, x.prefix_len, x.Pmax, plan.tiles, plan.chunks};
+  const PrefixPart joined{part, x.prefix_len, x.Pmax, plan.tiles, plan.chunks, plan.grid};
   if (e == cudaSuccess) e = launch_join(D, plan.own, p, ws, joined, stream);
   return e;
 }

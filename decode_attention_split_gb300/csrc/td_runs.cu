@@ -42,8 +42,7 @@ td_status plan_attn_runs(int B, int Hq, int Hkv, int T, int keys, int D, RunsPla
   if (most >= (1LL << 30) || B * GT > (1LL << 26)) return TD_ERR_UNSUPPORTED;  // counted in 32 bits
   const long long ctas = (most / kRunLeast + kRunWarps) / kRunWarps;
   plan->grid = (int)std::min((long long)sms, ctas);
-  plan->off_blocks = align256(((size_t)B + 2) * sizeof(int));
-  plan->bytes = plan->off_blocks + align256((size_t)(groups + plan->grid * kRunWarps) * run_block_floats(plan->R, D) * sizeof(float));
+  plan->bytes = align256((size_t)(groups + plan->grid * kRunWarps) * run_block_floats(plan->R, D) * sizeof(float));
   return TD_OK;
 }
 
@@ -51,8 +50,7 @@ bool fill_runs(RunArgs *a, int D, const RunsPlan &plan, const SplitParams &p, un
   a->p = p;
   a->p.R = plan.R;
   a->p.RB = plan.RB;
-  a->p.ws_part = reinterpret_cast<float *>(ws + plan.off_blocks);
-  a->plan = reinterpret_cast<int *>(ws);
+  a->p.ws_part = reinterpret_cast<float *>(ws);
   return encode_cache_map(&a->kmap, p.k, p.B, p.Hkv, p.Smax, D, kRunKeys) &&
          encode_cache_map(&a->vmap, p.v, p.B, p.Hkv, p.Smax, D, kRunKeys);
 }
@@ -60,10 +58,11 @@ bool fill_runs(RunArgs *a, int D, const RunsPlan &plan, const SplitParams &p, un
 cudaError_t launch_join(int D, const RunsPlan &plan, const SplitParams &p, const unsigned char *ws, const PrefixPart &x,
                         cudaStream_t stream) {
   JoinArgs a = {};
-  a.runs = reinterpret_cast<const float *>(ws + plan.off_blocks);
-  a.plan = reinterpret_cast<const int *>(ws);
+  a.runs = reinterpret_cast<const float *>(ws);
+  a.seq_lens = p.seq_lens;
   a.out = p.out, a.lse = p.lse;
   a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.T = p.T, a.GT = p.G * p.T, a.R = plan.R, a.RB = plan.RB;
+  a.Smax = p.Smax, a.grid = x.grid;
   a.prefix = x.part, a.prefix_len = x.prefix_len, a.Pmax = x.Pmax, a.tiles = x.tiles, a.chunks = x.chunks;
   return D == 64 ? launch_join_d<64>(a, stream) : launch_join_d<128>(a, stream);
 }

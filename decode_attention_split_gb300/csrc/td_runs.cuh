@@ -33,7 +33,6 @@ struct RunArgs {
   CUtensorMap kmap;  // caches [B*Hkv][Smax][D], boxes of 16 rows
   CUtensorMap vmap;
   SplitParams p;
-  int *plan;         // workspace: [B + 1] units before each sequence, then the units of a run
 };
 bool fill_runs(RunArgs *a, int D, const RunsPlan &plan, const SplitParams &p, unsigned char *ws);
 
@@ -53,6 +52,12 @@ __device__ __forceinline__ long long run_block(long long g, int r) { return g + 
 template <int ID>
 __device__ __forceinline__ void run_barrier() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(kRunThreads) : "memory");
+}
+
+// Units of a run, of W in all dealt to `grid` CTAs.
+__device__ __forceinline__ int run_length(int W, int grid) {
+  const int runs = grid * kRunWarps;
+  return max((W + runs - 1) / runs, kRunLeast);
 }
 
 // Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]); returns the units of a
@@ -90,8 +95,7 @@ __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefi
   }
   if (tid == 0) s_prefix[p.B] = W;
   run_barrier<BAR>();
-  const int runs = gridDim.x * kRunWarps;
-  return max((W + runs - 1) / runs, kRunLeast);
+  return run_length(W, gridDim.x);
 }
 
 // Where a warp is in its run: group `ug` of sequence b, steps [s, e) of it left in this run.
@@ -120,13 +124,6 @@ __device__ __forceinline__ void init_ring(uint64_t *bars) {
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
   fence_mbar_init();
-}
-
-// What the join needs of the plan, from the first CTA.
-__device__ __forceinline__ void leave_plan(int *plan, int B, const int *s_prefix, int S, int tid) {
-  if (blockIdx.x != 0) return;
-  for (int b = tid; b <= B; b += kRunThreads) plan[b] = s_prefix[b];
-  if (tid == 0) plan[B + 1] = S;
 }
 
 // One warp's run: number `run`, S units long. The warp's ring (1024-byte aligned) and its barriers (initialised, one arrival).
@@ -276,13 +273,13 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
 // Joins the parts of a row: those that the runs left of its own keys and one per chunk of the shared
 // prefix (blocks acc [D / 4][128 rows][4], m [128], l [128] of 128-row tiles).
 struct JoinArgs {
-  const float *runs;      // runs_kernel's blocks
-  const int *plan;        // and what it left in RunArgs::plan
+  const float *runs;      // blocks of the runs that `grid` CTAs took
+  const int32_t *seq_lens;
   const float *prefix;    // [Hkv][tiles][chunks] blocks
   const int32_t *prefix_len;
   void *out;              // [B, Hq, T, D] bf16
   float *lse;             // [B, Hq, T] or null
-  int B, Hq, Hkv, T, GT, R, RB, Pmax, tiles, chunks;
+  int B, Hq, Hkv, T, GT, R, RB, Smax, Pmax, tiles, chunks, grid;
 };
 
 // Prefix length attended, and the keys of a chunk of it (whole tiles).
@@ -294,8 +291,10 @@ __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRow
 
 // Grid: kv heads x 32-row groups of their B * GT rows x slabs of dims. A lane has a row, a warp eight dims and every
 // SPLIT-th of the row's parts (its runs', then the prefix's); the warps of a row's dims meet in shared memory. What bounds it
-// is the chain of loads (the plan, a part's m and l and sums, one batch after another), so a batch is asked for at once,
-// and where rows are few their parts are spread over SPLIT warps.
+// is its chain of loads (a part's m and l and sums, one batch after another) behind the launch, so a batch is asked for at
+// once, where rows are few their parts are spread over SPLIT warps, and each warp finds its rows' parts before it waits
+// for the launch that leaves them. (It may read the lengths then: every CTA of that launch, which lets this one start, has
+// waited for the launches before it.)
 constexpr int kJoinThreads = 256;
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a) {
@@ -306,12 +305,22 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
   const int warp = threadIdx.x / 32, part0 = warp / COLS, d8 = slab * COLS + warp % COLS;
   const int row = min(group * 32 + (int)(threadIdx.x & 31), rows - 1);  // (the last group's lanes repeat a row)
   const int b = row / a.GT, gt = row % a.GT, rb = gt / a.R, r = gt % a.R;
-  griddep_wait();
-  griddep_launch_dependents();
   // the runs that hold steps of this row's group, and the chunks of the prefix
-  const int U = a.Hkv * a.RB, first = __ldcg(a.plan + b), next = __ldcg(a.plan + b + 1), S = __ldcg(a.plan + a.B + 1);
-  const int P = prefix_keys(__ldcg(a.prefix_len), a.Pmax);
-  const int units = (next - first) / U, base = first + (kvh * a.RB + rb) * units;
+  const int P = prefix_keys(__ldcg(a.prefix_len), a.Pmax), U = a.Hkv * a.RB, lane = threadIdx.x & 31;
+  int first = 0, units = 0, W = 0;  // units before the row's sequence, of one of its groups, and in all
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int mine = b0 + lane < a.B ? run_units(min(max(__ldcg(a.seq_lens + b0 + lane), 0), a.Smax)) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int own = __shfl_sync(0xffffffffu, mine, b & 31), upto = __shfl_sync(0xffffffffu, incl, b & 31);
+    if (b >= b0 && b < b0 + 32) first = W + (upto - own) * U, units = own;
+    W += __shfl_sync(0xffffffffu, incl, 31) * U;
+  }
+  const int S = run_length(W, a.grid), base = first + (kvh * a.RB + rb) * units;
   const int r0 = (base + kRunGroupUnits) / S, n_runs = units > 0 ? (base + units - 1) / S + 1 - r0 : 0;
   const int C = prefix_chunk(P, a.chunks), n = n_runs + (P > 0 ? (P + C - 1) / C : 0);
   const int BF = run_block_floats(a.R, D);
@@ -320,6 +329,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
   float M = -INFINITY, L = 0.f, A[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) A[k] = 0.f;
+  griddep_wait();
+  griddep_launch_dependents();
   for (int p0 = part0; p0 < n; p0 += SPLIT * kBatch) {
     float m[kBatch], l[kBatch];
     float4 x[kBatch], y[kBatch];

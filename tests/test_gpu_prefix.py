@@ -1,5 +1,7 @@
 """Attention over a shared prefix and each sequence's own keys on the GPU against plain masked attention over
 both in 64 bits (masked_ref), the bounds of parity.py. Rows that no token sees hold NaN in every test."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -283,6 +285,30 @@ def test_two_streams_at_once(td):
             outs[i].append(td.td_decode_attn_prefix(*args[i], stream=s, return_lse=True))
     torch.cuda.synchronize()
     for p, got in zip(ps, outs):
+        for out, lse in got:
+            assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+        p.check(got[0][0].cpu()[:, :, None], got[0][1].cpu()[:, :, None])
+
+
+def test_two_threads_on_one_stream(td):
+    """Calls of two threads share a stream and, without one of their own, a workspace."""
+    ps = [Problem(128, 8, 2, 1, 1500, 1400 + i, 200, [200, 50 + i, 0], seed=40 + i) for i in range(2)]
+    args = [p.args() for p in ps]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [[], []]
+
+    def work(i):
+        for _ in range(200):
+            outs[i].append(td.td_decode_attn_prefix(*args[i], stream=stream, return_lse=True))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for p, got in zip(ps, outs):
+        assert len(got) == 200
         for out, lse in got:
             assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
         p.check(got[0][0].cpu()[:, :, None], got[0][1].cpu()[:, :, None])
