@@ -4,8 +4,9 @@ Argument marshalling only: shapes and pointers are read off torch tensors, outpu
 workspace are allocated with torch when the caller does not pass them, and every step of
 the computation runs in the CUDA library. Nothing falls back to another implementation:
 without the built library, or with tensors off the GPU, the calls raise. The calls on the
-block-scaled cache (f8) do this marshalling in a native module (csrc/td_torch.cpp), the
-others here through ctypes.
+block-scaled cache (f8), the normed append and the attention over windows and shared
+prefixes do this marshalling in a native module (csrc/td_torch.cpp), the others here
+through ctypes.
 
 For CUDA-graph capture pass ``out`` (and ``lse``), ``workspace`` and ``stream`` explicitly
 and warm the call up once outside the capture.

@@ -1,5 +1,5 @@
 """Builds the CUDA library libtd.so in-tree (``decode_attention_split_gb300/_build``), and the
-native binding of the f8 calls, _td_torch.so (g++, torch's headers), beside it.
+native binding of the calls that have one, _td_torch.so (g++, torch's headers), beside it.
 
 One ``-gencode arch=compute_103a,code=sm_103a`` target (GB300), translation units compiled
 in parallel, the CUDA runtime linked statically with its symbols kept private. ptxas

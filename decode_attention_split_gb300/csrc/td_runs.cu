@@ -7,18 +7,27 @@ namespace td {
 
 namespace {
 
+constexpr int kSms = 152;
+
 template <int D, int SPLIT>
 cudaError_t launch_join_split(const JoinArgs &a, cudaStream_t stream) {
-  const long long groups = ((long long)a.B * a.GT + 31) / 32 * a.Hkv;
-  return launch_pdl(join_kernel<D, SPLIT>, dim3((unsigned)(groups * (D / 64) * SPLIT)), dim3(kJoinThreads), 0, stream, a);
+  constexpr int threads = join_threads(SPLIT), slabs = D / 8 / (threads / 32 / SPLIT);
+  constexpr int most = 200 * 1024, own = 40 * threads + 1024;  // a CTA's static shared memory and what the system takes
+  const long long ctas = ((long long)a.B * a.GT + 31) / 32 * a.Hkv * slabs;
+  const long long per = (ctas + kSms - 1) / kSms;  // an SM's share
+  const int spread = per <= kJoinSmThreads / threads ? std::min((int)(224 * 1024 / per) - own, most) / 1024 * 1024 : 0;
+  static OptIn opt_in;
+  const cudaError_t e = opt_in(reinterpret_cast<const void *>(&join_kernel<D, SPLIT>), most);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(join_kernel<D, SPLIT>, dim3((unsigned)ctas), dim3(threads), spread, stream, a);
 }
 
 template <int D>
 cudaError_t launch_join_d(const JoinArgs &a, cudaStream_t stream) {
-  // one batch of loads a thread for the prefix's chunks and a few runs, while the CTAs fit the GPU at once
-  const long long ctas = ((long long)a.B * a.GT + 31) / 32 * a.Hkv * (D / 64);  // without a split
+  // one batch of loads a thread for the prefix's chunks and a few runs, while all rows' threads fit the GPU at once
+  const long long threads = ((long long)a.B * a.GT + 31) / 32 * a.Hkv * (D / 8) * 32;  // without a split
   int split = 1;
-  while (split < 8 && split * 4 < a.chunks + 3 && ctas * split * 2 <= 2 * 152) split *= 2;
+  while (split < 8 && split * kJoinBatch < a.chunks + 3 && threads * split * 2 <= kJoinSmThreads * kSms) split *= 2;
   return split == 1   ? launch_join_split<D, 1>(a, stream)
          : split == 2 ? launch_join_split<D, 2>(a, stream)
          : split == 4 ? launch_join_split<D, 4>(a, stream)

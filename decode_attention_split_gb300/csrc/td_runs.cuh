@@ -295,11 +295,19 @@ __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRow
 // once, where rows are few their parts are spread over SPLIT warps, and each warp finds its rows' parts before it waits
 // for the launch that leaves them. (It may read the lengths then: every CTA of that launch, which lets this one start, has
 // waited for the launches before it.)
-constexpr int kJoinThreads = 256;
+//
+// CTAs of four warps (SPLIT's, if those are more), so that a few hundred of them spread evenly, and no more registers than
+// let an SM hold 768 threads. The launch asks for so much shared memory that no SM takes more than its share of the CTAs:
+// they start while SMs fall free one by one, and would share the first while others stay idle. Measured in us (calls
+// over 8k keys of 8 heads): 16 sequences of six tokens 26.5 -> 25.0, 48 single tokens 26.5 -> 25.5, 64 unchanged at 28.0;
+// 16 of a 360M-style layer behind 1000 keys 10.6 -> 8.7. Without the spreading, 3 CTAs of 256 threads an SM lose 1 us.
+constexpr int kJoinBatch = 4;         // parts of a row in flight at once (6 and 8: no gain, 2.5 us lost at 25 parts)
+constexpr int kJoinSmThreads = 768;
+__host__ __device__ constexpr int join_threads(int split) { return split > 4 ? 32 * split : 128; }
 template <int D, int SPLIT>
-__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a) {
-  constexpr int COLS = kJoinThreads / 32 / SPLIT;  // warps side by side, eight dims each
-  constexpr int SLABS = D / 8 / COLS, kBatch = 4;  // kBatch parts' loads in flight at once
+__global__ void __launch_bounds__(join_threads(SPLIT), kJoinSmThreads / join_threads(SPLIT)) join_kernel(const JoinArgs a) {
+  constexpr int THREADS = join_threads(SPLIT), COLS = THREADS / 32 / SPLIT;  // warps side by side, eight dims each
+  constexpr int SLABS = D / 8 / COLS;
   const int rows = a.B * a.GT, groups = (rows + 31) / 32;
   const int slab = blockIdx.x % SLABS, group = blockIdx.x / SLABS % groups, kvh = blockIdx.x / SLABS / groups;
   const int warp = threadIdx.x / 32, part0 = warp / COLS, d8 = slab * COLS + warp % COLS;
@@ -331,12 +339,12 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
   for (int k = 0; k < 8; ++k) A[k] = 0.f;
   griddep_wait();
   griddep_launch_dependents();
-  for (int p0 = part0; p0 < n; p0 += SPLIT * kBatch) {
-    float m[kBatch], l[kBatch];
-    float4 x[kBatch], y[kBatch];
+  for (int p0 = part0; p0 < n; p0 += SPLIT * kJoinBatch) {
+    float m[kJoinBatch], l[kJoinBatch];
+    float4 x[kJoinBatch], y[kJoinBatch];
     float Mn = M;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kJoinBatch; ++i) {
       const int p = p0 + i * SPLIT;
       const bool own = p < n_runs;
       const float *pb = own ? runs + (long long)p * BF : chunks + (long long)(p - n_runs) * prefix_block_floats(D);
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
       }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
+    for (int i = 0; i < kJoinBatch; ++i)
       if (l[i] != 0.f) Mn = fmaxf(Mn, m[i]);  // a part without keys (l = 0) counts nothing; a NaN stays one
     const float ref = Mn == -INFINITY ? 0.f : Mn;
     const float alpha = exp2f(M - ref);
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
 #pragma unroll
     for (int k = 0; k < 8; ++k) A[k] *= alpha;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < kJoinBatch; ++i) {
       if (l[i] != 0.f) {
         const float f = exp2f(m[i] - ref);
         L = fmaf(l[i], f, L);
@@ -369,8 +377,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const JoinArgs a)
     M = Mn;
   }
   if constexpr (SPLIT > 1) {
-    __shared__ float s_acc[8][kJoinThreads];
-    __shared__ float2 s_ml[kJoinThreads];
+    __shared__ float s_acc[8][THREADS];
+    __shared__ float2 s_ml[THREADS];
 #pragma unroll
     for (int k = 0; k < 8; ++k) s_acc[k][threadIdx.x] = A[k];
     s_ml[threadIdx.x] = make_float2(M, L);
