@@ -141,20 +141,32 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
   const uint32_t tmem = s_taddr;
   const uint32_t tS = tmem, tP = tmem + kPxKeys, tO = tmem + C::O_COL, tQ = tmem + C::Q_COL;
 
-  griddep_wait();
-  griddep_launch_dependents();
   bool ok = true;
-
   if (warp >= kPxRunWarp && warp < kPxRunWarp + kRunWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(px_run_regs(NT)));
     int *s_len = reinterpret_cast<int *>(smem + C::LEN_OFF);  // [B]
     int *s_prefix = s_len + p.B;                              // [B + 1]
-    const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp;
-    const int S = plan_runs<1>(p, rt, s_len, s_prefix, s_red);
-    run_warp<D, NT, 2>(p, a.own.kmap, a.own.vmap, s_len, s_prefix, S, blockIdx.x * kRunWarps + rw,
-                       smem + C::RUN_OFF + rw * C::Run::RING, run_bars[rw]);
+    const int rt = tid - 32 * kPxRunWarp, rw = warp - kPxRunWarp, run = blockIdx.x * kRunWarps + rw;
+    // planned on the lengths as they read ahead of the wait for the launches before, and again should they read otherwise
+    // after it
+    RunCursor start;
+    int u1;
+#pragma unroll 1
+    for (bool waited = false;;) {
+      const int S = plan_runs<1>(p, rt, s_len, s_prefix, s_red);
+      start = run_start(p, s_len, s_prefix, S, run, u1);
+      if (waited) break;
+      griddep_wait();
+      griddep_launch_dependents();
+      waited = true;
+      if (lens_stand<1>(p, rt, s_len)) break;
+    }
+    run_warp<D, NT, 2>(p, a.own.kmap, a.own.vmap, s_len, start, u1, run, smem + C::RUN_OFF + rw * C::Run::RING,
+                       run_bars[rw]);
   } else if (warp >= kPxMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxIssueRegs));
+    griddep_wait();
+    griddep_launch_dependents();
     const int P = prefix_keys(*a.prefix_len, a.Pmax);
     const int items = P > 0 ? a.tiles * p.Hkv * a.chunks : 0;
     if (warp == kPxMmaWarp) {
@@ -239,6 +251,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     }
   } else {
     if constexpr (px_soft_regs(NT) > 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(px_soft_regs(NT)));
+    griddep_wait();
+    griddep_launch_dependents();
     // thread `row` of half `half` (0: warps 0 .. 3) takes keys 64 half .. of the row's 128 a tile, and dims D / 2 half ..
     // of its output; the two of a row meet in s_max
     const int quarter = warp & 3, half = warp >> 2, row = tid & (kPxRows - 1);

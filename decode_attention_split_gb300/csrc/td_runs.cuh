@@ -60,9 +60,8 @@ __device__ __forceinline__ int run_length(int W, int grid) {
   return max((W + runs - 1) / runs, kRunLeast);
 }
 
-// Fills s_len (attended lengths) and s_prefix (units before each sequence; their total at [B]); returns the units of a
-// run; reports the status bits that the lengths raise. By kRunThreads threads, `tid` theirs, meeting at barrier BAR. Ends
-// with a barrier.
+// Fills s_len (attended lengths, as they read now) and s_prefix (units before each sequence; their total at [B]); returns
+// the units of a run. By kRunThreads threads, `tid` theirs, meeting at barrier BAR. Ends with a barrier.
 template <int BAR>
 __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefix, int *s_red) {
   const int lane = tid & 31, warp = tid >> 5;
@@ -70,11 +69,10 @@ __device__ int plan_runs(const SplitParams &p, int tid, int *s_len, int *s_prefi
   int seg = 0;
   uint32_t bits = 0;
   for (int b = b0; b < min(b0 + per, p.B); ++b) {
-    const int L = attended_len(p, p.seq_lens[b], bits);
+    const int L = attended_len(p, ld_relaxed(p.seq_lens + b), bits);
     s_len[b] = L;
     seg += run_units(L) * U;
   }
-  if (blockIdx.x == 0) report(p.status, bits);
   int incl = seg;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -118,28 +116,26 @@ __device__ __forceinline__ void next_group(const SplitParams &p, const int *s_le
   if (c.base + kRunGroupUnits < u1) c.e = min(run_steps(s_len[c.b]), u1 - c.base - kRunGroupUnits);
 }
 
-// A warp's ring: its barriers, by one thread.
-template <int STAGES>
-__device__ __forceinline__ void init_ring(uint64_t *bars) {
-#pragma unroll
-  for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
-  fence_mbar_init();
+// Whether the lengths still read as a plan_runs of these threads found them; reports the status bits that they raise.
+template <int BAR>
+__device__ __forceinline__ bool lens_stand(const SplitParams &p, int tid, const int *s_len) {
+  const int per = (p.B + kRunThreads - 1) / kRunThreads, b0 = tid * per;
+  uint32_t bits = 0, same = 1;
+  for (int b = b0; b < min(b0 + per, p.B); ++b) same &= attended_len(p, ld_relaxed(p.seq_lens + b), bits) == s_len[b];
+  if (blockIdx.x == 0) report(p.status, bits);
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.u32 p, %0, 0;\nbarrier.cta.red.and.pred q, %1, %2, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "+r"(same)
+      : "n"(BAR), "n"(kRunThreads)
+      : "memory");
+  return same != 0;
 }
 
-// One warp's run: number `run`, S units long. The warp's ring (1024-byte aligned) and its barriers (initialised, one arrival).
-template <int D, int NT, int ST>
-__device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
-                                         const int *s_len, const int *s_prefix, int S, int run, unsigned char *ring_p,
-                                         uint64_t *bars) {
-  using C = RunCfg<D, ST>;
-  constexpr int KSD = D / 16, NL = 2 * NT;
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const uint32_t ring = smem_u32(ring_p);
-  const int W = s_prefix[p.B], GT = p.G * p.T;
-  const int u0 = (int)min((long long)run * S, (long long)W), u1 = (int)min((long long)u0 + S, (long long)W);
-  const uint64_t policy = l2_evict_first_policy();
-
-  // the first group of the run
+// Where run number `run`, S units long, starts; u1 receives where it ends.
+__device__ __forceinline__ RunCursor run_start(const SplitParams &p, const int *s_len, const int *s_prefix, int S, int run,
+                                               int &u1) {
+  const int W = s_prefix[p.B], u0 = (int)min((long long)run * S, (long long)W);
+  u1 = (int)min((long long)u0 + S, (long long)W);
   RunCursor c{};
   if (u0 < u1) {
     int lo = 0, hi = p.B - 1;  // the last sequence whose units start at or before u0 (those without keys have none)
@@ -155,6 +151,30 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
     c.e = max(min(n, u1 - c.base) - kRunGroupUnits, 0);
     if (c.s >= c.e) next_group(p, s_len, u1, c);
   }
+  return c;
+}
+
+// A warp's ring: its barriers, by one thread.
+template <int STAGES>
+__device__ __forceinline__ void init_ring(uint64_t *bars) {
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&bars[i]), 1);
+  fence_mbar_init();
+}
+
+// One warp's run, number `run`, from c on to unit u1. The warp's ring (1024-byte aligned) and its barriers (initialised, one
+// arrival).
+template <int D, int NT, int ST>
+__device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                         const int *s_len, RunCursor c, int u1, int run, unsigned char *ring_p,
+                                         uint64_t *bars) {
+  using C = RunCfg<D, ST>;
+  constexpr int KSD = D / 16, NL = 2 * NT;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const uint32_t ring = smem_u32(ring_p);
+  const int GT = p.G * p.T;
+  const uint64_t policy = l2_evict_first_policy();
+
   RunCursor ahead = c;  // the next step to be fetched
   int fetched = 0, used = 0;
   auto fetch = [&]() {  // lane 0 of a warp whose ring has room
