@@ -12,9 +12,14 @@
 // The first is bound by the tensor cores and exponentials where many sequences share the prefix and by memory where few
 // do, the second by memory: in one CTA they fill each other's waits, and neither waits for the other's launch.
 // join_kernel then joins a row's parts and rounds once.
+// Measured (GPU time in a graph, 128 dims): 64 sequences of up to 512 own keys behind 8192 (32 + 8 heads) 27.7 us (102 MB,
+// 3.7 TB/s; either part alone 21 us), 16 of up to 1000 behind 32003 (24 + 8 heads) 33.2 us (168 MB, 5.1 TB/s), six tokens of
+// 16 sequences behind 4321 24.5 us (48 MB). The fixed part, 7 us with 4 short sequences, is two launches, the lengths and
+// queries, one tile, the partial blocks and the join.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "td_internal.h"
 #include "td_runs.cuh"
