@@ -360,12 +360,14 @@ __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], 
 // of them (three tiles: the 17 to 24 rows of kTileN24). A thread holds keys gid and gid + 8 of
 // rows 8 nt + 2 tig (+1) of each tile, i.e. 2 NT rows, reduced over the 8 lanes that share a tig.
 // o[nt][dt] holds O^T of dims 16 dt + gid (+8) and rows 8 nt + 2 tig (+1); the row limits, maxima
-// and sums are indexed 2 nt + e. TK: rows of the tiles at kt and vt.
+// and sums are indexed 2 nt + e. TK: rows of the tiles at kt and vt. edge: whether some row's window starts behind key0; the
+// steps inside every row's window (most of a long one's) then skip its tests (six tokens of 8 sequences through a window of
+// 2048: 26.0 -> 25.0 us).
 template <int D, int WIN = 0, int NT = 3, int TK = 64>
 __device__ __forceinline__ void warp_keys16_nt(const uint32_t (&qb)[NT][D / 16][2], uint32_t kt, uint32_t vt, int kr,
                                                int key0, const int (&lim)[2 * NT], float qscale,
                                                float (&o)[NT][D / 16][4], float (&m_run)[2 * NT], float (&l_run)[2 * NT],
-                                               int window = 0, int sinks = 0) {
+                                               int window = 0, int sinks = 0, bool edge = false) {
   constexpr int KSD = D / 16;
   const int lane = threadIdx.x & 31, gid = lane >> 2;
   // independent accumulators, one per n tile
@@ -384,15 +386,23 @@ __device__ __forceinline__ void warp_keys16_nt(const uint32_t (&qb)[NT][D / 16][
   // 8 nt + 2 tig + (i & 1)
   float alpha[2 * NT];
 #pragma unroll
+  for (int i = 0; i < 4 * NT; ++i) {
+    const int key = key0 + gid + 8 * ((i >> 1) & 1);
+    float &s = sc[i >> 2][i & 3];
+    s = key < lim[2 * (i >> 2) + (i & 1)] ? s * qscale : -INFINITY;
+  }
+  if (WIN != 0 && edge) {
+#pragma unroll
+    for (int i = 0; i < 4 * NT; ++i) {
+      const int key = key0 + gid + 8 * ((i >> 1) & 1);
+      if (!sees<WIN>(key, lim[2 * (i >> 2) + (i & 1)], window, sinks)) sc[i >> 2][i & 3] = -INFINITY;
+    }
+  }
+#pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int ri = 2 * nt + e;
-#pragma unroll
-      for (int hk = 0; hk < 2; ++hk) {
-        const int key = key0 + gid + 8 * hk;
-        sc[nt][2 * hk + e] = sees<WIN>(key, lim[ri], window, sinks) ? sc[nt][2 * hk + e] * qscale : -INFINITY;
-      }
       float mx = fmaxf(sc[nt][e], sc[nt][2 + e]);
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -631,7 +641,8 @@ __device__ bool stream_chunk(const typename MmaArgsOf<WIN>::type &a, unsigned ch
     const int key0 = j0 + kr;
     if (key0 < c1) {
       if constexpr (TILE == kTileN24)
-        warp_keys16_nt<D, WIN>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks);
+        warp_keys16_nt<D, WIN>(qa, kt, vt, kr, key0, lim, p.qscale, o, m_run, l_run, p.window, p.sinks,
+                               WIN != 0 && key0 < L - span.shift - p.window);
       else if constexpr (TILE == kTileN8)
         warp_keys16_n8<D, WIN>(qa[0], kt, vt, kr, key0, lim, p.qscale, o[0], m_run, l_run, p.window, p.sinks);
       else
