@@ -318,9 +318,9 @@ __host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRow
 //
 // CTAs of four warps (SPLIT's, if those are more), so that a few hundred of them spread evenly, and no more registers than
 // let an SM hold 768 threads. The launch asks for so much shared memory that no SM takes more than its share of the CTAs:
-// they start while SMs fall free one by one, and would share the first while others stay idle. Measured in us (calls
-// over 8k keys of 8 heads): 16 sequences of six tokens 26.5 -> 25.0, 48 single tokens 26.5 -> 25.5, 64 unchanged at 28.0;
-// 16 of a 360M-style layer behind 1000 keys 10.6 -> 8.7. Without the spreading, 3 CTAs of 256 threads an SM lose 1 us.
+// they start while SMs fall free one by one, and would share the first while others stay idle. Measured in us of a
+// call: six tokens of 16 sequences behind 4321 keys 26.5 -> 25.0, single tokens of 48 behind 8192 26.5 -> 25.5, of 64
+// unchanged at 28.0, of 16 behind 1000 (5 heads of 64) 10.6 -> 8.7. Without the spreading, 3 CTAs of 256 threads an SM lose 1 us.
 constexpr int kJoinBatch = 4;         // parts of a row in flight at once (6 and 8: no gain, 2.5 us lost at 25 parts)
 constexpr int kJoinSmThreads = 768;
 __host__ __device__ constexpr int join_threads(int split) { return split > 4 ? 32 * split : 128; }
