@@ -106,12 +106,14 @@ __device__ __forceinline__ void norm_turn(float eps, const Turn<VE> &turn, const
 // What becomes of a row: normed and turned, or copied.
 enum : int { kQuery = 0, kKey = 1, kValue = 2 };
 
-// Heads [first, h1) of one kind. Every lane of a warp makes every round (the exchanges are warp-wide); a row that is not
-// there is not loaded or stored.
+// Heads [first, h1) of one kind; of a kind that this CTA has no heads of nothing is read (without queries there are no
+// weights of theirs). Every lane of a warp makes every round (the exchanges are warp-wide); a row that is not there is not
+// loaded or stored.
 template <typename E, int D, int KIND, int VE>
 __device__ __forceinline__ void norm_heads(const NormAppend &p, const Turn<VE> &turn, int b, int t, int L, bool there,
                                            bool fits, int v, int first, int h1) {
   constexpr int NH = D / 2 / VE, NV = 2 * NH;
+  if (first >= h1) return;  // the same in every thread of the CTA
   const int H = KIND == kQuery ? p.Hq : p.Hkv;
   const uint4 *src = static_cast<const uint4 *>(KIND == kQuery ? p.q : KIND == kKey ? p.k_new : p.v_new) +
                      ((long long)b * H * p.T + t) * NV + v;

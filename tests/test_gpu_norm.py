@@ -142,6 +142,24 @@ def test_without_queries(td, T):
     p.check(q=False)
 
 
+@pytest.mark.parametrize("dtype,D,T,Hkv,A", [("bf16", 128, 32, 1, 0), ("bf16", 64, 300, 8, 0), ("f32", 128, 16, 3, 3),
+                                              ("f32", 64, 1000, 2, 1), ("bf16", 128, 2000, 8, 0)])
+def test_chunks_without_queries(td, dtype, D, T, Hkv, A):
+    """No queries and no weights of theirs, in chunks of one head a CTA and of several: the keys and values are those of
+    the call with queries, bit for bit."""
+    p = Problem(dtype, D, T, T + 9, [0, 9, 10], Hkv=Hkv, A=A, rows=50 if A else None, seed=T)
+    g = p.call(td, q=False)
+    assert g["q_out"] is None
+    kc, vc, lens = g["kc"].clone(), g["vc"].clone(), g["lens"].clone()
+    assert int(g["st"]) == td.DEV_APPEND_OVERFLOW
+    if T < 500:
+        p.check(q=False)
+    g = p.call(td)
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(g["kc"].view(bits), kc.view(bits)) and torch.equal(g["vc"].view(bits), vc.view(bits))
+    assert torch.equal(g["lens"], lens)
+
+
 @pytest.mark.parametrize("dtype,T", [("bf16", 1), ("f32", 19)])
 def test_queries_in_place(td, dtype, T):
     p = Problem(dtype, 64, T, 64, [4, 11])
