@@ -84,9 +84,8 @@ struct PxItem {
 };
 __device__ __forceinline__ PxItem px_item(const PxArgs &a, int item, int P) {
   PxItem w;
-  w.tile = item % a.tiles;  // the tiles of rows that read one chunk are neighbours
-  w.kvh = item / a.tiles % a.own.p.Hkv;
-  w.chunk = item / a.tiles / a.own.p.Hkv;
+  const PrefixItem at = prefix_item(item, a.tiles, a.own.p.Hkv);
+  w.tile = at.tile, w.kvh = at.kvh, w.chunk = at.chunk;
   w.rows = min(kPxRows, a.own.p.B * a.GT - w.tile * kPxRows);
   const int S = prefix_chunk(P, a.chunks);
   w.c0 = min(w.chunk * S, P);
@@ -403,7 +402,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
       if (!ok) continue;
       tc_fence_after();
       const PxItem here = px_item(a, item, P);  // (again: its numbers are not held over the tiles)
-      float *blk = a.part + (((long long)here.kvh * a.tiles + here.tile) * a.chunks + here.chunk) * prefix_block_floats(D);
+      float *blk = a.part + prefix_block(here.kvh, here.tile, here.chunk, a.tiles, a.chunks) * prefix_block_floats(D);
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         float o[32];
@@ -434,6 +433,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         mbar_wait_bounded(smem_u32(&bar_v[g % C::NST]), (uint32_t)(g / C::NST) & 1u);
       report(p.status, TD_DEV_WAIT_TIMEOUT);
     }
+    if (tid < kPxRows)
+      drop_items<D>(a.part, prefix_keys(*a.prefix_len, a.Pmax), a.tiles, p.Hkv, a.chunks, blockIdx.x, gridDim.x, tid, kPxRows);
   }
   tc_fence_before();
   __syncthreads();

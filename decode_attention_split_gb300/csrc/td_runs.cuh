@@ -43,10 +43,18 @@ __host__ __device__ constexpr int run_block_floats(int R, int D) { return (R * (
 // Units of a group of `keys` keys: its steps, and as many units as starting and finishing it costs, ahead of its own.
 constexpr int kRunGroupUnits = 1;
 constexpr int kRunLeast = 2;  // units of the shortest run
-__device__ __forceinline__ int run_steps(int keys) { return (keys + kRunKeys - 1) / kRunKeys; }
-__device__ __forceinline__ int run_units(int keys) { return keys > 0 ? run_steps(keys) + kRunGroupUnits : 0; }
+__host__ __device__ __forceinline__ int run_steps(int keys) { return (keys + kRunKeys - 1) / kRunKeys; }
+__host__ __device__ __forceinline__ int run_units(int keys) { return keys > 0 ? run_steps(keys) + kRunGroupUnits : 0; }
 // The block of group g's keys in run r: runs and groups advance together, so every (group, run) that meet have their own.
-__device__ __forceinline__ long long run_block(long long g, int r) { return g + r; }
+__host__ __device__ __forceinline__ long long run_block(long long g, int r) { return g + r; }
+// The runs, S units long, that hold steps of a group of `units` units behind `base` others: n of them from the first on.
+struct RunSpan {
+  int first, n;
+};
+__host__ __device__ __forceinline__ RunSpan runs_of(int base, int units, int S) {
+  const int first = (base + kRunGroupUnits) / S;
+  return {first, units > 0 ? (base + units - 1) / S + 1 - first : 0};
+}
 
 // A barrier of the kRunThreads threads that take runs.
 template <int ID>
@@ -55,7 +63,7 @@ __device__ __forceinline__ void run_barrier() {
 }
 
 // Units of a run, of W in all dealt to `grid` CTAs.
-__device__ __forceinline__ int run_length(int W, int grid) {
+__host__ __device__ __forceinline__ int run_length(int W, int grid) {
   const int runs = grid * kRunWarps;
   return max((W + runs - 1) / runs, kRunLeast);
 }
@@ -103,7 +111,7 @@ struct RunCursor {
 };
 
 // Moves the cursor to the next group with steps in units [.., u1); e = s where none is left.
-__device__ __forceinline__ void next_group(const SplitParams &p, const int *s_len, int u1, RunCursor &c) {
+__host__ __device__ __forceinline__ void next_group(const SplitParams &p, const int *s_len, int u1, RunCursor &c) {
   const int U = p.Hkv * p.RB;
   c.s = c.e = 0;
   c.base += run_units(s_len[c.b]);
@@ -132,8 +140,8 @@ __device__ __forceinline__ bool lens_stand(const SplitParams &p, int tid, const 
 }
 
 // Where run number `run`, S units long, starts; u1 receives where it ends.
-__device__ __forceinline__ RunCursor run_start(const SplitParams &p, const int *s_len, const int *s_prefix, int S, int run,
-                                               int &u1) {
+__host__ __device__ __forceinline__ RunCursor run_start(const SplitParams &p, const int *s_len, const int *s_prefix, int S,
+                                                        int run, int &u1) {
   const int W = s_prefix[p.B], u0 = (int)min((long long)run * S, (long long)W);
   u1 = (int)min((long long)u0 + S, (long long)W);
   RunCursor c{};
@@ -152,6 +160,17 @@ __device__ __forceinline__ RunCursor run_start(const SplitParams &p, const int *
     if (c.s >= c.e) next_group(p, s_len, u1, c);
   }
   return c;
+}
+
+// A run that gave up in the group at c: the groups behind it, which the join reads as well, are left without keys (l = 0;
+// their blocks may hold an earlier call's). By threads lane, lane + lanes, ...
+template <int D>
+__host__ __device__ inline void drop_rest_of_run(const SplitParams &p, const int *s_len, RunCursor c, int u1, int run, int lane,
+                                                 int lanes) {
+  for (next_group(p, s_len, u1, c); c.s < c.e; next_group(p, s_len, u1, c)) {
+    float *blk = p.ws_part + run_block((long long)c.b * p.Hkv * p.RB + c.ug, run) * run_block_floats(p.R, D);
+    for (int r = lane; r < p.R; r += lanes) blk[p.R * (D + 1) + r] = 0.f;
+  }
 }
 
 // A warp's ring: its barriers, by one thread.
@@ -287,6 +306,45 @@ __device__ __forceinline__ void run_warp(const SplitParams &p, const CUtensorMap
         mbar_wait_bounded(smem_u32(&bars[i % C::STAGES]), (uint32_t)(i / C::STAGES) & 1u);
       report(p.status, TD_DEV_WAIT_TIMEOUT);
     }
+    drop_rest_of_run<D>(p, s_len, c, u1, run, lane, 32);
+  }
+}
+
+// Prefix length attended, and the keys of a chunk of it (whole tiles).
+constexpr int kPrefixKeys = 128;
+__host__ __device__ __forceinline__ int prefix_keys(int raw, int Pmax) { return raw < 0 ? 0 : raw > Pmax ? Pmax : raw; }
+__host__ __device__ __forceinline__ int prefix_chunk(int P, int chunks) {
+  return ((P + kPrefixKeys - 1) / kPrefixKeys + chunks - 1) / chunks * kPrefixKeys;
+}
+// Chunks of it that hold keys.
+__host__ __device__ __forceinline__ int prefix_parts(int P, int chunks) {
+  const int C = prefix_chunk(P, chunks);
+  return P > 0 ? (P + C - 1) / C : 0;
+}
+constexpr int kPrefixRows = 128;  // query rows of a tile over the prefix
+__host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRows * (D + 2); }
+// The block of chunk `chunk` for tile `tile` of kv head kvh.
+__host__ __device__ __forceinline__ long long prefix_block(int kvh, int tile, int chunk, int tiles, int chunks) {
+  return ((long long)kvh * tiles + tile) * chunks + chunk;
+}
+
+// Work over the prefix, item by item: a tile of a kv head's rows over a chunk. The tiles that read one chunk are neighbours.
+struct PrefixItem {
+  int tile, kvh, chunk;
+};
+__host__ __device__ __forceinline__ PrefixItem prefix_item(int item, int tiles, int Hkv) {
+  return {item % tiles, item / tiles % Hkv, item / tiles / Hkv};
+}
+// A CTA that gave up: the blocks of its items (`item` and every grid-th behind it), which the join reads as well, are left
+// without keys (they may hold an earlier call's). By threads lane, lane + lanes, ...
+template <int D>
+__host__ __device__ inline void drop_items(float *part, int P, int tiles, int Hkv, int chunks, int item, int grid, int lane,
+                                           int lanes) {
+  const int items = tiles * Hkv * prefix_parts(P, chunks);
+  for (; item < items; item += grid) {
+    const PrefixItem w = prefix_item(item, tiles, Hkv);
+    float *blk = part + prefix_block(w.kvh, w.tile, w.chunk, tiles, chunks) * prefix_block_floats(D);
+    for (int r = lane; r < kPrefixRows; r += lanes) blk[kPrefixRows * (D + 1) + r] = 0.f;
   }
 }
 
@@ -301,13 +359,6 @@ struct JoinArgs {
   float *lse;             // [B, Hq, T] or null
   int B, Hq, Hkv, T, GT, R, RB, Smax, Pmax, tiles, chunks, grid;
 };
-
-// Prefix length attended, and the keys of a chunk of it (whole tiles).
-constexpr int kPrefixKeys = 128;
-__device__ __forceinline__ int prefix_keys(int raw, int Pmax) { return raw < 0 ? 0 : raw > Pmax ? Pmax : raw; }
-__device__ __forceinline__ int prefix_chunk(int P, int chunks) { return ((P + kPrefixKeys - 1) / kPrefixKeys + chunks - 1) / chunks * kPrefixKeys; }
-constexpr int kPrefixRows = 128;  // query rows of a tile over the prefix
-__host__ __device__ constexpr int prefix_block_floats(int D) { return kPrefixRows * (D + 2); }
 
 // Grid: kv heads x 32-row groups of their B * GT rows x slabs of dims. A lane has a row, a warp eight dims and every
 // SPLIT-th of the row's parts (its runs', then the prefix's); the warps of a row's dims meet in shared memory. What bounds it
@@ -349,11 +400,11 @@ __global__ void __launch_bounds__(join_threads(SPLIT), kJoinSmThreads / join_thr
     W += __shfl_sync(0xffffffffu, incl, 31) * U;
   }
   const int S = run_length(W, a.grid), base = first + (kvh * a.RB + rb) * units;
-  const int r0 = (base + kRunGroupUnits) / S, n_runs = units > 0 ? (base + units - 1) / S + 1 - r0 : 0;
-  const int C = prefix_chunk(P, a.chunks), n = n_runs + (P > 0 ? (P + C - 1) / C : 0);
+  const RunSpan span = runs_of(base, units, S);
+  const int n_runs = span.n, n = n_runs + prefix_parts(P, a.chunks);
   const int BF = run_block_floats(a.R, D);
-  const float *runs = a.runs + run_block(((long long)b * a.Hkv + kvh) * a.RB + rb, r0) * BF;
-  const float *chunks = a.prefix + ((long long)kvh * a.tiles + row / kPrefixRows) * a.chunks * prefix_block_floats(D);
+  const float *runs = a.runs + run_block(((long long)b * a.Hkv + kvh) * a.RB + rb, span.first) * BF;
+  const float *chunks = a.prefix + prefix_block(kvh, row / kPrefixRows, 0, a.tiles, a.chunks) * prefix_block_floats(D);
   float M = -INFINITY, L = 0.f, A[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) A[k] = 0.f;

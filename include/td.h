@@ -429,7 +429,8 @@ td_status td_prefill_attn_window(const void *q, const void *k_cache, const void 
  * rows without any key give out = 0 and lse = -inf, and L_b < T sets TD_DEV_VERIFY_SHORT as in td_verify_attn. bf16,
  * D 64 or 128. The parts over the prefix and over the own keys are kept in fp32 and joined; out is rounded once.
  * Two launches. The workspace is td_prefix_workspace_bytes', 256-byte aligned; it need not be zeroed and keeps nothing
- * from one call to the next, so any calls on one stream may share it.
+ * from one call to the next, so any calls on one stream may share it: where a bounded wait gives up (TD_DEV_WAIT_TIMEOUT,
+ * output invalid), the keys of the work it stopped are left out, and nothing of an earlier call comes in their place.
  */
 size_t td_prefix_workspace_bytes(int B, int Hq, int Hkv, int Pmax, int Smax, int D, int q_len);
 td_status td_decode_attn_prefix(const void *q, const void *k_prefix, const void *v_prefix, const int32_t *prefix_len,
