@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
     const int row = tid, t = t0 + row;
     const bool row_valid = t < a.T;
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const float inv = (ok && l > 0.f) ? 1.f / l : 0.f;
+    const float inv = (ok && l != 0.f) ? 1.f / l : 0.f;
     __nv_bfloat16 *orow =
         static_cast<__nv_bfloat16 *>(a.out) + (((size_t)b * a.Hq + hq) * a.T + (row_valid ? t : 0)) * D;
 #pragma unroll
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       }
     }
     if (row_valid && a.lse != nullptr)
-      a.lse[((size_t)b * a.Hq + hq) * a.T + t] = (ok && l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      a.lse[((size_t)b * a.Hq + hq) * a.T + t] = (ok && l != 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
   }
   tc_fence_before();
   __syncthreads();

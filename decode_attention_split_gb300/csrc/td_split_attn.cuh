@@ -325,6 +325,9 @@ __host__ __device__ constexpr int merge_fixed_floats() {
   return ROWS * D + 4 * ROWS + ROWS * 64;
 }
 
+// A part without keys has l = 0 and counts nothing in a merge. Every other one counts, so the tests are for l != 0: a row that
+// saw a NaN key has a NaN sum, which has to reach its result.
+
 // Output row (flattened [B, Hq*T]) of local row r of row block rb of kv head kvh.
 __device__ __forceinline__ long long out_row_of(const SplitParams &p, int b, int kvh, int rb, int r) {
   const int gr = rb * p.R + r;
@@ -380,7 +383,7 @@ __device__ void merge_group(const SplitParams &p, float *smem_f, int smem_floats
       for (int k = 0; k < 2; ++k) {
         const int c = lane + 32 * k;
         lv[k] = c < nb ? stage[c * BF + r * RF + D + 1] : 0.f;
-        mv[k] = lv[k] > 0.f ? stage[c * BF + r * RF + D] : -INFINITY;
+        mv[k] = lv[k] != 0.f ? stage[c * BF + r * RF + D] : -INFINITY;
       }
       float bm = fmaxf(mv[0], mv[1]);
 #pragma unroll
@@ -391,7 +394,7 @@ __device__ void merge_group(const SplitParams &p, float *smem_f, int smem_floats
       float ls = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float f = lv[k] > 0.f ? exp2f(mv[k] - base) : 0.f;
+        const float f = lv[k] != 0.f ? exp2f(mv[k] - base) : 0.f;
         if (lane + 32 * k < nb) fac[r * kFB + lane + 32 * k] = f;
         ls = fmaf(lv[k], f, ls);
       }
@@ -403,9 +406,9 @@ __device__ void merge_group(const SplitParams &p, float *smem_f, int smem_floats
         st[r] = Mn;
         st[ROWS + r] = Ls;
         st[2 * ROWS + r] = alpha;
-        st[3 * ROWS + r] = Ls > 0.f ? 1.f / Ls : 0.f;
+        st[3 * ROWS + r] = Ls != 0.f ? 1.f / Ls : 0.f;
         if (last && p.lse != nullptr)
-          p.lse[out_row_of(p, b, kvh, rb, r)] = Ls > 0.f ? (Mn + log2f(Ls)) * kLn2 : -INFINITY;
+          p.lse[out_row_of(p, b, kvh, rb, r)] = Ls != 0.f ? (Mn + log2f(Ls)) * kLn2 : -INFINITY;
       }
     }
     __syncthreads();
@@ -527,14 +530,14 @@ __device__ void merge_rows_direct(const SplitParams &p, float *sm, int b, int kv
       float bm = M;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (lv[k] > 0.f) bm = fmaxf(bm, mv[k]);
+        if (lv[k] != 0.f) bm = fmaxf(bm, mv[k]);
       const float base = bm == -INFINITY ? 0.f : bm;
       const float alpha = exp2f(M - base);  // 0 while nothing is folded in (M = -inf)
       Ls *= alpha;
       A.x *= alpha, A.y *= alpha, A.z *= alpha, A.w *= alpha;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (lv[k] > 0.f) {
+        if (lv[k] != 0.f) {
           const float f = exp2f(mv[k] - base);
           Ls = fmaf(lv[k], f, Ls);
           A.x = fmaf(v[k].x, f, A.x), A.y = fmaf(v[k].y, f, A.y), A.z = fmaf(v[k].z, f, A.z),
@@ -556,12 +559,12 @@ __device__ void merge_rows_direct(const SplitParams &p, float *sm, int b, int kv
   if (cg == 0) {
     float Mt = -INFINITY;
     for (int j = 0; j < CG; ++j)
-      if (sL[j * nr + rr] > 0.f) Mt = fmaxf(Mt, sM[j * nr + rr]);
+      if (sL[j * nr + rr] != 0.f) Mt = fmaxf(Mt, sM[j * nr + rr]);
     float Lt = 0.f;
     float4 At = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < CG; ++j) {
       const float lj = sL[j * nr + rr];
-      if (lj > 0.f) {
+      if (lj != 0.f) {
         const float f = exp2f(sM[j * nr + rr] - Mt);
         const float4 x = *reinterpret_cast<const float4 *>(sA + (j * nr + rr) * D + 4 * col);
         Lt = fmaf(lj, f, Lt);
@@ -569,13 +572,13 @@ __device__ void merge_rows_direct(const SplitParams &p, float *sm, int b, int kv
       }
     }
     const long long orow = out_row_of(p, b, kvh, rb, s0 + rr);
-    const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+    const float inv = Lt != 0.f ? 1.f / Lt : 0.f;
     E *o = static_cast<E *>(p.out) + orow * D + 4 * col;
     store_elem<E>(o + 0, At.x * inv);
     store_elem<E>(o + 1, At.y * inv);
     store_elem<E>(o + 2, At.z * inv);
     store_elem<E>(o + 3, At.w * inv);
-    if (col == 0 && p.lse != nullptr) p.lse[orow] = Lt > 0.f ? (Mt + log2f(Lt)) * kLn2 : -INFINITY;
+    if (col == 0 && p.lse != nullptr) p.lse[orow] = Lt != 0.f ? (Mt + log2f(Lt)) * kLn2 : -INFINITY;
   }
   __syncthreads();  // the scratch may be reused
 }
@@ -668,18 +671,18 @@ __device__ void finish_item(const SplitParams &p, float *smem_f, int smem_floats
     }
     if (single) {
       const long long row = out_row_of(p, b, kvh, rb, r);
-      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
       E *o = static_cast<E *>(p.out) + row * D + d;
       store_elem<E>(o + 0, A.x * inv);
       store_elem<E>(o + 1, A.y * inv);
       store_elem<E>(o + 2, A.z * inv);
       store_elem<E>(o + 3, A.w * inv);
-      if (d == 0 && p.lse != nullptr) p.lse[row] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
+      if (d == 0 && p.lse != nullptr) p.lse[row] = Ls != 0.f ? (M + log2f(Ls)) * kLn2 : -INFINITY;
     } else {
       float *dst = blk + r * RF;
       *reinterpret_cast<float4 *>(dst + d) = A;
       if (d == 0) {
-        dst[D] = Ls > 0.f ? M : -INFINITY;
+        dst[D] = Ls != 0.f ? M : -INFINITY;
         dst[D + 1] = Ls;
       }
     }

@@ -95,20 +95,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s < CS) {
           const float *pb = map_to_rank(static_cast<const float *>(blk), (uint32_t)s);
           ls[s] = pb[R * D + R + r];
-          ms[s] = ls[s] > 0.f ? pb[R * D + r] : -INFINITY;
+          ms[s] = ls[s] != 0.f ? pb[R * D + r] : -INFINITY;
         }
         M = fmaxf(M, ms[s]);
       }
       float Ls = 0.f;
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) {
-        ms[s] = ls[s] > 0.f ? expf(ms[s] - M) : 0.f;
+        ms[s] = ls[s] != 0.f ? expf(ms[s] - M) : 0.f;
         Ls = fmaf(ls[s], ms[s], Ls);
       }
-      const float inv = Ls > 0.f ? 1.f / Ls : 0.f;
+      const float inv = Ls != 0.f ? 1.f / Ls : 0.f;
 #pragma unroll
       for (int s = 0; s < kMaxCluster; ++s) s_w[s][r] = ms[s] * inv;
-      s_lse[r] = Ls > 0.f ? M + logf(Ls) : -INFINITY;
+      s_lse[r] = Ls != 0.f ? M + logf(Ls) : -INFINITY;
     }
     __syncthreads();
     for (int idx = tid; idx < nv * D4; idx += kThreads) {

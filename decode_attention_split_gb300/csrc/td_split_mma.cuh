@@ -921,7 +921,7 @@ __device__ void combine_block(const float *combine, float *dst, int R, int nv) {
     }
     *reinterpret_cast<float4 *>(dst + r * D + d) = A;
     if (d == 0) {
-      dst[R * D + r] = Ls > 0.f ? M * kLn2 : -INFINITY;
+      dst[R * D + r] = Ls != 0.f ? M * kLn2 : -INFINITY;
       dst[R * D + R + r] = Ls;
     }
   }

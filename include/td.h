@@ -159,6 +159,8 @@ td_status td_kv_append(td_dtype dtype, const void *k_new, const void *v_new, voi
  * split: keys per chunk; 0 lets the library size chunks from the device lengths and the
  * GPU's SM count. The grid depends only on the arguments (never on the lengths), and
  * chunks past a sequence's length do no work. D must be 64 or 128.
+ * A row that sees a NaN key gives NaN in out and lse, here and in the other attention calls over rows, windows,
+ * prefixes and int8 codes.
  */
 td_status td_decode_attn(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
                          const int32_t *seq_lens, int B, int Hq, int Hkv, int Smax, int D, float scale, int split,
