@@ -47,9 +47,6 @@ constexpr int kPfSoftmaxWarps = 4;                         // one query row per 
 constexpr int kPfMmaWarp = kPfSoftmaxWarps;                  // issues the tensor-core products
 constexpr int kPfLoadWarp = kPfSoftmaxWarps + 1;             // issues the TMA copies
 constexpr int kPfThreads = 32 * (kPfSoftmaxWarps + 2);
-// The window's kernel rescales later: sums in floating point lose nothing against a reference 2^32 below the maximum
-// (a value of up to 2^75 over 2^20 keys stays finite), and every move waits for a product.
-constexpr float kWindowGap = 32.f;
 constexpr int kPfRows = 128;   // query rows per CTA
 constexpr int kQRegion = kPfRows * 128;  // bytes of one swizzled [128 rows][64 bf16] region
 constexpr int kKRegion = kPfKeys * 128;  // bytes of one swizzled [64 rows][64 bf16] region
@@ -326,11 +323,12 @@ __global__ void __launch_bounds__(kPfThreads, 2) prefill_kernel(const __grid_con
       // independent chains of three-input steps
       const float ext = qscale >= 0.f ? row_extreme<false>(sv) : row_extreme<true>(sv);
       const float mx = full || seen.any() ? ext * qscale : -INFINITY;
-      const bool move = mx > m_ref + (WIN ? kWindowGap : kRescaleGap) || (m_ref == -INFINITY && mx > -INFINITY);
-      const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
+      const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
+      const float m_new = WIN ? mx + kRescaleLead : mx;  // (the 8000-token prompt: 127.2 -> 120.1 us)
+      const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - m_new) : 1.f;
       if (move) {
         l *= alpha;
-        m_ref = mx;
+        m_ref = m_new;
       }
       // a warp rescales its rows of O when any of them must, once the previous P V product
       // is complete (TMEM loads and stores are warp-wide). The product of kt-2 may still be

@@ -38,11 +38,9 @@ constexpr int kPxRows = kPrefixRows;           // query rows per tile
 constexpr int kPxKeys = kPrefixKeys;           // keys per tile
 constexpr int kPxHalf = kPxKeys / 2;           // of them, one softmax thread's
 constexpr int kPxKRegion = kPxKeys * 128;      // bytes of one swizzled [128 keys][64 bf16] region
-// Base-2 rise of a row's maximum before the reference moves. Probabilities and sums are floating point, so a reference 2^32
-// below the maximum costs no bits (fp32 holds 2^32 times a value of up to 2^75 over 2^20 keys), while every move makes a
-// warp wait for the product before it and rescale its rows of O: with a rise of 8 and now and then a key of four times the
-// others' strength, some row of the 128 moved in nearly every tile (490 cycles of a tile's 3600, 175 with 32).
-constexpr float kPxGap = 32.f;
+// The reference of a row moves to kRescaleLead above its maximum: without that lead, and now and then a key of four times
+// the others' strength, some row of the 128 moved in nearly every tile (490 cycles of a tile's 3600, 175 with it; a call of 16
+// sequences behind 32003 keys 34.1 -> 33.8 us, six tokens of 16 behind 4321 25.2 -> 24.9).
 // Registers a thread: launched with 128 (65536 / 512), then split between softmax, run, and product and copy warps. A run
 // over row blocks of more than 16 rows needs more than 200, and the softmax warps then keep to what they have.
 __host__ __device__ constexpr int px_soft_regs(int NT) { return NT <= 2 ? 136 : 128; }
@@ -348,13 +346,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         meet();
         mx = fmaxf(mx, s_max[b0][half ^ 1][row]);
         if (!ok) continue;
-        // the reference maximum moves only when the row's rises more than kPxGap above it (a row's first scores
+        // the reference moves only when the row's maximum rises more than kRescaleGap above it (a row's first scores
         // always move it); only then are O and l rescaled, once the previous product is complete
-        const bool move = mx > m_ref + kPxGap || (m_ref == -INFINITY && mx > -INFINITY);
-        const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - mx) : 1.f;
+        const bool move = mx > m_ref + kRescaleGap || (m_ref == -INFINITY && mx > -INFINITY);
+        const float m_new = mx + kRescaleLead;
+        const float alpha = (move && m_ref != -INFINITY) ? exp2_approx(m_ref - m_new) : 1.f;
         if (move) {
           l *= alpha;
-          m_ref = mx;
+          m_ref = m_new;
         }
         if (k > g0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           // (the product of k - 2 may still run: S of k is issued before the product of k - 1. Each of the two barriers'

@@ -11,7 +11,12 @@
 namespace td {
 
 constexpr int kPfKeys = 64;         // keys per tile
-constexpr float kRescaleGap = 8.f;  // base-2 rise of a row maximum before m moves
+constexpr float kRescaleGap = 8.f;  // base-2 rise of a row maximum above its reference before that moves
+// Where moves are dear (each makes a warp wait for the product before it and rescale its rows of O), the reference moves to
+// this far above the maximum, and so again only after a rise of kRescaleLead + kRescaleGap. The largest weight then lies
+// between 2^-24 and 2^8: no higher than with a reference that moves to the maximum, so that sums stay finite under the
+// same values, and at the low end fp32 and bf16, which float, lose nothing but of values below 2^-102.
+constexpr float kRescaleLead = 24.f;
 
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
   asm volatile(

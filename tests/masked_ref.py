@@ -60,3 +60,32 @@ def window_mask(lens, T, S, window, sinks):
     p = L - T + np.arange(T)[None, :, None]
     j = np.arange(S)[None, None, :]
     return (j <= p) & ((j > p - window) | (j < sinks))
+
+
+def rising_keys(q, S, rise, g, period=None):
+    """Keys [Hkv, S, D] over which the scores q k D^-1/2 of every row of q [Hkv, T, D] rise by `rise` (base 2) from the first
+    to the last (with a period: and again from each multiple of it on), give or take a hundredth and the rows' noise; q is
+    made alike within a head: a direction and a little of its own per row."""
+    Hkv, T, D = q.shape
+    u = torch.randn(Hkv, 1, D, generator=g)
+    u *= D ** 0.5 / u.norm(dim=-1, keepdim=True)
+    q.copy_(u + 0.002 * q)
+    n = S if period is None else period
+    ramp = (torch.arange(S) % n / (n - 1.0) * rise / 1.4426950408889634)[None, :, None]
+    return u * ramp * D ** -0.5 + 0.002 * torch.randn(Hkv, S, D, generator=g)
+
+
+def check_large(out, lse, q, k, v, see, scale, what=""):
+    """check() for values far from 1: the value bound alone, whose terms all follow the values' size, and lse."""
+    G = q.shape[1] // k.shape[1]
+    for b in range(q.shape[0]):
+        for h in range(k.shape[1]):
+            heads = slice(h * G, (h + 1) * G)
+            ref, rl, stats = attend(q[b, heads].double().numpy(), k[b, h].double().numpy(), v[b, h].double().numpy(),
+                                    see[b], scale)
+            got = out[b, heads].double().numpy()
+            name = f"{what} sequence {b} kv head {h}"
+            assert np.isfinite(got).all(), f"{name}: not finite"
+            err, bound = np.abs(got - ref), value_bound(ref, stats)
+            assert np.all(err <= bound), f"{name}: worst err/bound {float((err / bound).max()):.2f}"
+            assert_lse_close(lse[b, heads], rl, what=name)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from decode_attention_split_gb300.workloads import rope_tables
-from masked_ref import check
+from masked_ref import check, check_large, rising_keys
 
 pytestmark = pytest.mark.gpu
 
@@ -126,6 +126,27 @@ def test_a_large_maximum_late_in_the_prefix(td):
     ramp = torch.linspace(0, 6, 640)[None, :, None]
     p.kp = (p.q[0, 0, 0].float() * ramp + 0.1 * p.kp.float()).to(torch.bfloat16)
     p.check(*p.run(td))
+
+
+@pytest.mark.parametrize("rise", [7, 9, 31, 34, 90, 200])
+@pytest.mark.parametrize("size", [0, 100])
+@pytest.mark.parametrize("D,G,T", [(128, 4, 1), (64, 3, 6)])
+def test_rising_scores(td, D, G, T, size, rise):
+    """The same, by less and by more than the reference is let to lag, under values of magnitude 2^size."""
+    period = 384                    # three tiles of keys, and with two kv heads and 76 periods so is a chunk
+    B, Hkv, P, S = 2, 2, 76 * period, 100
+    g = torch.Generator().manual_seed(rise)
+    p = Problem(D, Hkv * G, Hkv, T, P, P, S, [S, S - 7], seed=8)
+    q = torch.randn(Hkv, B * G * T, D, generator=g)
+    p.kp = rising_keys(q, P, rise, g, period).bfloat16()
+    p.q = q.view(Hkv, B, G, T, D).transpose(0, 1).reshape(B, Hkv * G, T, D).bfloat16()
+    p.k, p.v = p.k.nan_to_num(), (p.v.nan_to_num().float() * 2.0 ** size).bfloat16()
+    p.vp = (p.vp.float() * 2.0 ** size).bfloat16()
+    out, lse = p.run(td)
+    both = [torch.cat([a[None].expand(B, -1, -1, -1), x], dim=2) for a, x in ((p.kp, p.k), (p.vp, p.v))]
+    check_large(out, lse, p.q, *both, p.see, p.scale)
+    plain = td.td_verify_attn(p.q.cuda(), *(x.cuda() for x in both), torch.tensor([P + S] * B, dtype=torch.int32).cuda())
+    assert plain.isfinite().all()
 
 
 @pytest.mark.parametrize("T", [1, 5])

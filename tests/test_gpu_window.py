@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from decode_attention_split_gb300.workloads import rope_tables
-from masked_ref import check, window_mask
+from masked_ref import check, check_large, rising_keys, window_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -137,6 +137,25 @@ def test_prompt_matches_verify(td):
     b, lb = p.run(td)
     p.check(a, la)
     p.check(b, lb)
+
+
+@pytest.mark.parametrize("rise", [7, 9, 31, 34, 90, 200])
+@pytest.mark.parametrize("size", [0, 100])
+@pytest.mark.parametrize("D,window,sinks", [(128, 1000, 0), (64, 300, 4), (128, 257, 70)])
+def test_prompt_of_rising_scores(td, D, window, sinks, size, rise):
+    """A row's maximum moves many tiles after its first, by less and by more than its reference is let to lag (its sums are
+    rescaled then), under values of magnitude 2^size: as far as the plain call stays finite, so does this one."""
+    B, Hkv, G, T, S = 1, 2, 2, 200, 700
+    g = torch.Generator().manual_seed(rise)
+    p = Problem("bf16", D, Hkv * G, Hkv, T, S, [S], window, sinks, seed=17)
+    q = torch.randn(Hkv, G * T, D, generator=g)
+    p.k = rising_keys(q, S, rise, g)[None].bfloat16()
+    p.q = q.view(B, Hkv * G, T, D).bfloat16()
+    p.v = (torch.randn(B, Hkv, S, D, generator=g) * 2.0 ** size).bfloat16()
+    out, lse = p.run(td, prompt=True)
+    check_large(out, lse, p.q, p.k, p.v, p.see, p.scale)
+    plain = td.td_prefill_attn(p.q.cuda(), p.k.cuda(), p.v.cuda(), torch.tensor([S], dtype=torch.int32).cuda())
+    assert plain.isfinite().all()
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05])
