@@ -44,6 +44,32 @@ def test_prefill_repeats_itself(td, D, T, L, window):
     assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
 
 
+@pytest.mark.parametrize("D,T,L,window", [(128, 700, 2047, 1500), (64, 257, 1999, 1200)])
+def test_windowed_prefill_of_rising_scores_repeats_itself(td, D, T, L, window):
+    """Scores that rise by more than the reference is let to lag (2^32) from one tile of keys to the next but one: rows are
+    rescaled in most tiles."""
+    g = torch.Generator(device="cuda").manual_seed(D + T)
+    q = torch.ones(2, 8, T, D, device="cuda")
+    q += 0.1 * torch.randn(2, 8, T, D, generator=g, device="cuda")
+    ramp = 20 * torch.arange(L, device="cuda") / 64 * 0.6931 * D ** -0.5          # base 2: 20 a tile of 64 keys
+    k = (ramp[None, None, :, None] + torch.randn(2, 4, L, D, generator=g, device="cuda")).bfloat16()
+    q, v = q.bfloat16(), torch.randn(2, 4, L, D, generator=g, device="cuda").bfloat16()
+    lens = torch.tensor([L, L - 5], dtype=torch.int32, device="cuda")
+    a = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    b = torch.empty_like(a)
+    want = td.td_prefill_attn_window(q, k, v, lens, window, 4, return_lse=True)
+    torch.cuda.synchronize()
+    assert want[0].isfinite().all()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(60):
+        with torch.cuda.stream(side):
+            b.copy_(a)
+        got.append(td.td_prefill_attn_window(q, k, v, lens, window, 4, return_lse=True))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[0]) and torch.equal(y, want[1]) for x, y in got)
+
+
 @pytest.mark.parametrize("D,G,T,B,P", [(128, 4, 6, 33, 2048), (64, 3, 6, 33, 1999), (128, 4, 1, 70, 2047), (64, 8, 1, 40, 300)])
 def test_prefix_attention_repeats_itself(td, D, G, T, B, P):
     Hkv, S = 3, 300
