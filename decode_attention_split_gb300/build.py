@@ -90,7 +90,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     """Compile every .cu under csrc/ and link libtd.so, then the native binding; returns libtd.so's path.
 
     Where the binding does not build (no Python or torch headers) libtd.so is in place when this
-    raises: every call but the f8 ones from Python works with it."""
+    raises: the C calls work with it, and from Python those that api.py binds through ctypes."""
     if not force and not extra_flags and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)

@@ -27,8 +27,9 @@
 // the same m, need no correction. Query tiles are launched longest first (causal rows late in
 // the prompt see the most keys). Every wait is bounded; a timeout sets TD_DEV_WAIT_TIMEOUT,
 // and the CTA waits (bounded) for its copies and products in flight before it frees TMEM.
-// Measured, 24 + 8 heads of 128: prompts of 4096 and 8192 tokens 90.1 and 303 us (1144, 1361 TFLOP/s); 8000 tokens through a
-// window of 1024 with 4 sinks 119.9 us (799 TFLOP/s of visible work, 1000 with the masked parts of its tiles).
+// Measured, 24 + 8 heads of 128: a prompt of 4096 tokens 90 us (1144 TFLOP/s), of 8192 302 to 313 (1364 to 1319; 320 in long
+// runs, the power cap); 8000 tokens through a window of 1024 with 4 sinks 120.1 us (798 TFLOP/s of visible work, 1000
+// with the masked parts of its tiles).
 #include <cudaTypedefs.h>
 #include <math.h>
 

@@ -362,7 +362,7 @@ __device__ __forceinline__ void warp_keys16_n8(const uint32_t (&qb)[D / 16][2], 
 // o[nt][dt] holds O^T of dims 16 dt + gid (+8) and rows 8 nt + 2 tig (+1); the row limits, maxima
 // and sums are indexed 2 nt + e. TK: rows of the tiles at kt and vt. edge: whether some row's window starts behind key0; the
 // steps inside every row's window (most of a long one's) then skip its tests (six tokens of 8 sequences through a window of
-// 2048: 26.0 -> 25.0 us).
+// 2048, in a graph: 26.0 -> 25.0 us).
 template <int D, int WIN = 0, int NT = 3, int TK = 64>
 __device__ __forceinline__ void warp_keys16_nt(const uint32_t (&qb)[NT][D / 16][2], uint32_t kt, uint32_t vt, int kr,
                                                int key0, const int (&lim)[2 * NT], float qscale,

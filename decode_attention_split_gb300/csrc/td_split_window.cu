@@ -6,9 +6,11 @@
 // workspace follow the window's size, not the context's. What they add per score is two comparisons, and per sequence
 // the copies of the stages that hold sinks in boxes of 16 rows, since the rows of one stage then lie apart.
 // Measured: one token at 32k keys through a window of 4096 (24 + 8 heads of 128) 9.3 us, latency (16.8 MB, 2.5 us); 32 ragged
-// sequences of up to 8k keys through one of 1024 (32 + 8 heads) 27.2 us (127 MB, 4.7 TB/s), instruction fetch and the chunks'
-// starts and ends; six tokens of 8 sequences through 2048 23.6 us (69 MB, 2.9 TB/s), the 24-row step; fp32, 4 sequences
-// through 250 (4 + 2 heads of 64) 6.3 us, latency. A launch of equal runs with a join after it took 27 us for the first.
+// sequences of up to 8k keys through one of 1024 (32 + 8 heads) 27.0 us (127 MB, 4.7 TB/s), instruction fetch and places
+// left empty (one chunk a group: 256 on 304 places); six tokens of 8 sequences through 2048 23.8 us (69 MB, 2.9 TB/s), the
+// 24-row step; fp32, 4 sequences through 250 (4 + 2 heads of 64) 6.3 us, latency. (Calls among others on a stream; replayed
+// from a graph they take up to 5 % longer.) A launch of equal runs with a join after it took 27 us for the first, and 28.5
+// instead of 37.5 for 200 sequences through a window of 128.
 #include <mutex>
 
 #include "td_internal.h"

@@ -406,9 +406,9 @@ td_status td_prefill_attn(const void *q, const void *k_cache, const void *v_cach
  * tile of 128 sees and another does not must be finite for both (a weight of 0 times NaN is NaN), as in the plain calls.
  * td_decode_attn_window and td_verify_attn_window: TD_F32 and TD_BF16; split is 0 or a multiple of 16; a workspace of
  * td_window_workspace_bytes, used as td_decode_workspace_bytes says, for one dtype and (B, Hq, Hkv, Smax, D, q_len,
- * window, sinks, split). Their cost follows the window, not the context: per sequence and kv head they read
- * min(L, sinks + window + T - 1) rows. td_prefill_attn_window: bf16, whole tiles of 64 keys; of values below 2^-102 in
- * magnitude it may lose bits.
+ * window, sinks, split). Their cost follows the window, not the context: per sequence, kv head and block of query rows (at
+ * most 24 in bf16, 8 or, with D 128, 4 in fp32) they read about min(L, sinks + window + T - 1) rows, in whole stages.
+ * td_prefill_attn_window: bf16, whole tiles of 64 keys; of values below 2^-102 in magnitude it may lose bits.
  */
 size_t td_window_workspace_bytes(int B, int Hq, int Hkv, int Smax, int D, int q_len, int window, int sinks, int split);
 td_status td_decode_attn_window(td_dtype dtype, const void *q, const void *k_cache, const void *v_cache,
@@ -432,6 +432,7 @@ td_status td_prefill_attn_window(const void *q, const void *k_cache, const void 
  * rows without any key give out = 0 and lse = -inf, and L_b < T sets TD_DEV_VERIFY_SHORT as in td_verify_attn. bf16,
  * D 64 or 128. The parts over the prefix and over the own keys are kept in fp32 and joined; out is rounded once. Of prefix
  * values below 2^-102 in magnitude bits may be lost.
+ * An own value that one token of a chunk sees and another does not must be finite for both, as in td_verify_attn.
  * Two launches. The workspace is td_prefix_workspace_bytes', 256-byte aligned; it need not be zeroed and keeps nothing
  * from one call to the next, so any calls on one stream may share it: where a bounded wait gives up (TD_DEV_WAIT_TIMEOUT,
  * output invalid), the keys of the work it stopped are left out, and nothing of an earlier call comes in their place.
